@@ -73,6 +73,10 @@ typedef enum { SPEC_BF16 = 0, SPEC_F32 = 1 } spec_dtype;
 #define SPEC_STATUS_NONFINITE 4        /* a row that was read holds NaN or +inf, or is all -inf   */
 #define SPEC_STATUS_INTERNAL 5         /* a bounded internal wait gave up, or the workspace was not
                                           zeroed before its first use; results are not valid   */
+#define SPEC_STATUS_BAD_LENGTH 2       /* cache calls: offsets or lengths of the request that are
+                                          negative, decreasing or past the arrays or its pages  */
+#define SPEC_STATUS_BAD_PAGE 6         /* cache calls: a page the request needs is not in
+                                          [0, num_pages)                                        */
 /* Rows read: target and draft rows 0..k_b-1 (target only for greedy requests); the
  * target row k_b only when every draft is accepted (it holds the bonus token).
  * A request with a non-zero status has out_accepted[b] = 0, every token -1 and
@@ -351,6 +355,109 @@ int spec_schedule_verify_len_stale(const float *conf_stale, const float *conf, c
  */
 int spec_schedule_threshold(const float *conf, const int32_t *max_len, int B, int Kmax, float threshold,
                             int32_t *out_len, void *cuda_stream);
+
+/*
+ * The 8-bit paged key/value cache of the target model, and the verify step's
+ * attention over it.  The target scores a request's anchor and drafts in one pass
+ * whose memory traffic is this cache: spec_kv_append writes the new tokens' keys and
+ * values, spec_cache_attention reads everything cached, and after the verify call
+ * the cached length advances by accepted + 1 -- the rejected drafts' slots are simply
+ * written again by the next append.
+ *
+ * Entries are e4m3 codes (sign, 4 exponent bits with bias 7, 3 mantissa bits; largest
+ * 448; 0x7F and 0xFF are NaN) with one scale for each page and head, keys and values
+ * apart: the entry stands for code * scale.  A page holds page_size consecutive tokens
+ * of one request; page_table[b * ld_table + i] is the page of tokens i * page_size ..
+ * of request b (ld_table pages a request at most).
+ *
+ *  k, v          codes; entry (page, head, slot, d) at byte page * page_stride +
+ *                head * head_stride + slot * token_stride + d, in both arrays;
+ *                16-byte aligned, strides positive multiples of 16
+ *  k_scale, v_scale  [num_pages, num_heads] positive float
+ *  page_size     16, 32, 64 or 128
+ *  head_dim      a multiple of 16, at most SPEC_KV_MAX_HEAD_DIM
+ * Two requests may share pages that neither call writes.
+ */
+#define SPEC_KV_MAX_HEAD_DIM 256
+typedef struct spec_kv_cache {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t page_stride, head_stride, token_stride;
+    int32_t num_pages, page_size, num_heads, head_dim;
+} spec_kv_cache;
+
+/*
+ * Quantise new keys and values into the cache.  Request b's n_b = cu_new[b+1] -
+ * cu_new[b] new tokens are rows cu_new[b] .. of k and v and go to positions
+ * cached_len[b] .. cached_len[b] + n_b - 1; what the cache held at or after
+ * cached_len[b] is forgotten.  For each page and head that receives tokens:
+ *   want = the smallest power of two 2^e with max |new entry| <= 448 * 2^e, e clamped
+ *          to [-100, 119] (finite entries only; -100 when all are zero);
+ *   scale = want if the page keeps no token (its first position is at or after
+ *           cached_len[b]), else max(want, its present scale);
+ *   kept codes become e4m3(code * old / scale) when the scale grew;
+ *   new codes are e4m3(entry / scale), round to nearest even, saturating at 448;
+ *   a NaN or infinite entry becomes a NaN code.
+ * Division by a power of two is exact, so each new entry is rounded once, and a kept
+ * code loses bits only where it falls below the new scale's normal range.
+ *
+ *  k, v        rows of num_heads * head_dim elements of type dtype, ld_k / ld_v
+ *              elements apart (slices of a fused projection's output are fine)
+ *  n_tokens    rows of k and v; max_new a bound on every n_b
+ *  out_status  [B]: 0, SPEC_STATUS_BAD_LENGTH (nothing of the request is written) or
+ *              SPEC_STATUS_BAD_PAGE (its other pages are written)
+ * One kernel, no workspace.  Appending the same tokens at the same length again leaves
+ * the cache as it is.
+ */
+int spec_kv_append(const spec_kv_cache *cache, const void *k, const void *v, int dtype, int64_t ld_k, int64_t ld_v,
+                   int n_tokens, int B, const int32_t *cu_new, int max_new, const int32_t *cached_len,
+                   const int32_t *page_table, int ld_table, int32_t *out_status, void *cuda_stream);
+
+/*
+ * Read ranges of the cache back.  Request b's positions first[b] .. first[b] + n_b - 1
+ * (first NULL: 0), n_b = cu_out[b+1] - cu_out[b], become rows cu_out[b] .. of out_k and
+ * out_v, each [n_out, num_heads, head_dim] of type dtype, holding code * scale (exact
+ * in bf16 for scales that spec_kv_append wrote).  Rows outside every request's range
+ * are not written.
+ *  out_status  [B]: 0, SPEC_STATUS_BAD_LENGTH (none of its rows is written) or
+ *              SPEC_STATUS_BAD_PAGE (the rows of that page are NaN)
+ * out_k and out_v 16-byte aligned.  One kernel, no workspace.
+ */
+int spec_kv_gather(const spec_kv_cache *cache, int B, const int32_t *cu_out, int n_out, const int32_t *first,
+                   const int32_t *page_table, int ld_table, void *out_k, void *out_v, int dtype,
+                   int32_t *out_status, void *cuda_stream);
+
+/*
+ * Attention of the new tokens' queries over the cache.  Request b's n_b = cu_query[b+1]
+ * - cu_query[b] queries are the last n_b of its seq_len[b] cached tokens: query t is at
+ * position P = seq_len[b] - n_b + t and sees the positions j <= P with
+ *   window == 0,  or  j > P - window,  or  j < sinks.
+ * For query head h, with key head h / (num_query_heads / num_heads):
+ *   s_j = scale * (q . k_j),  out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j).
+ * A query that sees nothing (P < 0) gets out = 0 and lse = -inf.  Pages that no query
+ * of the request sees are not read and may hold any id.  A NaN code among a query's
+ * visible entries makes its results NaN; unseen entries never matter.
+ *
+ *  q           rows of num_query_heads * head_dim elements of type dtype, ld_q
+ *              elements apart
+ *  n_tokens    rows of q, out and out_lse; max_query a bound on every n_b
+ *  scale       positive and finite; window >= 0; sinks >= 0 (unused when window == 0)
+ *  out         [n_tokens, num_query_heads, head_dim] of type dtype
+ *  out_lse     [n_tokens, num_query_heads] float, or NULL
+ *  out_status  [B]: 0, SPEC_STATUS_BAD_LENGTH, SPEC_STATUS_BAD_PAGE or
+ *              SPEC_STATUS_INTERNAL; rows of a failed request are unspecified
+ *  ws          at least spec_cache_attention_workspace_size bytes, 256-byte aligned,
+ *              ZERO-FILLED before its first use; every call leaves its counters zero,
+ *              so one workspace serves any number of calls in stream order.  The
+ *              workspace of another entry point must not be passed here.
+ * Results are the same from call to call: partial sums are joined in a fixed order.
+ */
+size_t spec_cache_attention_workspace_size(int num_query_heads, int num_heads, int head_dim, int dtype);
+int spec_cache_attention(const spec_kv_cache *cache, const void *q, int dtype, int64_t ld_q, int num_query_heads,
+                         int n_tokens, int B, const int32_t *cu_query, int max_query, const int32_t *seq_len,
+                         const int32_t *page_table, int ld_table, float scale, int window, int sinks, void *out,
+                         float *out_lse, int32_t *out_status, void *ws, size_t ws_bytes, void *cuda_stream);
 
 /* Short text for a return code. */
 const char *spec_error_string(int err);

@@ -13,8 +13,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libspecverify.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
-SOURCES = ["verify.cu", "schedule.cu", "markov.cu"]
-HEADERS = ["spec_common.cuh"]
+SOURCES = ["verify.cu", "schedule.cu", "markov.cu", "kv_cache.cu", "cache_attention.cu"]
+HEADERS = ["spec_common.cuh", "kv_common.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -6,11 +6,13 @@ manages tensors.  Shapes follow the C ABI: target logits [B, K+1, V], draft logi
 """
 from __future__ import annotations
 
+import contextlib
 import threading
 
 import torch
 
 from . import binding
+from .binding import KVCache
 
 _ws_lock = threading.Lock()
 _ws_cache: dict[int, torch.Tensor] = {}
@@ -223,3 +225,82 @@ def verify_sample_host(target_h, draft_h, tokens_h, temperature_h, seed: int, st
     host = {k: v.to("cpu", non_blocking=True) for k, v in out.items() if v is not None}
     torch.cuda.current_stream().synchronize()
     return host
+
+
+# ------------------------------------------------------------------ 8-bit paged key/value cache
+_attn_ws: dict[tuple[int, int], torch.Tensor] = {}
+
+
+def _on(stream):
+    """Run what the call itself allocates and converts on the stream it launches on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _attention_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int) -> torch.Tensor:
+    """One zero-filled workspace for each device and stream: calls on one stream run in
+    order and may share it, calls on two streams may not."""
+    key = (device.index, stream.cuda_stream)
+    with _ws_lock:
+        ws = _attn_ws.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = _attn_ws[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        return ws
+
+
+def kv_cache(num_pages: int, num_heads: int, page_size: int, head_dim: int, device="cuda") -> KVCache:
+    """An empty cache: codes [num_pages, num_heads, page_size, head_dim] and scales
+    [num_pages, num_heads] for keys and values.  Any tensors of that form serve (a
+    token-major pool transposed to it, for instance): KVCache(k, v, k_scale, v_scale)."""
+    if page_size not in binding.KV_PAGE_SIZES or head_dim % 16 or not 16 <= head_dim <= binding.KV_MAX_HEAD_DIM:
+        raise ValueError(f"page_size must be one of {binding.KV_PAGE_SIZES}, head_dim a multiple of 16 of at most "
+                         f"{binding.KV_MAX_HEAD_DIM}")
+    codes = [torch.zeros((num_pages, num_heads, page_size, head_dim), dtype=torch.uint8, device=device) for _ in "kv"]
+    scales = [torch.ones((num_pages, num_heads), dtype=torch.float32, device=device) for _ in "kv"]
+    return KVCache(*(c.view(torch.float8_e4m3fn) for c in codes), *scales)
+
+
+def kv_append(cache: KVCache, k, v, page_table, cached_len, cu_new, max_new: int, stream=None) -> dict:
+    """Quantise the new tokens' keys and values k, v [tokens, heads, head_dim] (bfloat16
+    or float32) into the cache in place: request b's rows cu_new[b] .. cu_new[b+1] - 1
+    become its positions cached_len[b] ..; max_new bounds the rows of any request.
+    Returns status [B]."""
+    dev = k.device
+    with _on(stream):
+        out = dict(status=torch.empty(cu_new.numel() - 1, dtype=torch.int32, device=dev))
+        binding.spec_kv_append(cache, k, v, _as_i32(page_table, dev), _as_i32(cached_len, dev), _as_i32(cu_new, dev),
+                               max_new, out["status"], stream)
+    return out
+
+
+def kv_gather(cache: KVCache, page_table, cu_out, n_out: int, first=None, dtype=torch.bfloat16, stream=None) -> dict:
+    """Read the cache back: rows cu_out[b] .. cu_out[b+1] - 1 of k and v [n_out, heads,
+    head_dim] are request b's positions from first[b] (None: 0).  Returns k, v, status."""
+    dev = cache.k.device
+    shape = (n_out, cache.k.shape[1], cache.k.shape[3])
+    with _on(stream):
+        out = dict(k=torch.empty(shape, dtype=dtype, device=dev), v=torch.empty(shape, dtype=dtype, device=dev),
+                   status=torch.empty(cu_out.numel() - 1, dtype=torch.int32, device=dev))
+        binding.spec_kv_gather(cache, _as_i32(page_table, dev), _as_i32(cu_out, dev), _as_i32(first, dev), out["k"],
+                               out["v"], out["status"], stream)
+    return out
+
+
+def cache_attention(q, cache: KVCache, page_table, seq_len, cu_query, max_query: int, scale: float | None = None,
+                    window: int = 0, sinks: int = 0, want_lse: bool = False, stream=None) -> dict:
+    """Attention of the new tokens' queries q [tokens, query heads, head_dim] over the
+    cache, causal among the new tokens: request b's queries are rows cu_query[b] ..
+    cu_query[b+1] - 1 and sit at the last of its seq_len[b] cached positions.  window
+    limits each query to the last `window` positions and the first `sinks`; scale
+    defaults to head_dim ** -0.5.  Returns out, lse (None unless want_lse), status."""
+    dev = q.device
+    n, heads, dim = q.shape
+    with _on(stream):
+        out = dict(out=torch.empty((n, heads, dim), dtype=q.dtype, device=dev),
+                   lse=torch.empty((n, heads), dtype=torch.float32, device=dev) if want_lse else None,
+                   status=torch.empty(cu_query.numel() - 1, dtype=torch.int32, device=dev))
+        at = stream if stream is not None else torch.cuda.current_stream(dev)
+        nbytes = binding.spec_cache_attention_workspace_size(heads, cache.k.shape[1], dim, binding._dtype_code(q))
+        binding.spec_cache_attention(q, cache, _as_i32(page_table, dev), _as_i32(seq_len, dev), _as_i32(cu_query, dev),
+                                     max_query, dim ** -0.5 if scale is None else scale, window, sinks, out["out"],
+                                     out["lse"], out["status"], _attention_workspace(dev, at, nbytes), at)
+    return out

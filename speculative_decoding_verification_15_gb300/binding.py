@@ -12,6 +12,7 @@ import ctypes
 import os
 import re
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -21,6 +22,8 @@ SPEC_OK, SPEC_EINVAL, SPEC_ECUDA, SPEC_EUNSUPPORTED, SPEC_EWORKSPACE = 0, 1, 2, 
 SPEC_ESCRATCH = 5
 SPEC_BF16, SPEC_F32 = 0, 1
 STATUS_OK, STATUS_BAD_TOKEN, STATUS_BAD_K, STATUS_BAD_TEMPERATURE, STATUS_NONFINITE = 0, 1, 2, 3, 4
+STATUS_INTERNAL, STATUS_BAD_LENGTH, STATUS_BAD_PAGE = 5, 2, 6
+KV_PAGE_SIZES, KV_MAX_HEAD_DIM = (16, 32, 64, 128), 256
 
 _lock = threading.Lock()
 _lib = None
@@ -35,6 +38,23 @@ class SpecError(RuntimeError):
                 msg += f", cudaError {lib.spec_last_cuda_error()}"
         super().__init__(msg)
         self.rc = rc
+
+
+class KVCache(NamedTuple):
+    """The 8-bit paged key/value cache: codes [pages, heads, page_size, head_dim]
+    (float8_e4m3fn, head_dim contiguous, other strides multiples of 16 and the same
+    for keys and values) and one float32 scale for each page and head."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 def lib_path() -> str:
@@ -85,6 +105,16 @@ def load(path: str | None = None):
         lib.spec_schedule_verify_len_stale.restype = I32
         lib.spec_schedule_threshold.argtypes = [P, P, I32, I32, ctypes.c_float, P, P]
         lib.spec_schedule_threshold.restype = I32
+        C = ctypes.POINTER(_CacheStruct)
+        lib.spec_kv_append.argtypes = [C, P, P, I32, I64, I64, I32, I32, P, I32, P, P, I32, P, P]
+        lib.spec_kv_append.restype = I32
+        lib.spec_kv_gather.argtypes = [C, I32, P, I32, P, P, I32, P, P, I32, P, P]
+        lib.spec_kv_gather.restype = I32
+        lib.spec_cache_attention_workspace_size.argtypes = [I32, I32, I32, I32]
+        lib.spec_cache_attention_workspace_size.restype = SZ
+        lib.spec_cache_attention.argtypes = [C, P, I32, I64, I32, I32, I32, P, I32, P, P, I32, ctypes.c_float, I32,
+                                             I32, P, P, P, P, SZ, P]
+        lib.spec_cache_attention.restype = I32
         lib.spec_error_string.argtypes = [I32]
         lib.spec_error_string.restype = ctypes.c_char_p
         lib.spec_last_cuda_error.argtypes = []
@@ -468,6 +498,111 @@ def spec_schedule_threshold(conf, max_len, threshold: float, out_len, stream=Non
     _need(out_len, "out_len", torch.int32, (B,), dev)
     _call(lib, "spec_schedule_threshold", dev, _ptr(conf), _ptr(max_len), B, Kmax, float(threshold), _ptr(out_len),
                                      _stream_handle(stream, dev))
+
+
+def _cache_struct(cache, device) -> _CacheStruct:
+    k, v, ks, vs = cache
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        raise ValueError("cache keys and values must be [pages, heads, page_size, head_dim] of one layout")
+    if k.dtype is not torch.float8_e4m3fn and k.dtype is not torch.uint8:
+        raise TypeError(f"cache codes must be float8_e4m3fn (or their bytes), got {k.dtype}")
+    pages, heads, size, dim = k.shape
+    sp, sh, st, sd = k.stride()
+    if sd != 1:
+        raise ValueError("cache codes must have head_dim contiguous")
+    if k.device != device or v.device != device:
+        raise ValueError(f"the cache must be on {device}")
+    _need(ks, "k_scale", torch.float32, (pages, heads), device)
+    _need(vs, "v_scale", torch.float32, (pages, heads), device)
+    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), sp, sh, st, pages, size, heads, dim)
+
+
+def _token_rows(t, name, heads, dim, device) -> int:
+    """Row stride of [tokens, heads, dim] rows whose heads are contiguous."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must have heads and head_dim contiguous within a token")
+    ld = t.stride(0) if t.shape[0] > 1 else heads * dim
+    if ld < heads * dim:
+        raise ValueError(f"{name}: token rows overlap")
+    return ld
+
+
+def _page_table(t, B, device) -> int:
+    if t.dim() != 2:
+        raise ValueError("page_table must be [B, pages a request]")
+    _need(t, "page_table", torch.int32, (B, t.shape[1]), device)
+    return t.shape[1]
+
+
+def spec_kv_append(cache, k, v, page_table, cached_len, cu_new, max_new: int, out_status, stream=None) -> None:
+    """k, v [tokens, heads, head_dim]; cached_len [B]; cu_new [B + 1]; out_status [B]."""
+    lib = load()
+    dev = k.device
+    c = _cache_struct(cache, dev)
+    ldk = _token_rows(k, "k", c.num_heads, c.head_dim, dev)
+    ldv = _token_rows(v, "v", c.num_heads, c.head_dim, dev)
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must share tokens and dtype")
+    B = cu_new.numel() - 1
+    _need(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+    _need(cached_len, "cached_len", torch.int32, (B,), dev)
+    width = _page_table(page_table, B, dev)
+    _need(out_status, "out_status", torch.int32, (B,), dev)
+    _call(lib, "spec_kv_append", dev, ctypes.byref(c), _ptr(k), _ptr(v), _dtype_code(k), ldk, ldv, k.shape[0], B,
+          _ptr(cu_new), int(max_new), _ptr(cached_len), _ptr(page_table), width, _ptr(out_status),
+          _stream_handle(stream, dev))
+
+
+def spec_kv_gather(cache, page_table, cu_out, first, out_k, out_v, out_status, stream=None) -> None:
+    """out_k, out_v [rows, heads, head_dim]; cu_out [B + 1]; first [B] or None; out_status [B]."""
+    lib = load()
+    dev = out_k.device
+    c = _cache_struct(cache, dev)
+    n = out_k.shape[0]
+    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
+        _need(t, name, out_k.dtype, (n, c.num_heads, c.head_dim), dev)
+    B = cu_out.numel() - 1
+    _need(cu_out, "cu_out", torch.int32, (B + 1,), dev)
+    if first is not None:
+        _need(first, "first", torch.int32, (B,), dev)
+    width = _page_table(page_table, B, dev)
+    _need(out_status, "out_status", torch.int32, (B,), dev)
+    _call(lib, "spec_kv_gather", dev, ctypes.byref(c), B, _ptr(cu_out), n, _ptr(first), _ptr(page_table), width,
+          _ptr(out_k), _ptr(out_v), _dtype_code(out_k), _ptr(out_status), _stream_handle(stream, dev))
+
+
+def spec_cache_attention_workspace_size(num_query_heads: int, num_heads: int, head_dim: int, dtype: int) -> int:
+    return int(load().spec_cache_attention_workspace_size(num_query_heads, num_heads, head_dim, dtype))
+
+
+def spec_cache_attention(q, cache, page_table, seq_len, cu_query, max_query: int, scale: float, window: int,
+                         sinks: int, out, out_lse, out_status, workspace, stream=None) -> None:
+    """q, out [tokens, query heads, head_dim]; seq_len [B]; cu_query [B + 1]; out_lse
+    [tokens, query heads] float32 or None; out_status [B]; workspace zeroed once."""
+    lib = load()
+    dev = q.device
+    c = _cache_struct(cache, dev)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, query heads, head_dim], got {tuple(q.shape)}")
+    n, heads = q.shape[0], q.shape[1]
+    ldq = _token_rows(q, "q", heads, c.head_dim, dev)
+    _need(out, "out", q.dtype, (n, heads, c.head_dim), dev)
+    if out_lse is not None:
+        _need(out_lse, "out_lse", torch.float32, (n, heads), dev)
+    B = cu_query.numel() - 1
+    _need(cu_query, "cu_query", torch.int32, (B + 1,), dev)
+    _need(seq_len, "seq_len", torch.int32, (B,), dev)
+    width = _page_table(page_table, B, dev)
+    _need(out_status, "out_status", torch.int32, (B,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    _call(lib, "spec_cache_attention", dev, ctypes.byref(c), _ptr(q), _dtype_code(q), ldq, heads, n, B,
+          _ptr(cu_query), int(max_query), _ptr(seq_len), _ptr(page_table), width, float(scale), int(window),
+          int(sinks), _ptr(out), _ptr(out_lse), _ptr(out_status), _ptr(workspace), workspace.numel(),
+          _stream_handle(stream, dev))
 
 
 def profile_enable(on: bool) -> None:

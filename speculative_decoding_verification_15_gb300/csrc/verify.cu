@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include "spec_common.cuh"
+#include "kv_common.cuh"
 #include "spec_verify.h"
 
 using namespace specv;
@@ -3373,6 +3374,8 @@ int early_exit_impl(const void *target, const void *draft, int dtype, int B, int
 
 namespace specv {
 void note_cuda_error(int e) { t_last_cuda_error = e; }
+int kv_device_info(int *dev, int *sms) { return device_info(dev, sms); }
+int kv_check_device_pointer(const void *p, int dev) { return check_device_pointer(p, dev); }
 }  // namespace specv
 
 extern "C" {

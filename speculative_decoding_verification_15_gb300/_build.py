@@ -14,7 +14,7 @@ LIB_NAME = "libspecverify.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["verify.cu", "schedule.cu", "markov.cu", "kv_cache.cu", "cache_attention.cu"]
-HEADERS = ["spec_common.cuh", "kv_common.cuh"]
+HEADERS = ["spec_common.cuh", "kv_common.cuh", "tcgen05.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -14,7 +14,13 @@
 // load every SM alike.  A CTA whose part holds an item whole writes its output; an
 // item cut by a boundary leaves (m, l, o) of each part in the workspace, and the part
 // that arrives last (a counter; nobody waits) joins them in CTA order.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
 #include "kv_common.cuh"
+#include "tcgen05.cuh"
 
 namespace specv {
 namespace {
@@ -34,6 +40,7 @@ struct AttnParams {
     int64_t ld_q;
     int B, ld_table, n_tokens, max_query, Hq, group, window, sinks;
     float scale_log2;  // scale * log2(e)
+    bool q_vec;        // rows of q are 16-byte aligned
     int *tickets;      // [kMaxCtas], zero between calls
     float *partial;    // [2 * kMaxCtas][rows * (D + 2)]
 };
@@ -134,8 +141,9 @@ __device__ Share find_share(const AttnParams &p, int rows) {
 struct Part {
     Request r;
     int b, h, rt, t0, t1;
+    int nrows, pos0, pos1;  // rows of the row tile, positions of its first and last
+    bool whole;
     int64_t item;  // the item's first tile on the line
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == r.nt; }
     __device__ __forceinline__ int tile(int i) const { return i < r.s1 ? i : r.w0 + (i - r.s1); }
 };
 
@@ -158,6 +166,16 @@ __device__ __forceinline__ Part next_part(const AttnParams &p, Share &s, int row
     x.t1 = (int)min((int64_t)x.r.nt, x.t0 + left);
     s.u += x.t1 - x.t0;
     s.off += x.t1 - x.t0;
+    x.whole = x.t0 == 0 && x.t1 == x.r.nt;
+    const int row0 = x.rt * rows;
+    x.nrows = min(rows, x.r.n * p.group - row0);
+    x.pos0 = x.r.len - x.r.n + row0 / p.group;
+    x.pos1 = x.r.len - x.r.n + (row0 + x.nrows - 1) / p.group;
+    // tiles that start after the row tile's last position hold nothing for it; a part
+    // keeps at least one tile, so that it has a result to join
+    const int seen = x.pos1 < 0 ? 0 : (x.pos1 / kTile < x.r.w0 ? min(x.r.s1, x.pos1 / kTile + 1)
+                                                               : x.r.s1 + x.pos1 / kTile - x.r.w0 + 1);
+    x.t1 = max(x.t0 + 1, min(x.t1, seen));
     return x;
 }
 
@@ -170,6 +188,7 @@ __device__ __forceinline__ void write_statuses(const AttnParams &p, int lane) {
             const int bs = p.c.page_size, np = (r.len + bs - 1) / bs, ns = (r.sinks + bs - 1) / bs;
             const int32_t *t = p.table + (int64_t)b * p.ld_table;
             for (int i = lane; i < ns; i += 32) bad |= t[i] < 0 || t[i] >= p.c.num_pages;
+#pragma unroll 8
             for (int i = r.low / bs + lane; i < np; i += 32) bad |= t[i] < 0 || t[i] >= p.c.num_pages;
         }
         bad = __any_sync(0xffffffffu, bad);
@@ -272,8 +291,7 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
     Share share = find_share<kSimtThreads>(p, R);
     while (share.u < share.end) {
         const Part x = next_part(p, share, R);
-        const int nrows = min(R, x.r.n * p.group - x.rt * R);
-        const int first = x.r.len - x.r.n;
+        const int nrows = x.nrows, first = x.r.len - x.r.n;
         __syncthreads();  // the part before is done with shared memory
         for (int i = tid; i < R * D; i += kSimtThreads) {
             const int r = i / D, d = i - r * D;
@@ -415,7 +433,7 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
             s_w[R + tid] = ll;
         }
         __syncthreads();
-        if (x.whole()) {
+        if (x.whole) {
             for (int i = tid; i < nrows * D; i += kSimtThreads) {
                 const int r = i / D, d = i - r * D;
                 store_out<T>(p, x, x.rt * R + r, d, s_o[r][d] * inverse_sum(s_w[R + r]));
@@ -437,6 +455,599 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
                 join_parts<T, kSimtThreads>(p, x, R, nrows, c0, c1, s_w, 1);
         }
     }
+}
+
+// ------------------------------------------------------------------ tensor-core kernel
+// bf16 queries, head sizes up to 128.  Both products run on the fifth-generation
+// tensor cores straight from the e4m3 codes that the tiled copies bring to shared
+// memory; nothing is converted on the way.  With the tokens as M:
+//   S^T [128 tokens, R rows] = K [128, D] Q^T      (K's rows run along K)
+//   O^T [128 >= D, R rows]  = V^T [D, 128] P^T     (V transposed by the operand's layout)
+// so the rows of a tile, few in a verify step, are the products' narrow side and cost
+// what they are, and a thread of the softmax owns one token in S^T and one column of
+// the head in O^T: R values each.
+//  - e4m3 keeps 4 significant bits, so Q and P are each the sum of two e4m3 terms and
+//    every product runs twice.  A row of Q is scaled by a power of two to a largest
+//    magnitude of 128 .. 256: a bf16 entry (8 bits) is then exact in two terms down to
+//    2^-10 of the row's largest, and off by 2^-18 of it at most below.  P needs a
+//    reference near its own size: every tile has its own, its largest score, so that
+//    a tail of small probabilities next to one large one elsewhere keeps its bits.
+//  - The scale of a key's page multiplies the score; the scale of a value's page, over
+//    the tile's largest, multiplies the probability before it is rounded (2^8 at most,
+//    448 is the type's largest), and the tile's largest joins the weight with which
+//    O^T is added to the fp32 sums, 2^(tile reference - running reference).
+//  - The running reference of a row moves only when a tile's is more than 2^64 above
+//    it, so sums are rescaled at a part's first tile and hardly ever after.
+// Roles: warps of 128 threads a group of up to 32 rows for the softmax and the sums,
+// one warp for the copies (page ids and scales are read a batch ahead), one thread for
+// the products.  S^T and O^T are double-buffered: S^T of the next tile is multiplied
+// while the softmax of this one runs, O^T of this one while the sums take the last.
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kSlotBytes = kTile * 128;  // a tile of keys or values
+constexpr int kInfo = 8;                 // tiles whose scales are held at a time
+constexpr float kRefStep = 64.f;         // how far (log2) a tile may pass the running reference
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float redux_max(float x) {  // over the warp; a NaN counts as absent
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+__device__ __forceinline__ uint32_t float2_to_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_to_e4m3x2(uint32_t h) {
+    uint32_t r;
+    asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n cvt.u32.u16 %0, t;\n}" : "=r"(r) : "r"(h));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two floats as two pairs of e4m3 codes, the values and what is left of them.
+__device__ __forceinline__ void split_e4m3x2(float lo, float hi, uint32_t &first, uint32_t &rest) {
+    const uint32_t h = float2_to_half2(lo, hi);
+    first = half2_to_e4m3x2(h);
+    rest = half2_to_e4m3x2(half2_sub(h, e4m3x2_to_half2(first)));  // exact before the rounding
+}
+template <int NT>
+__device__ __forceinline__ void named_sync(int bar) {
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
+}
+
+template <int R>
+struct TcShape {
+    static constexpr int kRowsG = R < 32 ? R : 32;        // rows of a softmax group
+    static constexpr int kGroups = R / kRowsG;            // groups of 128 threads
+    static constexpr int kSoft = 128 * kGroups;           // softmax threads
+    static constexpr int kThreads = kSoft + 64;
+    static constexpr int kPerSM = R < 64 ? 2 : 1;         // CTAs an SM
+    static constexpr int kSlots = R == 16 ? 6 : (R == 32 ? 5 : 10);
+    static constexpr uint32_t kCols = 4 * R;              // S^T and O^T, two of each
+};
+
+template <int R>
+struct TcShared {
+    using C = TcShape<R>;
+    uint8_t ring[C::kSlots][kSlotBytes];
+    uint8_t q[2][R * 128];         // two terms, rows of 128 bytes, swizzled
+    uint8_t p[2][R / 16][kTile * 16];  // two terms, blocks of 16 rows, a token's 16 bytes together
+    uint64_t full[C::kSlots], empty[C::kSlots], info_full[kInfo], s_full[2], p_full, o_full, q_full;
+    float ks[kInfo][8], gv[kInfo][8], wv[kInfo];  // a tile's scales (TileInfo)
+    float4 cm[2][R / 2];           // row pairs: score factors, then minus the references
+    float beta[2][R], w[2][R], alpha[2][R];
+    int moved[2][2 * C::kGroups];
+    float red[4][R];
+    float c[R];                    // score factor of a row: scale * log2(e) / its power of two
+    float m[R], l[R];              // at a part's end
+    int pos[R];                    // a row's position
+    int orow[2][R];                // its output row (token * query heads + head), by the part's parity
+    float join[2 * R];
+    uint32_t tmem;
+    int flag;
+};
+
+// Sum over the warp of each of N <= 32 values a lane: lane i gets value i (mod N).
+template <int N>
+__device__ __forceinline__ float warp_sum_scatter(float (&v)[N], int lane) {
+#pragma unroll
+    for (int s = N / 2; s > 0; s >>= 1) {
+#pragma unroll
+        for (int i = 0; i < s; ++i) {
+            const bool up = lane & s;
+            const float keep = up ? v[i + s] : v[i], send = up ? v[i] : v[i + s];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        }
+    }
+    float x = v[0];
+#pragma unroll
+    for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+    return x;
+}
+
+// The queries of a part as two e4m3 terms, 128 / kRowsG threads a row.
+template <int R>
+__device__ __forceinline__ void load_queries(const AttnParams &p, const Part &x, TcShared<R> &sm, int tid, int parity) {
+    using C = TcShape<R>;
+    constexpr int kCols = C::kRowsG;            // 128 columns over 128 / kRowsG threads
+    constexpr int TPR = 128 / C::kRowsG;
+    const int row = (tid >> 7) * C::kRowsG + (tid & 127) / TPR, c0 = (tid % TPR) * kCols;
+    const int grow = x.rt * R + row, t = grow / p.group, g = grow - t * p.group, D = p.c.head_dim;
+    const bool live = row < x.nrows;
+    const int orow = live ? (x.r.row0 + t) * p.Hq + x.h * p.group + g : 0;
+    const char *src = (const char *)p.q + ((int64_t)(x.r.row0 + t) * p.ld_q + (int64_t)(x.h * p.group + g) * D) * 2;
+    float amax = 0.f;
+    bool bad = false;
+    float v[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; c += 8) {
+        float e[8] = {};
+        if (live && c0 + c < D) {
+            if (p.q_vec) load8<2, true>(src + (c0 + c) * 2, e);
+            else load8<2, false>(src + (c0 + c) * 2, e);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[c + i] = e[i];
+            bad |= !(fabsf(e[i]) < __int_as_float(0x7f800000));
+            amax = fmaxf(amax, fabsf(e[i]));
+        }
+    }
+#pragma unroll
+    for (int s = 1; s < TPR; s <<= 1) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+        bad |= (bool)__shfl_xor_sync(0xffffffffu, (int)bad, s);
+    }
+    // the largest magnitude's exponent becomes 7; a row with a NaN or an infinity is NaN
+    const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -110);
+    const float up = __uint_as_float((uint32_t)(bad ? 127 : 134 - e) << 23);
+    const float down = bad ? 1.f : __uint_as_float((uint32_t)(120 + e) << 23);
+#pragma unroll
+    for (int c = 0; c < kCols; c += 16) {
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a0, a1, b0, b1;
+            split_e4m3x2(v[c + 4 * i] * up, v[c + 4 * i + 1] * up, a0, b0);
+            split_e4m3x2(v[c + 4 * i + 2] * up, v[c + 4 * i + 3] * up, a1, b1);
+            a[i] = bad ? 0x7f7f7f7fu : a0 | (a1 << 16);
+            b[i] = b0 | (b1 << 16);
+        }
+        const int at = row * 128 + (((((c0 + c) >> 4)) ^ (row & 7)) << 4);
+        *(uint4 *)(sm.q[0] + at) = make_uint4(a[0], a[1], a[2], a[3]);
+        *(uint4 *)(sm.q[1] + at) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+    if (c0 == 0) {
+        sm.c[row] = p.scale_log2 * down;
+        sm.pos[row] = live ? x.r.len - x.r.n + t : -1;
+        sm.orow[parity][row] = orow;
+    }
+    fence_async_shared();
+    mbar_arrive(&sm.q_full);
+}
+
+template <int R>
+__global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
+    attention_tc_kernel(AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = TcShape<R>;
+    constexpr int NR = C::kRowsG, NS = C::kSlots;
+    extern __shared__ uint8_t raw[];
+    TcShared<R> &sm = *reinterpret_cast<TcShared<R> *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < kInfo; ++i) mbar_init(&sm.info_full[i], 1);
+        mbar_init(&sm.s_full[0], 1);
+        mbar_init(&sm.s_full[1], 1);
+        mbar_init(&sm.p_full, C::kSoft);
+        mbar_init(&sm.o_full, 1);
+        mbar_init(&sm.q_full, C::kSoft);
+        mbar_init_fence();
+    }
+    if (warp == C::kSoft / 32 + 1) tmem_alloc(&sm.tmem, C::kCols);
+    tc_fence_before();
+    Share share = find_share<C::kThreads>(p, R);  // it synchronises the CTA
+    tc_fence_after();
+    const uint32_t tm = sm.tmem, tS = tm, tO = tm + 2 * R;
+    bool dead = false;  // a wait ran out: wait no more, finish, report
+    auto wait = [&](uint64_t *bar, int parity) {
+        if (!dead && !mbar_wait(bar, parity, kWaitNs)) dead = true;
+    };
+
+    if (warp == C::kSoft / 32) {
+        // ---------------------------------------------------------------- copies
+        const int bs = p.c.page_size, shift = 31 - __clz(kTile / bs), ppt = 1 << shift, batch = 32 >> shift;
+        int seq = 0, g = 0;  // slots filled, tiles
+        while (share.u < share.end && !dead) {
+            const Part x = next_part(p, share, R);
+            const int32_t *table = p.table + (int64_t)x.b * p.ld_table;
+            auto fetch_page = [&](int i0) {
+                const int i = i0 + (lane >> shift);
+                if (i >= x.t1) return -1;
+                const int j = x.tile(i) * kTile + (lane & (ppt - 1)) * bs;
+                if (j >= x.r.len || (j + bs <= x.r.low && j >= x.r.sinks)) return -1;
+                const int page = table[j / bs];
+                return page < p.c.num_pages ? page : -1;
+            };
+            auto fetch_scale = [&](const float *s, int page) {
+                return page >= 0 ? __ldg(s + (int64_t)page * p.c.num_heads + x.h) : 0.f;
+            };
+            int page_n = fetch_page(x.t0);
+            float ks_n = fetch_scale(p.c.k_scale, page_n), vs_n = fetch_scale(p.c.v_scale, page_n);
+            for (int i0 = x.t0; i0 < x.t1; i0 += batch) {
+                const int page = page_n;
+                const float ks = ks_n, vs = vs_n;
+                page_n = fetch_page(i0 + batch);
+                for (int k = 0; k < batch && i0 + k < x.t1; ++k, ++g) {
+                    const int from = (k << shift) + (lane & (ppt - 1));
+                    const int pg = __shfl_sync(0xffffffffu, page, from);
+                    const float tks = __shfl_sync(0xffffffffu, ks, from), tvs = __shfl_sync(0xffffffffu, vs, from);
+                    float top = tvs;
+                    for (int s = 1; s < ppt; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++seq) {
+                        const int slot = seq % NS, turn = seq / NS;
+                        if (turn > 0) wait(&sm.empty[slot], (turn - 1) & 1);
+                        dead = __any_sync(0xffffffffu, dead);
+                        if (dead) break;
+                        if (kv == 0) {
+                            const int n = g % kInfo;
+                            if (lane < ppt) {
+                                sm.ks[n][lane] = tks;
+                                sm.gv[n][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
+                            }
+                            if (lane == 0) sm.wv[n] = top * (1.f / 256.f);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.info_full[n]);
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kSlotBytes);
+                        __syncwarp();
+                        // a page that is not there reads as zeros: past the map's end
+                        if (lane < ppt)
+                            tma_load_4d(sm.ring[slot] + lane * bs * 128, kv ? &vmap : &kmap, 0, 0, x.h,
+                                        pg >= 0 ? pg : p.c.num_pages, &sm.full[slot]);
+                    }
+                    if (dead) break;
+                    if (k == 0) {
+                        ks_n = fetch_scale(p.c.k_scale, page_n);
+                        vs_n = fetch_scale(p.c.v_scale, page_n);
+                    }
+                }
+                if (dead) break;
+            }
+        }
+    } else if (warp == C::kSoft / 32 + 1) {
+        // ---------------------------------------------------------------- products
+        write_statuses(p, lane);  // while the first tile is on its way
+        if (lane == 0) {
+            constexpr uint32_t iqk = fp8_idesc(R, false, false), ipv = fp8_idesc(R, true, true);
+            const int ksteps = (p.c.head_dim + 31) / 32;
+            const uint32_t ring = smem_addr(sm.ring), q = smem_addr(sm.q), pp = smem_addr(sm.p);
+            int part = 0;
+            auto scores = [&](int g, bool first) {
+                if (first) wait(&sm.q_full, part++ & 1);
+                const int seq = 2 * g, slot = seq % NS;
+                wait(&sm.full[slot], (seq / NS) & 1);
+                if (dead) return;
+                tc_fence_after();
+                const uint32_t a = ring + slot * kSlotBytes;
+                for (int t = 0; t < 2; ++t)
+                    for (int k = 0; k < ksteps; ++k)
+                        mma_fp8(tS + (g & 1) * R, smem_desc(a + 32 * k, 16, 1024, 2),
+                                smem_desc(q + t * R * 128 + 32 * k, 16, 1024, 2), iqk, (t | k) != 0);
+                mma_commit(&sm.s_full[g & 1]);
+                mma_commit(&sm.empty[slot]);
+            };
+            auto values = [&](int g) {
+                const int seq = 2 * g + 1, slot = seq % NS;
+                wait(&sm.full[slot], (seq / NS) & 1);
+                wait(&sm.p_full, g & 1);
+                if (dead) return;
+                tc_fence_after();
+                const uint32_t a = ring + slot * kSlotBytes;
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < kTile / 32; ++k)
+                        mma_fp8(tO + (g & 1) * R, smem_desc(a + 4096 * k, 1024, 1024, 2),
+                                smem_desc(pp + t * R * kTile + 512 * k, 128, kTile * 16, 0), ipv, (t | k) != 0);
+                mma_commit(&sm.o_full);
+                mma_commit(&sm.empty[slot]);
+            };
+            int g = 0;
+            while (share.u < share.end && !dead) {
+                const Part x = next_part(p, share, R);
+                scores(g, true);
+                for (int i = x.t0; i < x.t1; ++i, ++g) {
+                    if (i + 1 < x.t1) scores(g + 1, false);
+                    values(g);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- softmax and sums
+        const int grp = tid >> 7, t128 = tid & 127, w4 = warp & 3, r0 = grp * NR;
+        const int bs_shift = 31 - __clz(p.c.page_size), bar = 1 + grp;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        int g = 0;
+        Part x;
+        bool more = share.u < share.end;
+        if (more) {
+            x = next_part(p, share, R);
+            load_queries<R>(p, x, sm, tid, 0);
+            named_sync<C::kSoft>(3);
+        }
+        for (int parity = 0; more; parity ^= 1) {
+            float acc[NR], l[NR];
+            float m_run = kNegInf;  // thread r of the group: row r's running reference
+#pragma unroll
+            for (int r = 0; r < NR; ++r) acc[r] = l[r] = 0.f;
+            auto add_values = [&](int gg) {  // O^T of tile gg into the sums
+                const int buf = gg & 1;
+                wait(&sm.o_full, gg & 1);
+                tc_fence_after();
+                uint32_t o[NR];
+                tmem_ld<NR>(tO + buf * R + r0 + lanes, o);
+                bool moved = sm.moved[buf][2 * grp] != 0;
+                tmem_wait_ld();
+                if (moved) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) acc[r] *= sm.alpha[buf][r0 + r];
+                }
+#pragma unroll
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 f = *(const float4 *)&sm.w[buf][r0 + r];
+                    float2 a = make_float2(acc[r], acc[r + 1]), b = make_float2(acc[r + 2], acc[r + 3]);
+                    a = ffma2(make_float2(__uint_as_float(o[r]), __uint_as_float(o[r + 1])), make_float2(f.x, f.y), a);
+                    b = ffma2(make_float2(__uint_as_float(o[r + 2]), __uint_as_float(o[r + 3])), make_float2(f.z, f.w), b);
+                    acc[r] = a.x;
+                    acc[r + 1] = a.y;
+                    acc[r + 2] = b.x;
+                    acc[r + 3] = b.y;
+                }
+            };
+            for (int i = x.t0; i < x.t1; ++i, ++g) {
+                const int buf = g & 1, inf = g % kInfo, j0 = x.tile(i) * kTile, j = j0 + t128;
+                wait(&sm.info_full[inf], (g / kInfo) & 1);
+                const float ks = sm.ks[inf][t128 >> bs_shift], gv = sm.gv[inf][t128 >> bs_shift], wv = sm.wv[inf];
+                wait(&sm.s_full[buf], (g >> 1) & 1);
+                tc_fence_after();
+                uint32_t s[NR];
+                tmem_ld<NR>(tS + buf * R + r0 + lanes, s);
+                tmem_wait_ld();
+                float v[NR];
+#pragma unroll
+                for (int r = 0; r < NR; r += 2) {
+                    const float2 f = fmul2(make_float2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), make_float2(ks, ks));
+                    v[r] = f.x;
+                    v[r + 1] = f.y;
+                }
+                // every row of the tile sees every token of it, or not
+                const bool masked = j0 + kTile - 1 > x.pos0 ||
+                                    (p.window > 0 && j0 <= x.pos1 - p.window && j0 + kTile > p.sinks);
+                uint32_t sees = 0xffffffffu;
+                bool spoilt = false;
+                if (masked) {
+                    sees = 0;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        const int at = sm.pos[r0 + r];
+                        const bool see = j <= at && (p.window == 0 || j > at - p.window || j < p.sinks);
+                        sees |= see ? 1u << r : 0u;
+                        v[r] = see ? v[r] : kNegInf;
+                    }
+                    // 0 times a NaN is a NaN: a value row that some rows do not see is
+                    // cleared if no row sees it, or if it holds a NaN, which then
+                    // reaches the rows that see it through their probability
+                    const bool any = j <= x.pos1 && (p.window == 0 || j > x.pos0 - p.window || j < p.sinks);
+                    const bool all = j <= x.pos0 && (p.window == 0 || j > x.pos1 - p.window || j < p.sinks);
+                    const int slot = (2 * g + 1) % NS;
+                    wait(&sm.full[slot], ((2 * g + 1) / NS) & 1);
+                    uint4 *row = (uint4 *)(sm.ring[slot] + t128 * 128);
+                    if (any && !all) {
+                        uint32_t nan = 0;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 q = row[(c + lane) & 7];
+                            nan |= __vcmpeq4(q.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(q.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                                   __vcmpeq4(q.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(q.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        }
+                        spoilt = nan != 0;
+                    }
+                    __syncwarp();
+                    // one group clears; with two, both have looked before it does
+                    if constexpr (C::kGroups > 1) named_sync<C::kSoft>(4);
+                    if ((!any || spoilt) && grp == 0) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) row[(c + lane) & 7] = make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+                // the tile's largest score of every row
+                float top = kNegInf;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float mr = redux_max(v[r]);
+                    if ((lane & (NR - 1)) == r) top = mr;
+                }
+                if (lane < NR) sm.red[w4][r0 + lane] = top;
+                named_sync<128>(bar);
+                if (w4 == 0) {
+                    const int r = r0 + (lane & (NR - 1));
+                    float mt = fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]), fmaxf(sm.red[2][r], sm.red[3][r]));
+                    const float c = sm.c[r];
+                    const bool some = mt > kNegInf;
+                    const float ref = some ? mt * c : 0.f, mm = some ? ref : kNegInf;
+                    float alpha = 1.f;
+                    const bool moves = mm > m_run + kRefStep;  // also from -inf
+                    if (moves) {
+                        alpha = m_run == kNegInf ? 0.f : ex2_approx(m_run - mm);
+                        m_run = mm;
+                    }
+                    const float beta = some ? ex2_approx(mm - m_run) : 1.f;
+                    const bool any_moves = __any_sync(0xffffffffu, moves);
+                    if (lane < NR) {
+                        float *cm = (float *)&sm.cm[buf][r >> 1];
+                        cm[r & 1] = c;
+                        cm[2 + (r & 1)] = -ref;
+                        sm.beta[buf][r] = beta;
+                        sm.w[buf][r] = beta * wv;
+                        sm.alpha[buf][r] = alpha;
+                    }
+                    if (lane == 0) sm.moved[buf][2 * grp] = any_moves;
+                }
+                named_sync<128>(bar);
+                if (sm.moved[buf][2 * grp]) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) l[r] *= sm.alpha[buf][r0 + r];
+                }
+                uint32_t hi[NR / 4], lo[NR / 4];
+                const float2 gv2 = make_float2(gv, gv);
+#pragma unroll
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 b = *(const float4 *)&sm.beta[buf][r0 + r];
+                    uint32_t h2[2], l2[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k = r + 2 * e;
+                        const float4 f = sm.cm[buf][(r0 + k) >> 1];
+                        float2 z = ffma2(make_float2(v[k], v[k + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
+                        z.x = ex2_approx(z.x);
+                        z.y = ex2_approx(z.y);
+                        if (masked) {
+                            const float nan = __int_as_float(0x7fffffff);
+                            z.x = (sees >> k) & 1 ? (spoilt ? nan : z.x) : 0.f;
+                            z.y = (sees >> (k + 1)) & 1 ? (spoilt ? nan : z.y) : 0.f;
+                        }
+                        const float2 ll = ffma2(z, e ? make_float2(b.z, b.w) : make_float2(b.x, b.y), make_float2(l[k], l[k + 1]));
+                        l[k] = ll.x;
+                        l[k + 1] = ll.y;
+                        z = fmul2(z, gv2);
+                        split_e4m3x2(z.x, z.y, h2[e], l2[e]);
+                    }
+                    hi[r / 4] = h2[0] | (h2[1] << 16);
+                    lo[r / 4] = l2[0] | (l2[1] << 16);
+                }
+                if (i > x.t0) wait(&sm.o_full, (g - 1) & 1);  // the last tile's product has read P
+#pragma unroll
+                for (int k = 0; k < NR / 16; ++k) {
+                    *(uint4 *)(sm.p[0][r0 / 16 + k] + t128 * 16) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                    *(uint4 *)(sm.p[1][r0 / 16 + k] + t128 * 16) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                }
+                fence_async_shared();
+                tc_fence_before();
+                mbar_arrive(&sm.p_full);
+                if (i > x.t0) add_values(g - 1);
+            }
+            // the next part's queries go out before this part's last product is waited for
+            const Part done = x;
+            more = share.u < share.end;
+            named_sync<C::kSoft>(3);
+            if (more) {
+                x = next_part(p, share, R);
+                load_queries<R>(p, x, sm, tid, parity ^ 1);
+            }
+            add_values(g - 1);
+            tc_fence_before();
+            const float lt = warp_sum_scatter<NR>(l, lane);
+            if (lane < NR) sm.red[w4][r0 + lane] = lt;
+            named_sync<128>(bar);
+            if (w4 == 0 && lane < NR) {
+                const int r = r0 + lane;
+                sm.m[r] = m_run;
+                sm.l[r] = sm.red[0][r] + sm.red[1][r] + sm.red[2][r] + sm.red[3][r];
+            }
+            named_sync<128>(bar);
+            if (dead) p.status[done.b] = SPEC_STATUS_INTERNAL;
+            const int D = p.c.head_dim;
+            if (done.whole) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    if (r0 + r < done.nrows && t128 < D)
+                        ((uint16_t *)p.out)[(int64_t)sm.orow[parity][r0 + r] * D + t128] =
+                            (uint16_t)pack_bf16x2(acc[r] * inverse_sum(sm.l[r0 + r]), 0.f);
+                if (p.lse && t128 < NR && r0 + t128 < done.nrows)
+                    store_lse(p, done, done.rt * R + r0 + t128, sm.m[r0 + t128], sm.l[r0 + t128]);
+            } else {
+                float *slot = slot_of(p, blockIdx.x, done.t0 == 0, R);
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    if (r0 + r < done.nrows && t128 < D) slot[(r0 + r) * D + t128] = acc[r];
+                if (t128 < NR && r0 + t128 < done.nrows) {
+                    slot[R * D + r0 + t128] = sm.m[r0 + t128];
+                    slot[R * D + R + r0 + t128] = sm.l[r0 + t128];
+                }
+                const int c0 = cta_of(share.total, done.item, share.ctas);
+                const int c1 = cta_of(share.total, done.item + done.r.nt - 1, share.ctas);
+                if (arrive_last<C::kSoft>(p, c0, c1 - c0 + 1, &sm.flag, 3))
+                    join_parts<uint16_t, C::kSoft>(p, done, R, done.nrows, c0, c1, sm.join, 3);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::kSoft / 32 + 1) tmem_free(tm, C::kCols);
+}
+
+// ------------------------------------------------------------------ host
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 got = fn.load();
+    if (!got) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn.store(got = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f));
+        cudaGetLastError();
+    }
+    return got;
+}
+
+// The codes as a map {head_dim, page_size, heads, pages}: a box is one page of one head,
+// its rows filled with zeros to 128 bytes and swizzled.
+bool codes_map(const spec_kv_cache &c, const void *codes, CUtensorMap *map) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_heads,
+                                (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride};
+    const cuuint32_t box[4] = {128, (cuuint32_t)c.page_size, 1, 1}, one[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(codes), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int R>
+int launch_tc(const AttnParams &p, int dev, int sms, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+    using C = TcShape<R>;
+    constexpr int bytes = (int)sizeof(TcShared<R>) + 1024;
+    static_assert(C::kPerSM * (bytes + 1024) <= 228 * 1024, "shared memory of an SM");
+    static std::atomic<bool> set[64];
+    if (!set[dev].load()) {
+        const cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) {
+            note_cuda_error((int)e);
+            return SPEC_ECUDA;
+        }
+        set[dev].store(true);
+    }
+    const int ctas = C::kPerSM * sms < kMaxCtas ? C::kPerSM * sms : kMaxCtas;
+    attention_tc_kernel<R><<<ctas, C::kThreads, bytes, st>>>(p, kmap, vmap);
+    return launch_status();
 }
 
 }  // namespace
@@ -498,6 +1109,16 @@ extern "C" int spec_cache_attention(const spec_kv_cache *cache, const void *q, i
     p.tickets = (int *)ws;
     p.partial = (float *)((char *)ws + sizeof(int) * kMaxCtas);
     const cudaStream_t st = (cudaStream_t)cuda_stream;
+    p.q_vec = !((uintptr_t)q & 15) && !((ld_q * esz) & 15);
+    // bf16 heads of up to 128 columns (one swizzled row of a tile): the tensor cores, in
+    // row tiles of 16, 32 or 64
+    alignas(64) CUtensorMap kmap, vmap;
+    if (esz == 2 && cache->head_dim <= 128 && codes_map(*cache, cache->k, &kmap) && codes_map(*cache, cache->v, &vmap)) {
+        const int64_t rows = (int64_t)max_query * p.group;
+        if (rows <= 16) return launch_tc<16>(p, dev, sms, kmap, vmap, st);
+        if (rows <= 32) return launch_tc<32>(p, dev, sms, kmap, vmap, st);
+        return launch_tc<64>(p, dev, sms, kmap, vmap, st);
+    }
     const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
     if (cache->head_dim <= 128) {
         if (esz == 2) attention_simt_kernel<uint16_t, 1><<<ctas, kSimtThreads, 0, st>>>(p);

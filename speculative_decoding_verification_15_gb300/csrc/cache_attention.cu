@@ -60,7 +60,7 @@ __device__ __forceinline__ Request load_request(const AttnParams &p, int b, int 
     r.len = p.seq_len[b];
     r.n = row1 - r.row0;
     r.ok = r.row0 >= 0 && row1 >= r.row0 && row1 <= p.n_tokens && r.n <= p.max_query && r.len >= 0 &&
-           r.len <= (int64_t)p.ld_table * p.c.page_size;
+           r.len <= min((int64_t)p.ld_table * p.c.page_size, (int64_t)0x7fffffff - 2 * kTile);
     if (!r.ok) r.n = r.len = 0;
     const int first = r.len - r.n;  // position of the first query
     r.low = p.window > 0 ? max(0, first - p.window + 1) : 0;
@@ -68,12 +68,18 @@ __device__ __forceinline__ Request load_request(const AttnParams &p, int b, int 
     r.w0 = r.low / kTile;
     r.s1 = min((r.sinks + kTile - 1) / kTile, r.w0);
     r.nt = max(1, r.s1 + (r.len + kTile - 1) / kTile - r.w0);
-    r.rt = (int)(((int64_t)r.n * p.group + rows - 1) / rows);
+    r.rt = (int)(((uint32_t)r.n * p.group + rows - 1) / rows);  // the host keeps n * group below 2^31
     return r;
 }
 
 __device__ __forceinline__ int64_t request_tiles(const AttnParams &p, const Request &r) {
     return (int64_t)p.c.num_heads * r.rt * r.nt;
+}
+
+// a / b for a >= 0, b > 0: most quotients here fit 32 bits, where a division is short.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
 }
 
 // A CTA's place on the line of tiles: [u, end), starting `off` tiles into request b.
@@ -84,10 +90,12 @@ struct Share {
     int b, ctas;
 };
 
-__device__ __forceinline__ int64_t share_start(int64_t total, int cta, int ctas) { return total * cta / ctas; }
+__device__ __forceinline__ int64_t share_start(int64_t total, int cta, int ctas) {
+    return quotient(total * cta, ctas);
+}
 // The CTA whose share holds tile u.
 __device__ __forceinline__ int cta_of(int64_t total, int64_t u, int ctas) {
-    return (int)(((u + 1) * ctas - 1) / total);
+    return (int)quotient((u + 1) * ctas - 1, total);
 }
 
 // Every thread of the CTA calls it (it synchronises); NT threads.
@@ -143,7 +151,7 @@ struct Part {
     int b, h, rt, t0, t1;
     int nrows, pos0, pos1;  // rows of the row tile, positions of its first and last
     bool whole;
-    int64_t item;  // the item's first tile on the line
+    int c0, c1;  // the CTAs that hold the item's first and last tile
     __device__ __forceinline__ int tile(int i) const { return i < r.s1 ? i : r.w0 + (i - r.s1); }
 };
 
@@ -157,16 +165,20 @@ __device__ __forceinline__ Part next_part(const AttnParams &p, Share &s, int row
         ++s.b;
     }
     x.b = s.b;
-    const int64_t i = s.off / x.r.nt;
+    const int64_t i = quotient(s.off, x.r.nt);
     x.t0 = (int)(s.off - i * x.r.nt);
-    x.h = (int)(i / x.r.rt);
+    x.h = (int)quotient(i, x.r.rt);
     x.rt = (int)(i - (int64_t)x.h * x.r.rt);
-    x.item = s.u - x.t0;
-    const int64_t left = s.end - s.u;
+    const int64_t item = s.u - x.t0, left = s.end - s.u;
     x.t1 = (int)min((int64_t)x.r.nt, x.t0 + left);
     s.u += x.t1 - x.t0;
     s.off += x.t1 - x.t0;
     x.whole = x.t0 == 0 && x.t1 == x.r.nt;
+    x.c0 = x.c1 = blockIdx.x;
+    if (!x.whole) {
+        x.c0 = cta_of(s.total, item, s.ctas);
+        x.c1 = cta_of(s.total, item + x.r.nt - 1, s.ctas);
+    }
     const int row0 = x.rt * rows;
     x.nrows = min(rows, x.r.n * p.group - row0);
     x.pos0 = x.r.len - x.r.n + row0 / p.group;
@@ -239,33 +251,89 @@ __device__ __forceinline__ bool arrive_last(const AttnParams &p, int first_cta, 
     return last;
 }
 
-// Joins the parts of an item in CTA order and writes its rows.  s_w: 2 * rows floats.
-template <typename T, int NT>
-__device__ void join_parts(const AttnParams &p, const Part &x, int rows, int nrows, int c0, int c1, float *s_w,
-                           int bar) {
-    const int D = p.c.head_dim, tid = threadIdx.x;
-    for (int r = tid; r < nrows; r += NT) {
+// Joins the parts of an item in CTA order and writes its rows.  The weights of up to
+// kJoin parts at a time are laid out first, so that the sums' loads, four columns a
+// thread, depend on nothing and are in flight together.
+constexpr int kJoin = 16;
+template <int R>
+struct JoinSpace {
+    float m[R], l[R];
+    float w[kJoin][R];
+};
+
+template <typename T, int NT, int R>
+__device__ void join_parts(const AttnParams &p, const Part &x, JoinSpace<R> &sp, int bar) {
+    const int D = p.c.head_dim, tid = threadIdx.x, nrows = x.nrows, parts = x.c1 - x.c0 + 1;
+    if (tid < nrows) {
         float m = kNegInf, l = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const float *s = slot_of(p, c, c == c0, rows) + (int64_t)rows * D;
-            const float mc = __ldcg(s + r), lc = __ldcg(s + rows + r);
-            const float mn = fmaxf(m, mc);
-            l = l * weight_of(m, mn) + lc * weight_of(mc, mn);
-            m = mn;
+        for (int i0 = 0; i0 < parts; i0 += 8) {
+            float mc[8], lc[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float *s = slot_of(p, x.c0 + min(i0 + k, parts - 1), i0 + k == 0, R) + (int64_t)R * D + tid;
+                mc[k] = i0 + k < parts ? __ldcg(s) : kNegInf;
+                lc[k] = i0 + k < parts ? __ldcg(s + R) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float mn = fmaxf(m, mc[k]);
+                l = l * weight_of(m, mn) + lc[k] * weight_of(mc[k], mn);
+                m = mn;
+            }
         }
-        s_w[r] = m;
-        s_w[rows + r] = inverse_sum(l);
-        if (p.lse) store_lse(p, x, x.rt * rows + r, m, l);
+        sp.m[tid] = m;
+        sp.l[tid] = inverse_sum(l);
+        if (p.lse) store_lse(p, x, x.rt * R + tid, m, l);
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
-    for (int i = tid; i < nrows * D; i += NT) {
-        const int r = i / D, d = i - r * D;
-        float o = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const float *s = slot_of(p, c, c == c0, rows);
-            o = fmaf(__ldcg(s + i), weight_of(__ldcg(s + (int64_t)rows * D + r), s_w[r]), o);
+    const int groups = D / 4, step = NT / 32;  // a warp a row, four columns a lane
+    for (int base = 0; base < nrows; base += 4 * step) {
+        float4 o[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k][0] = o[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < parts; i0 += kJoin) {
+            asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
+            for (int i = tid; i < kJoin * nrows; i += NT) {
+                const int c = i / nrows, r = i - c * nrows;
+                if (i0 + c < parts)
+                    sp.w[c][r] = weight_of(__ldcg(slot_of(p, x.c0 + i0 + c, i0 + c == 0, R) + (int64_t)R * D + r), sp.m[r]);
+            }
+            asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
+#pragma unroll 4
+            for (int c = 0; c < min(kJoin, parts - i0); ++c) {
+                const float4 *s = (const float4 *)slot_of(p, x.c0 + i0 + c, i0 + c == 0, R);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = base + k * step + (tid >> 5);
+                    if (r >= nrows) continue;
+                    const float w = sp.w[c][r];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int d = n * 32 + (tid & 31);
+                        if (d >= groups) continue;
+                        const float4 v = __ldcg(s + r * groups + d);
+                        o[k][n].x = fmaf(v.x, w, o[k][n].x);
+                        o[k][n].y = fmaf(v.y, w, o[k][n].y);
+                        o[k][n].z = fmaf(v.z, w, o[k][n].z);
+                        o[k][n].w = fmaf(v.w, w, o[k][n].w);
+                    }
+                }
+            }
         }
-        store_out<T>(p, x, x.rt * rows + r, d, o * s_w[rows + r]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = base + k * step + (tid >> 5);
+            if (r >= nrows) continue;
+            const float inv = sp.l[r];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int d = n * 32 + (tid & 31);
+                if (d >= groups) continue;
+                store_out<T>(p, x, x.rt * R + r, 4 * d, o[k][n].x * inv);
+                store_out<T>(p, x, x.rt * R + r, 4 * d + 1, o[k][n].y * inv);
+                store_out<T>(p, x, x.rt * R + r, 4 * d + 2, o[k][n].z * inv);
+                store_out<T>(p, x, x.rt * R + r, 4 * d + 3, o[k][n].w * inv);
+            }
+        }
     }
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
 }
@@ -283,6 +351,7 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
     __shared__ __align__(16) float s_q[R][128 * ND];
     __shared__ float s_p[4][32][R];
     __shared__ float s_m[4][R], s_l[4][R], s_w[2 * R];
+    __shared__ JoinSpace<R> s_join;
     __shared__ __align__(16) float s_o[R][128 * ND];
     __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -449,10 +518,8 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
                 slot[R * D + tid] = s_w[tid];
                 slot[R * D + R + tid] = s_w[R + tid];
             }
-            const int c0 = cta_of(share.total, x.item, share.ctas);
-            const int c1 = cta_of(share.total, x.item + x.r.nt - 1, share.ctas);
-            if (arrive_last<kSimtThreads>(p, c0, c1 - c0 + 1, &s_flag, 1))
-                join_parts<T, kSimtThreads>(p, x, R, nrows, c0, c1, s_w, 1);
+            if (arrive_last<kSimtThreads>(p, x.c0, x.c1 - x.c0 + 1, &s_flag, 1))
+                join_parts<T, kSimtThreads, R>(p, x, s_join, 1);
         }
     }
 }
@@ -504,21 +571,28 @@ __device__ __forceinline__ uint32_t float2_to_half2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t half2_to_e4m3x2(uint32_t h) {
-    uint32_t r;
-    asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n cvt.u32.u16 %0, t;\n}" : "=r"(r) : "r"(h));
-    return r;
-}
 __device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Two floats as two pairs of e4m3 codes, the values and what is left of them.
-__device__ __forceinline__ void split_e4m3x2(float lo, float hi, uint32_t &first, uint32_t &rest) {
-    const uint32_t h = float2_to_half2(lo, hi);
-    first = half2_to_e4m3x2(h);
-    rest = half2_to_e4m3x2(half2_sub(h, e4m3x2_to_half2(first)));  // exact before the rounding
+__device__ __forceinline__ uint32_t half4_to_e4m3x4(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n .reg .b16 t, u;\n cvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 u, %2;\n"
+        " mov.b32 %0, {t, u};\n}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+    return r;
+}
+// Four floats as two words of e4m3 codes: the values, and what is left of them.
+__device__ __forceinline__ void split_e4m3x4(float2 x, float2 y, uint32_t &first, uint32_t &rest) {
+    const uint32_t a = float2_to_half2(x.x, x.y), b = float2_to_half2(y.x, y.y);
+    uint32_t c, d;
+    first = half4_to_e4m3x4(a, b);
+    asm("{\n .reg .b16 t, u;\n mov.b32 {t, u}, %2;\n cvt.rn.f16x2.e4m3x2 %0, t;\n cvt.rn.f16x2.e4m3x2 %1, u;\n}"
+        : "=r"(c), "=r"(d)
+        : "r"(first));
+    rest = half4_to_e4m3x4(half2_sub(a, c), half2_sub(b, d));  // exact before the rounding
 }
 template <int NT>
 __device__ __forceinline__ void named_sync(int bar) {
@@ -536,23 +610,27 @@ struct TcShape {
     static constexpr uint32_t kCols = 4 * R;              // S^T and O^T, two of each
 };
 
+constexpr int kParts = 4;  // parts known ahead
+
 template <int R>
 struct TcShared {
     using C = TcShape<R>;
     uint8_t ring[C::kSlots][kSlotBytes];
-    uint8_t q[2][R * 128];         // two terms, rows of 128 bytes, swizzled
+    uint8_t q[2][R * 128];             // two terms, rows of 128 bytes, swizzled
     uint8_t p[2][R / 16][kTile * 16];  // two terms, blocks of 16 rows, a token's 16 bytes together
     uint64_t full[C::kSlots], empty[C::kSlots], info_full[kInfo], s_full[2], p_full, o_full, q_full;
-    float ks[kInfo][8], gv[kInfo][8], wv[kInfo];  // a tile's scales (TileInfo)
-    float4 cm[2][R / 2];           // row pairs: score factors, then minus the references
-    float beta[2][R], w[2][R], alpha[2][R];
-    int moved[2][2 * C::kGroups];
-    float red[4][R];
-    float c[R];                    // score factor of a row: scale * log2(e) / its power of two
-    float m[R], l[R];              // at a part's end
-    int pos[R];                    // a row's position
-    int orow[2][R];                // its output row (token * query heads + head), by the part's parity
-    float join[2 * R];
+    uint64_t part_full[kParts], part_empty[kParts];
+    Part part[kParts];                      // b < 0: no more
+    float ks[kInfo][8], gv[kInfo][8], wv[kInfo];  // a tile's scales
+    // every softmax warp's own copy, by the tile's parity: row pairs' score factors and
+    // minus references, weights of the sums, of O^T, and of the sums before
+    float4 cm[4 * C::kGroups][2][C::kRowsG / 2];
+    float beta[4 * C::kGroups][2][C::kRowsG], w[4 * C::kGroups][2][C::kRowsG], alpha[4 * C::kGroups][2][C::kRowsG];
+    float red[2][4][R];
+    float c[R];        // score factor of a row: scale * log2(e) / its power of two
+    float m[R], l[R];  // at a part's end
+    int orow[2][R];    // a row's output row (token * query heads + head), by the part's parity
+    JoinSpace<R> join;
     uint32_t tmem;
     int flag;
 };
@@ -575,6 +653,19 @@ __device__ __forceinline__ float warp_sum_scatter(float (&v)[N], int lane) {
     return x;
 }
 
+// Brings a part's queries into L1 before they are needed.
+template <int R>
+__device__ __forceinline__ void touch_queries(const AttnParams &p, const Part &x, int tid) {
+    using C = TcShape<R>;
+    constexpr int kCols = C::kRowsG, TPR = 128 / C::kRowsG;
+    const int row = (tid >> 7) * C::kRowsG + (tid & 127) / TPR, c0 = (tid % TPR) * kCols;
+    const int grow = x.rt * R + row, t = grow / p.group, g = grow - t * p.group;
+    if (row < x.nrows && c0 < p.c.head_dim) {
+        const char *src = (const char *)p.q + ((int64_t)(x.r.row0 + t) * p.ld_q + (int64_t)(x.h * p.group + g) * p.c.head_dim + c0) * 2;
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
+    }
+}
+
 // The queries of a part as two e4m3 terms, 128 / kRowsG threads a row.
 template <int R>
 __device__ __forceinline__ void load_queries(const AttnParams &p, const Part &x, TcShared<R> &sm, int tid, int parity) {
@@ -593,7 +684,15 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Part &x,
     for (int c = 0; c < kCols; c += 8) {
         float e[8] = {};
         if (live && c0 + c < D) {
-            if (p.q_vec) load8<2, true>(src + (c0 + c) * 2, e);
+            if (p.q_vec) {
+                const uint4 u = __ldg((const uint4 *)(src + (c0 + c) * 2));  // in L1: see touch_queries
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    e[2 * i] = bf16_lo(w[i]);
+                    e[2 * i + 1] = bf16_hi(w[i]);
+                }
+            }
             else load8<2, false>(src + (c0 + c) * 2, e);
         }
 #pragma unroll
@@ -617,19 +716,16 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Part &x,
         uint32_t a[4], b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t a0, a1, b0, b1;
-            split_e4m3x2(v[c + 4 * i] * up, v[c + 4 * i + 1] * up, a0, b0);
-            split_e4m3x2(v[c + 4 * i + 2] * up, v[c + 4 * i + 3] * up, a1, b1);
-            a[i] = bad ? 0x7f7f7f7fu : a0 | (a1 << 16);
-            b[i] = b0 | (b1 << 16);
+            split_e4m3x4(make_float2(v[c + 4 * i] * up, v[c + 4 * i + 1] * up),
+                         make_float2(v[c + 4 * i + 2] * up, v[c + 4 * i + 3] * up), a[i], b[i]);
+            if (bad) a[i] = 0x7f7f7f7fu;
         }
         const int at = row * 128 + (((((c0 + c) >> 4)) ^ (row & 7)) << 4);
         *(uint4 *)(sm.q[0] + at) = make_uint4(a[0], a[1], a[2], a[3]);
         *(uint4 *)(sm.q[1] + at) = make_uint4(b[0], b[1], b[2], b[3]);
     }
     if (c0 == 0) {
-        sm.c[row] = p.scale_log2 * down;
-        sm.pos[row] = live ? x.r.len - x.r.n + t : -1;
+        sm.c[row] = fmaxf(p.scale_log2 * down, 1.1754944e-38f);  // -inf times it stays -inf
         sm.orow[parity][row] = orow;
     }
     fence_async_shared();
@@ -655,6 +751,10 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         mbar_init(&sm.p_full, C::kSoft);
         mbar_init(&sm.o_full, 1);
         mbar_init(&sm.q_full, C::kSoft);
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(&sm.part_full[i], 1);
+            mbar_init(&sm.part_empty[i], 2);
+        }
         mbar_init_fence();
     }
     if (warp == C::kSoft / 32 + 1) tmem_alloc(&sm.tmem, C::kCols);
@@ -669,64 +769,92 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
 
     if (warp == C::kSoft / 32) {
         // ---------------------------------------------------------------- copies
+        // This warp also finds the parts and tells the others, one part ahead; page ids
+        // and scales come a batch of 32 pages ahead.
         const int bs = p.c.page_size, shift = 31 - __clz(kTile / bs), ppt = 1 << shift, batch = 32 >> shift;
-        int seq = 0, g = 0;  // slots filled, tiles
-        while (share.u < share.end && !dead) {
-            const Part x = next_part(p, share, R);
-            const int32_t *table = p.table + (int64_t)x.b * p.ld_table;
-            auto fetch_page = [&](int i0) {
-                const int i = i0 + (lane >> shift);
-                if (i >= x.t1) return -1;
-                const int j = x.tile(i) * kTile + (lane & (ppt - 1)) * bs;
-                if (j >= x.r.len || (j + bs <= x.r.low && j >= x.r.sinks)) return -1;
-                const int page = table[j / bs];
-                return page < p.c.num_pages ? page : -1;
-            };
-            auto fetch_scale = [&](const float *s, int page) {
-                return page >= 0 ? __ldg(s + (int64_t)page * p.c.num_heads + x.h) : 0.f;
-            };
-            int page_n = fetch_page(x.t0);
-            float ks_n = fetch_scale(p.c.k_scale, page_n), vs_n = fetch_scale(p.c.v_scale, page_n);
-            for (int i0 = x.t0; i0 < x.t1; i0 += batch) {
-                const int page = page_n;
-                const float ks = ks_n, vs = vs_n;
-                page_n = fetch_page(i0 + batch);
-                for (int k = 0; k < batch && i0 + k < x.t1; ++k, ++g) {
-                    const int from = (k << shift) + (lane & (ppt - 1));
-                    const int pg = __shfl_sync(0xffffffffu, page, from);
-                    const float tks = __shfl_sync(0xffffffffu, ks, from), tvs = __shfl_sync(0xffffffffu, vs, from);
-                    float top = tvs;
-                    for (int s = 1; s < ppt; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        int seq = 0, g = 0, n = 0;  // slots filled, tiles, parts told
+        auto tell_part = [&](const Part &x) {
+            const int at = n % kParts;
+            if (n >= kParts) wait(&sm.part_empty[at], (n / kParts - 1) & 1);
+            dead = __any_sync(0xffffffffu, dead);
+            if (lane == 0) {
+                sm.part[at] = x;
+                mbar_arrive(&sm.part_full[at]);
+            }
+            ++n;
+        };
+        auto fetch_page = [&](const Part &x, int i0) {
+            const int i = i0 + (lane >> shift);
+            if (i >= x.t1) return -1;
+            const int j = x.tile(i) * kTile + (lane & (ppt - 1)) * bs;
+            if (j >= x.r.len || (j + bs <= x.r.low && j >= x.r.sinks)) return -1;
+            const int page = p.table[(int64_t)x.b * p.ld_table + j / bs];
+            return page < p.c.num_pages ? page : -1;
+        };
+        auto fetch_scale = [&](const float *s, const Part &x, int page) {
+            return page >= 0 ? __ldg(s + (int64_t)page * p.c.num_heads + x.h) : 0.f;
+        };
+        Part x, xn;
+        x.b = xn.b = -1;
+        if (share.u < share.end) xn = next_part(p, share, R);
+        tell_part(xn);
+        int i0 = 0, in = xn.t0, page = -1, page_n = -1;
+        float ks = 0.f, vs = 0.f, ks_n = 0.f, vs_n = 0.f;
+        if (xn.b >= 0) {
+            page_n = fetch_page(xn, in);
+            ks_n = fetch_scale(p.c.k_scale, xn, page_n);
+            vs_n = fetch_scale(p.c.v_scale, xn, page_n);
+        }
+        while (xn.b >= 0 && !dead) {
+            x = xn;
+            i0 = in;
+            page = page_n;
+            ks = ks_n;
+            vs = vs_n;
+            for (int k = 0; k < batch && i0 + k < x.t1 && !dead; ++k, ++g) {
+                const int from = (k << shift) + (lane & (ppt - 1));
+                const int pg = __shfl_sync(0xffffffffu, page, from);
+                const float tks = __shfl_sync(0xffffffffu, ks, from), tvs = __shfl_sync(0xffffffffu, vs, from);
+                float top = tvs;
+                for (int s = 1; s < ppt; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++seq) {
-                        const int slot = seq % NS, turn = seq / NS;
-                        if (turn > 0) wait(&sm.empty[slot], (turn - 1) & 1);
-                        dead = __any_sync(0xffffffffu, dead);
-                        if (dead) break;
-                        if (kv == 0) {
-                            const int n = g % kInfo;
-                            if (lane < ppt) {
-                                sm.ks[n][lane] = tks;
-                                sm.gv[n][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
-                            }
-                            if (lane == 0) sm.wv[n] = top * (1.f / 256.f);
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sm.info_full[n]);
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kSlotBytes);
-                        __syncwarp();
-                        // a page that is not there reads as zeros: past the map's end
-                        if (lane < ppt)
-                            tma_load_4d(sm.ring[slot] + lane * bs * 128, kv ? &vmap : &kmap, 0, 0, x.h,
-                                        pg >= 0 ? pg : p.c.num_pages, &sm.full[slot]);
-                    }
+                for (int kv = 0; kv < 2; ++kv, ++seq) {
+                    const int slot = seq % NS, turn = seq / NS;
+                    if (turn > 0) wait(&sm.empty[slot], (turn - 1) & 1);
+                    dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
-                    if (k == 0) {
-                        ks_n = fetch_scale(p.c.k_scale, page_n);
-                        vs_n = fetch_scale(p.c.v_scale, page_n);
+                    if (kv == 0) {
+                        const int at = g % kInfo;
+                        if (lane < ppt) {
+                            sm.ks[at][lane] = tks;
+                            sm.gv[at][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
+                        }
+                        if (lane == 0) sm.wv[at] = top * (1.f / 256.f);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.info_full[at]);
                     }
+                    if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kSlotBytes);
+                    __syncwarp();
+                    // a page that is not there reads as zeros: past the map's end
+                    if (lane < ppt)
+                        tma_load_4d(sm.ring[slot] + lane * bs * 128, kv ? &vmap : &kmap, 0, 0, x.h,
+                                    pg >= 0 ? pg : p.c.num_pages, &sm.full[slot]);
                 }
-                if (dead) break;
+                if (k == 0) {  // the next batch, of this part or of the next
+                    if (i0 + batch < x.t1) {
+                        in = i0 + batch;
+                    } else {
+                        xn.b = -1;
+                        if (share.u < share.end) xn = next_part(p, share, R);
+                        tell_part(xn);
+                        in = xn.t0;
+                    }
+                    page_n = xn.b >= 0 ? fetch_page(xn, in) : -1;
+                }
+                if (k == min(1, min(batch, x.t1 - i0) - 1)) {
+                    ks_n = fetch_scale(p.c.k_scale, xn, page_n);
+                    vs_n = fetch_scale(p.c.v_scale, xn, page_n);
+                }
             }
         }
     } else if (warp == C::kSoft / 32 + 1) {
@@ -736,9 +864,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
             constexpr uint32_t iqk = fp8_idesc(R, false, false), ipv = fp8_idesc(R, true, true);
             const int ksteps = (p.c.head_dim + 31) / 32;
             const uint32_t ring = smem_addr(sm.ring), q = smem_addr(sm.q), pp = smem_addr(sm.p);
-            int part = 0;
-            auto scores = [&](int g, bool first) {
-                if (first) wait(&sm.q_full, part++ & 1);
+            auto scores = [&](int g) {
                 const int seq = 2 * g, slot = seq % NS;
                 wait(&sm.full[slot], (seq / NS) & 1);
                 if (dead) return;
@@ -767,11 +893,16 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                 mma_commit(&sm.empty[slot]);
             };
             int g = 0;
-            while (share.u < share.end && !dead) {
-                const Part x = next_part(p, share, R);
-                scores(g, true);
-                for (int i = x.t0; i < x.t1; ++i, ++g) {
-                    if (i + 1 < x.t1) scores(g + 1, false);
+            for (int n = 0; !dead; ++n) {
+                const int at = n % kParts;
+                wait(&sm.part_full[at], (n / kParts) & 1);
+                if (dead || sm.part[at].b < 0) break;
+                const int tiles = sm.part[at].t1 - sm.part[at].t0;
+                mbar_arrive(&sm.part_empty[at]);
+                wait(&sm.q_full, n & 1);
+                scores(g);
+                for (int i = 0; i < tiles; ++i, ++g) {
+                    if (i + 1 < tiles) scores(g + 1);
                     values(g);
                 }
             }
@@ -779,37 +910,36 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax and sums
-        const int grp = tid >> 7, t128 = tid & 127, w4 = warp & 3, r0 = grp * NR;
+        const int grp = tid >> 7, t128 = tid & 127, w4 = warp & 3, r0 = grp * NR, D = p.c.head_dim;
         const int bs_shift = 31 - __clz(p.c.page_size), bar = 1 + grp;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        // Every barrier phase is waited for once by a thread, before the arrival of that
+        // thread without which the phase after it cannot end: parities never alias.
+        wait(&sm.part_full[0], 0);
+        Part x = sm.part[0];
         int g = 0;
-        Part x;
-        bool more = share.u < share.end;
-        if (more) {
-            x = next_part(p, share, R);
+        if (x.b >= 0) {
             load_queries<R>(p, x, sm, tid, 0);
             named_sync<C::kSoft>(3);
         }
-        for (int parity = 0; more; parity ^= 1) {
+        for (int n = 0; x.b >= 0; ++n) {
             float acc[NR], l[NR];
-            float m_run = kNegInf;  // thread r of the group: row r's running reference
+            float m_run = kNegInf;  // lane r: row r's running reference
+            bool moved = false, moved_last = false;
 #pragma unroll
             for (int r = 0; r < NR; ++r) acc[r] = l[r] = 0.f;
-            auto add_values = [&](int gg) {  // O^T of tile gg into the sums
-                const int buf = gg & 1;
-                wait(&sm.o_full, gg & 1);
+            auto add_values = [&](int gg, bool rescale) {  // O^T of tile gg into the sums
                 tc_fence_after();
                 uint32_t o[NR];
-                tmem_ld<NR>(tO + buf * R + r0 + lanes, o);
-                bool moved = sm.moved[buf][2 * grp] != 0;
+                tmem_ld<NR>(tO + (gg & 1) * R + r0 + lanes, o);
                 tmem_wait_ld();
-                if (moved) {
+                if (rescale) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) acc[r] *= sm.alpha[buf][r0 + r];
+                    for (int r = 0; r < NR; ++r) acc[r] *= sm.alpha[warp][gg & 1][r];
                 }
 #pragma unroll
                 for (int r = 0; r < NR; r += 4) {
-                    const float4 f = *(const float4 *)&sm.w[buf][r0 + r];
+                    const float4 f = *(const float4 *)&sm.w[warp][gg & 1][r];
                     float2 a = make_float2(acc[r], acc[r + 1]), b = make_float2(acc[r + 2], acc[r + 3]);
                     a = ffma2(make_float2(__uint_as_float(o[r]), __uint_as_float(o[r + 1])), make_float2(f.x, f.y), a);
                     b = ffma2(make_float2(__uint_as_float(o[r + 2]), __uint_as_float(o[r + 3])), make_float2(f.z, f.w), b);
@@ -821,6 +951,10 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
             };
             for (int i = x.t0; i < x.t1; ++i, ++g) {
                 const int buf = g & 1, inf = g % kInfo, j0 = x.tile(i) * kTile, j = j0 + t128;
+                if (i + 1 == x.t1) {
+                    wait(&sm.part_full[(n + 1) % kParts], ((n + 1) / kParts) & 1);
+                    if (sm.part[(n + 1) % kParts].b >= 0) touch_queries<R>(p, sm.part[(n + 1) % kParts], tid);
+                }
                 wait(&sm.info_full[inf], (g / kInfo) & 1);
                 const float ks = sm.ks[inf][t128 >> bs_shift], gv = sm.gv[inf][t128 >> bs_shift], wv = sm.wv[inf];
                 wait(&sm.s_full[buf], (g >> 1) & 1);
@@ -835,20 +969,17 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     v[r] = f.x;
                     v[r + 1] = f.y;
                 }
-                // every row of the tile sees every token of it, or not
-                const bool masked = j0 + kTile - 1 > x.pos0 ||
-                                    (p.window > 0 && j0 <= x.pos1 - p.window && j0 + kTile > p.sinks);
-                uint32_t sees = 0xffffffffu;
-                bool spoilt = false;
-                if (masked) {
-                    sees = 0;
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        const int at = sm.pos[r0 + r];
-                        const bool see = j <= at && (p.window == 0 || j > at - p.window || j < p.sinks);
-                        sees |= see ? 1u << r : 0u;
-                        v[r] = see ? v[r] : kNegInf;
-                    }
+                if (j0 + kTile - 1 > x.pos0 || (p.window > 0 && j0 <= x.pos1 - p.window && j0 + kTile > p.sinks)) {
+                    // Some row does not see some token of the tile.  Rows are token-major,
+                    // so the rows that see token j are an interval: from the first at a
+                    // position >= j to the last at a position < j + window.
+                    const int first = x.r.len - x.r.n, base = x.rt * R + r0;
+                    const int lo = j - first <= 0 ? 0 : (j - first >= x.r.n ? NR : min(NR, max(0, (j - first) * p.group - base)));
+                    int hi = min(NR, max(0, x.nrows - r0));
+                    if (p.window > 0 && j >= p.sinks && j - first + p.window < x.r.n)
+                        hi = min(hi, max(0, (j - first + p.window) * p.group - base));
+                    const uint32_t below_hi = hi >= 32 ? 0xffffffffu : (1u << hi) - 1;
+                    const uint32_t sees = lo >= hi ? 0u : below_hi & ~((1u << lo) - 1);
                     // 0 times a NaN is a NaN: a value row that some rows do not see is
                     // cleared if no row sees it, or if it holds a NaN, which then
                     // reaches the rows that see it through their probability
@@ -857,6 +988,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     const int slot = (2 * g + 1) % NS;
                     wait(&sm.full[slot], ((2 * g + 1) / NS) & 1);
                     uint4 *row = (uint4 *)(sm.ring[slot] + t128 * 128);
+                    bool spoilt = false;
                     if (any && !all) {
                         uint32_t nan = 0;
 #pragma unroll
@@ -875,112 +1007,104 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                         for (int c = 0; c < 8; ++c) row[(c + lane) & 7] = make_uint4(0, 0, 0, 0);
                     }
                     __syncwarp();
-                }
-                // the tile's largest score of every row
-                float top = kNegInf;
+                    const float put = spoilt ? __int_as_float(0x7fffffff) : 0.f;
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const float mr = redux_max(v[r]);
-                    if ((lane & (NR - 1)) == r) top = mr;
+                    for (int r = 0; r < NR; ++r) v[r] = (sees >> r) & 1 ? v[r] + put : kNegInf;
                 }
-                if (lane < NR) sm.red[w4][r0 + lane] = top;
+                // the tile's largest score of every row: over the warp, then over the four
+                // warps, which each keep the rows' references for themselves (lane = row)
+#pragma unroll
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 f = make_float4(redux_max(v[r]), redux_max(v[r + 1]), redux_max(v[r + 2]), redux_max(v[r + 3]));
+                    if (lane == 0) *(float4 *)&sm.red[buf][w4][r0 + r] = f;
+                }
                 named_sync<128>(bar);
-                if (w4 == 0) {
-                    const int r = r0 + (lane & (NR - 1));
-                    float mt = fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]), fmaxf(sm.red[2][r], sm.red[3][r]));
+                {
+                    const int k = lane & (NR - 1), r = r0 + k;
+                    const float mt = fmaxf(fmaxf(sm.red[buf][0][r], sm.red[buf][1][r]), fmaxf(sm.red[buf][2][r], sm.red[buf][3][r]));
                     const float c = sm.c[r];
                     const bool some = mt > kNegInf;
                     const float ref = some ? mt * c : 0.f, mm = some ? ref : kNegInf;
-                    float alpha = 1.f;
                     const bool moves = mm > m_run + kRefStep;  // also from -inf
+                    moved_last = moved;
+                    moved = __any_sync(0xffffffffu, moves);
+                    float alpha = 1.f;
                     if (moves) {
                         alpha = m_run == kNegInf ? 0.f : ex2_approx(m_run - mm);
                         m_run = mm;
                     }
                     const float beta = some ? ex2_approx(mm - m_run) : 1.f;
-                    const bool any_moves = __any_sync(0xffffffffu, moves);
                     if (lane < NR) {
-                        float *cm = (float *)&sm.cm[buf][r >> 1];
-                        cm[r & 1] = c;
-                        cm[2 + (r & 1)] = -ref;
-                        sm.beta[buf][r] = beta;
-                        sm.w[buf][r] = beta * wv;
-                        sm.alpha[buf][r] = alpha;
+                        float *cm = (float *)&sm.cm[warp][buf][k >> 1];
+                        cm[k & 1] = c;
+                        cm[2 + (k & 1)] = -ref;
+                        sm.beta[warp][buf][k] = beta;
+                        sm.w[warp][buf][k] = beta * wv;
+                        sm.alpha[warp][buf][k] = alpha;
                     }
-                    if (lane == 0) sm.moved[buf][2 * grp] = any_moves;
+                    __syncwarp();
                 }
-                named_sync<128>(bar);
-                if (sm.moved[buf][2 * grp]) {
+                if (moved) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) l[r] *= sm.alpha[buf][r0 + r];
+                    for (int r = 0; r < NR; ++r) l[r] *= sm.alpha[warp][buf][r];
                 }
-                uint32_t hi[NR / 4], lo[NR / 4];
+                uint32_t first[NR / 4], rest[NR / 4];
                 const float2 gv2 = make_float2(gv, gv);
 #pragma unroll
                 for (int r = 0; r < NR; r += 4) {
-                    const float4 b = *(const float4 *)&sm.beta[buf][r0 + r];
-                    uint32_t h2[2], l2[2];
+                    const float4 b = *(const float4 *)&sm.beta[warp][buf][r];
+                    float2 z[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int k = r + 2 * e;
-                        const float4 f = sm.cm[buf][(r0 + k) >> 1];
-                        float2 z = ffma2(make_float2(v[k], v[k + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
-                        z.x = ex2_approx(z.x);
-                        z.y = ex2_approx(z.y);
-                        if (masked) {
-                            const float nan = __int_as_float(0x7fffffff);
-                            z.x = (sees >> k) & 1 ? (spoilt ? nan : z.x) : 0.f;
-                            z.y = (sees >> (k + 1)) & 1 ? (spoilt ? nan : z.y) : 0.f;
-                        }
-                        const float2 ll = ffma2(z, e ? make_float2(b.z, b.w) : make_float2(b.x, b.y), make_float2(l[k], l[k + 1]));
+                        const float4 f = sm.cm[warp][buf][k >> 1];
+                        z[e] = ffma2(make_float2(v[k], v[k + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
+                        z[e].x = ex2_approx(z[e].x);
+                        z[e].y = ex2_approx(z[e].y);
+                        const float2 ll = ffma2(z[e], e ? make_float2(b.z, b.w) : make_float2(b.x, b.y), make_float2(l[k], l[k + 1]));
                         l[k] = ll.x;
                         l[k + 1] = ll.y;
-                        z = fmul2(z, gv2);
-                        split_e4m3x2(z.x, z.y, h2[e], l2[e]);
+                        z[e] = fmul2(z[e], gv2);
                     }
-                    hi[r / 4] = h2[0] | (h2[1] << 16);
-                    lo[r / 4] = l2[0] | (l2[1] << 16);
+                    split_e4m3x4(z[0], z[1], first[r / 4], rest[r / 4]);
                 }
                 if (i > x.t0) wait(&sm.o_full, (g - 1) & 1);  // the last tile's product has read P
 #pragma unroll
                 for (int k = 0; k < NR / 16; ++k) {
-                    *(uint4 *)(sm.p[0][r0 / 16 + k] + t128 * 16) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                    *(uint4 *)(sm.p[1][r0 / 16 + k] + t128 * 16) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                    *(uint4 *)(sm.p[0][r0 / 16 + k] + t128 * 16) = make_uint4(first[4 * k], first[4 * k + 1], first[4 * k + 2], first[4 * k + 3]);
+                    *(uint4 *)(sm.p[1][r0 / 16 + k] + t128 * 16) = make_uint4(rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
                 }
                 fence_async_shared();
                 tc_fence_before();
                 mbar_arrive(&sm.p_full);
-                if (i > x.t0) add_values(g - 1);
+                if (i > x.t0) add_values(g - 1, moved_last);
             }
             // the next part's queries go out before this part's last product is waited for
             const Part done = x;
-            more = share.u < share.end;
-            named_sync<C::kSoft>(3);
-            if (more) {
-                x = next_part(p, share, R);
-                load_queries<R>(p, x, sm, tid, parity ^ 1);
-            }
-            add_values(g - 1);
+            x = sm.part[(n + 1) % kParts];  // waited for at the last tile
+            named_sync<C::kSoft>(3);  // every warp has the last scores: the queries may go
+            if (x.b >= 0) load_queries<R>(p, x, sm, tid, (n + 1) & 1);
+            wait(&sm.o_full, (g - 1) & 1);
+            add_values(g - 1, moved);
             tc_fence_before();
             const float lt = warp_sum_scatter<NR>(l, lane);
-            if (lane < NR) sm.red[w4][r0 + lane] = lt;
+            if (lane < NR) sm.red[0][w4][r0 + lane] = lt;
             named_sync<128>(bar);
             if (w4 == 0 && lane < NR) {
                 const int r = r0 + lane;
+                const float sum = sm.red[0][0][r] + sm.red[0][1][r] + sm.red[0][2][r] + sm.red[0][3][r];
                 sm.m[r] = m_run;
-                sm.l[r] = sm.red[0][r] + sm.red[1][r] + sm.red[2][r] + sm.red[3][r];
+                sm.l[r] = done.whole ? inverse_sum(sum) : sum;
+                if (p.lse && done.whole && r < done.nrows) store_lse(p, done, done.rt * R + r, m_run, sum);
             }
             named_sync<128>(bar);
             if (dead) p.status[done.b] = SPEC_STATUS_INTERNAL;
-            const int D = p.c.head_dim;
             if (done.whole) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
                     if (r0 + r < done.nrows && t128 < D)
-                        ((uint16_t *)p.out)[(int64_t)sm.orow[parity][r0 + r] * D + t128] =
-                            (uint16_t)pack_bf16x2(acc[r] * inverse_sum(sm.l[r0 + r]), 0.f);
-                if (p.lse && t128 < NR && r0 + t128 < done.nrows)
-                    store_lse(p, done, done.rt * R + r0 + t128, sm.m[r0 + t128], sm.l[r0 + t128]);
+                        ((uint16_t *)p.out)[(int64_t)sm.orow[n & 1][r0 + r] * D + t128] =
+                            (uint16_t)pack_bf16x2(acc[r] * sm.l[r0 + r], 0.f);
             } else {
                 float *slot = slot_of(p, blockIdx.x, done.t0 == 0, R);
 #pragma unroll
@@ -990,11 +1114,10 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     slot[R * D + r0 + t128] = sm.m[r0 + t128];
                     slot[R * D + R + r0 + t128] = sm.l[r0 + t128];
                 }
-                const int c0 = cta_of(share.total, done.item, share.ctas);
-                const int c1 = cta_of(share.total, done.item + done.r.nt - 1, share.ctas);
-                if (arrive_last<C::kSoft>(p, c0, c1 - c0 + 1, &sm.flag, 3))
-                    join_parts<uint16_t, C::kSoft>(p, done, R, done.nrows, c0, c1, sm.join, 3);
+                if (arrive_last<C::kSoft>(p, done.c0, done.c1 - done.c0 + 1, &sm.flag, 3))
+                    join_parts<uint16_t, C::kSoft, R>(p, done, sm.join, 3);
             }
+            if (tid == 0) mbar_arrive(&sm.part_empty[n % kParts]);
         }
     }
     tc_fence_before();

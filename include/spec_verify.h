@@ -443,7 +443,7 @@ int spec_kv_gather(const spec_kv_cache *cache, int B, const int32_t *cu_out, int
  *              elements apart
  *  n_tokens    rows of q, out and out_lse; max_query a bound on every n_b
  *  scale       positive and finite; window >= 0; sinks >= 0 (unused when window == 0)
- *  out         [n_tokens, num_query_heads, head_dim] of type dtype
+ *  out         [n_tokens, num_query_heads, head_dim] of type dtype, 16-byte aligned
  *  out_lse     [n_tokens, num_query_heads] float, or NULL
  *  out_status  [B]: 0, SPEC_STATUS_BAD_LENGTH, SPEC_STATUS_BAD_PAGE or
  *              SPEC_STATUS_INTERNAL; rows of a failed request are unspecified

@@ -77,9 +77,10 @@ __device__ __forceinline__ int64_t request_tiles(const AttnParams &p, const Requ
 }
 
 // a / b for a >= 0, b > 0: most quotients here fit 32 bits, where a division is short.
+__device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-    return a / b;
+    return quotient64(a, b);
 }
 
 // A CTA's place on the line of tiles: [u, end), starting `off` tiles into request b.
@@ -100,7 +101,7 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t u, int ctas) {
 
 // Every thread of the CTA calls it (it synchronises); NT threads.
 template <int NT>
-__device__ Share find_share(const AttnParams &p, int rows) {
+__device__ __noinline__ Share find_share(const AttnParams &p, int rows) {
     __shared__ int64_t s_warp[NT / 32];
     __shared__ Share s_share;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -156,7 +157,7 @@ struct Part {
 };
 
 // The share's next part; call while s.u < s.end.
-__device__ __forceinline__ Part next_part(const AttnParams &p, Share &s, int rows) {
+__device__ __noinline__ Part next_part(const AttnParams &p, Share &s, int rows) {
     Part x;
     for (;;) {
         x.r = load_request(p, s.b, rows);
@@ -192,7 +193,7 @@ __device__ __forceinline__ Part next_part(const AttnParams &p, Share &s, int row
 }
 
 // Lengths and pages of the requests, told by one warp for every gridDim.x-th request.
-__device__ __forceinline__ void write_statuses(const AttnParams &p, int lane) {
+__device__ __noinline__ void write_statuses(const AttnParams &p, int lane) {
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const Request r = load_request(p, b, 1);
         bool bad = false;
@@ -210,6 +211,11 @@ __device__ __forceinline__ void write_statuses(const AttnParams &p, int lane) {
 }
 
 // ------------------------------------------------------------------ joining parts
+template <int NT>
+__device__ __forceinline__ void named_sync(int bar) {
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
+}
+
 // A part's slot: the first part of an item is its CTA's last part, every other part
 // its CTA's first, so two slots a CTA are enough.
 __device__ __forceinline__ float *slot_of(const AttnParams &p, int cta, bool first, int rows) {
@@ -235,107 +241,122 @@ __device__ __forceinline__ float weight_of(float a, float m) { return a == kNegI
 
 // Counts this CTA's part of a cut item in; true (in every thread) for the part that
 // arrives last, which may then read the other parts.  NT threads call it, `bar` a
-// named barrier of theirs.
+// named barrier of theirs; the barrier orders their stores before thread 0's fence.
 template <int NT>
 __device__ __forceinline__ bool arrive_last(const AttnParams &p, int first_cta, int parts, int *s_flag, int bar) {
-    __threadfence();
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
+    named_sync<NT>(bar);
     if (threadIdx.x == 0) {
+        __threadfence();
         const int before = atomicAdd(p.tickets + first_cta, 1);
         *s_flag = before == parts - 1;
         if (before == parts - 1) p.tickets[first_cta] = 0;  // for the next call
+        __threadfence();
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
-    const bool last = *s_flag != 0;
-    if (last) __threadfence();
-    return last;
+    named_sync<NT>(bar);
+    return *s_flag != 0;
 }
 
-// Joins the parts of an item in CTA order and writes its rows.  The weights of up to
-// kJoin parts at a time are laid out first, so that the sums' loads, four columns a
-// thread, depend on nothing and are in flight together.
+// Joins the parts of an item in CTA order and writes its rows, kJoin parts at a time:
+// a thread a row finds their weights (rescaling what is there where the reference
+// rises), then a warp takes rows, four columns a lane, with several parts' loads in
+// flight.  ND: 128-column blocks of the head.
 constexpr int kJoin = 16;
 template <int R>
 struct JoinSpace {
-    float m[R], l[R];
-    float w[kJoin][R];
+    float keep[R], w[kJoin][R];
 };
 
-template <typename T, int NT, int R>
-__device__ void join_parts(const AttnParams &p, const Part &x, JoinSpace<R> &sp, int bar) {
-    const int D = p.c.head_dim, tid = threadIdx.x, nrows = x.nrows, parts = x.c1 - x.c0 + 1;
-    if (tid < nrows) {
-        float m = kNegInf, l = 0.f;
-        for (int i0 = 0; i0 < parts; i0 += 8) {
-            float mc[8], lc[8];
+template <typename T, int NT, int R, int ND>
+__device__ __noinline__ void join_parts(const AttnParams &p, const Part &x, JoinSpace<R> &sp, int bar) {
+    constexpr int kWarps = NT / 32, kRows = (R + kWarps - 1) / kWarps;  // rows a warp
+    const int D = p.c.head_dim, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nrows = x.nrows;
+    const int parts = x.c1 - x.c0 + 1;
+    const int64_t stride = 2 * (int64_t)R * (D + 2);  // from a CTA's slot to the next one's
+    const float *slot0 = slot_of(p, x.c0, true, R), *slots = slot_of(p, x.c0, false, R);  // part 0; part c at c * stride
+    float m = kNegInf, l = 0.f;
+    float4 o[kRows][ND];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float *s = slot_of(p, x.c0 + min(i0 + k, parts - 1), i0 + k == 0, R) + (int64_t)R * D + tid;
-                mc[k] = i0 + k < parts ? __ldcg(s) : kNegInf;
-                lc[k] = i0 + k < parts ? __ldcg(s + R) : 0.f;
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+        for (int n = 0; n < ND; ++n) o[k][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += kJoin) {
+        const int here = min(kJoin, parts - i0);
+        if (tid < nrows) {
+            float mc[kJoin], lc[kJoin];
+            float top = m;
+#pragma unroll
+            for (int c = 0; c < kJoin; ++c) {
+                const float *s = (i0 + c == 0 ? slot0 : slots + (i0 + c) * stride) + R * D + tid;
+                mc[c] = c < here ? __ldcg(s) : kNegInf;
+                lc[c] = c < here ? __ldcg(s + R) : 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float mn = fmaxf(m, mc[k]);
-                l = l * weight_of(m, mn) + lc[k] * weight_of(mc[k], mn);
-                m = mn;
+            for (int c = 0; c < kJoin; ++c) top = fmaxf(top, mc[c]);
+            const float keep = weight_of(m, top);
+            sp.keep[tid] = keep;
+            l *= keep;
+#pragma unroll
+            for (int c = 0; c < kJoin; ++c) {
+                const float w = weight_of(mc[c], top);
+                sp.w[c][tid] = w;
+                l = fmaf(lc[c], w, l);
+            }
+            m = top;
+        }
+        named_sync<NT>(bar);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int r = k * kWarps + warp;
+            if (r >= nrows) break;
+            const float keep = sp.keep[r];
+#pragma unroll
+            for (int n = 0; n < ND; ++n) {
+                const int d = 128 * n + 4 * lane;
+                if (d >= D) break;
+                float4 a = o[k][n];
+                a.x *= keep;
+                a.y *= keep;
+                a.z *= keep;
+                a.w *= keep;
+#pragma unroll 8
+                for (int c = 0; c < here; ++c) {
+                    const float4 v = __ldcg((const float4 *)((i0 + c == 0 ? slot0 : slots + (i0 + c) * stride) + r * D + d));
+                    const float w = sp.w[c][r];
+                    a.x = fmaf(v.x, w, a.x);
+                    a.y = fmaf(v.y, w, a.y);
+                    a.z = fmaf(v.z, w, a.z);
+                    a.w = fmaf(v.w, w, a.w);
+                }
+                o[k][n] = a;
             }
         }
-        sp.m[tid] = m;
-        sp.l[tid] = inverse_sum(l);
+        named_sync<NT>(bar);
+    }
+    if (tid < nrows) {
+        sp.keep[tid] = inverse_sum(l);
         if (p.lse) store_lse(p, x, x.rt * R + tid, m, l);
     }
-    const int groups = D / 4, step = NT / 32;  // a warp a row, four columns a lane
-    for (int base = 0; base < nrows; base += 4 * step) {
-        float4 o[4][2];
+    named_sync<NT>(bar);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k][0] = o[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < parts; i0 += kJoin) {
-            asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
-            for (int i = tid; i < kJoin * nrows; i += NT) {
-                const int c = i / nrows, r = i - c * nrows;
-                if (i0 + c < parts)
-                    sp.w[c][r] = weight_of(__ldcg(slot_of(p, x.c0 + i0 + c, i0 + c == 0, R) + (int64_t)R * D + r), sp.m[r]);
-            }
-            asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
-#pragma unroll 4
-            for (int c = 0; c < min(kJoin, parts - i0); ++c) {
-                const float4 *s = (const float4 *)slot_of(p, x.c0 + i0 + c, i0 + c == 0, R);
+    for (int k = 0; k < kRows; ++k) {
+        const int r = k * kWarps + warp;
+        if (r >= nrows) break;
+        const float inv = sp.keep[r];
+        const int row = x.rt * R + r, t = row / p.group, g = row - t * p.group;
+        const int64_t at = ((int64_t)(x.r.row0 + t) * p.Hq + x.h * p.group + g) * D;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = base + k * step + (tid >> 5);
-                    if (r >= nrows) continue;
-                    const float w = sp.w[c][r];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int d = n * 32 + (tid & 31);
-                        if (d >= groups) continue;
-                        const float4 v = __ldcg(s + r * groups + d);
-                        o[k][n].x = fmaf(v.x, w, o[k][n].x);
-                        o[k][n].y = fmaf(v.y, w, o[k][n].y);
-                        o[k][n].z = fmaf(v.z, w, o[k][n].z);
-                        o[k][n].w = fmaf(v.w, w, o[k][n].w);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = base + k * step + (tid >> 5);
-            if (r >= nrows) continue;
-            const float inv = sp.l[r];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int d = n * 32 + (tid & 31);
-                if (d >= groups) continue;
-                store_out<T>(p, x, x.rt * R + r, 4 * d, o[k][n].x * inv);
-                store_out<T>(p, x, x.rt * R + r, 4 * d + 1, o[k][n].y * inv);
-                store_out<T>(p, x, x.rt * R + r, 4 * d + 2, o[k][n].z * inv);
-                store_out<T>(p, x, x.rt * R + r, 4 * d + 3, o[k][n].w * inv);
+        for (int n = 0; n < ND; ++n) {
+            const int d = 128 * n + 4 * lane;
+            if (d >= D) break;
+            const float4 v = make_float4(o[k][n].x * inv, o[k][n].y * inv, o[k][n].z * inv, o[k][n].w * inv);
+            if constexpr (sizeof(T) == 2) {
+                *(uint2 *)((uint16_t *)p.out + at + d) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            } else {
+                *(float4 *)((float *)p.out + at + d) = v;
             }
         }
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
+    named_sync<NT>(bar);
 }
 
 // ------------------------------------------------------------------ fp32 arithmetic kernel
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
                 slot[R * D + R + tid] = s_w[R + tid];
             }
             if (arrive_last<kSimtThreads>(p, x.c0, x.c1 - x.c0 + 1, &s_flag, 1))
-                join_parts<T, kSimtThreads, R>(p, x, s_join, 1);
+                join_parts<T, kSimtThreads, R, ND>(p, x, s_join, 1);
         }
     }
 }
@@ -594,14 +615,28 @@ __device__ __forceinline__ void split_e4m3x4(float2 x, float2 y, uint32_t &first
         : "r"(first));
     rest = half4_to_e4m3x4(half2_sub(a, c), half2_sub(b, d));  // exact before the rounding
 }
-template <int NT>
-__device__ __forceinline__ void named_sync(int bar) {
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
+// Waits for the phase of the given parity; false after kWaitNs.  These waits are a few
+// hundred cycles long and on the path of every tile, so the thread polls: one that
+// sleeps in the barrier is woken late.
+__device__ __forceinline__ bool poll_barrier(uint64_t *bar, int parity) {
+    uint64_t t0 = 0;
+    for (uint32_t n = 0;; ++n) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done)
+                     : "r"(smem_addr(bar)), "r"((uint32_t)parity)
+                     : "memory");
+        if (done) return true;
+        if ((n & 255) == 255) {
+            const uint64_t t = global_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitNs) return false;
+        }
+    }
 }
-
 template <int R>
 struct TcShape {
-    static constexpr int kRowsG = R < 32 ? R : 32;        // rows of a softmax group
+    static constexpr int kRowsG = 16;                     // rows of a softmax group
     static constexpr int kGroups = R / kRowsG;            // groups of 128 threads
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
     static constexpr int kThreads = kSoft + 64;
@@ -611,6 +646,7 @@ struct TcShape {
 };
 
 constexpr int kParts = 4;  // parts known ahead
+constexpr int kAllBar = 8, kLookBar = 9;  // named barriers of all softmax threads; group g's is 1 + g
 
 template <int R>
 struct TcShared {
@@ -668,7 +704,7 @@ __device__ __forceinline__ void touch_queries(const AttnParams &p, const Part &x
 
 // The queries of a part as two e4m3 terms, 128 / kRowsG threads a row.
 template <int R>
-__device__ __forceinline__ void load_queries(const AttnParams &p, const Part &x, TcShared<R> &sm, int tid, int parity) {
+__device__ __noinline__ void load_queries(const AttnParams &p, const Part &x, TcShared<R> &sm, int tid, int parity) {
     using C = TcShape<R>;
     constexpr int kCols = C::kRowsG;            // 128 columns over 128 / kRowsG threads
     constexpr int TPR = 128 / C::kRowsG;
@@ -729,7 +765,8 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Part &x,
         sm.orow[parity][row] = orow;
     }
     fence_async_shared();
-    mbar_arrive(&sm.q_full);
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(&sm.q_full);
 }
 
 template <int R>
@@ -739,7 +776,8 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
     constexpr int NR = C::kRowsG, NS = C::kSlots;
     extern __shared__ uint8_t raw[];
     TcShared<R> &sm = *reinterpret_cast<TcShared<R> *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the warp's: roles branch on it
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sm.full[i], 1);
@@ -748,12 +786,12 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         for (int i = 0; i < kInfo; ++i) mbar_init(&sm.info_full[i], 1);
         mbar_init(&sm.s_full[0], 1);
         mbar_init(&sm.s_full[1], 1);
-        mbar_init(&sm.p_full, C::kSoft);
+        mbar_init(&sm.p_full, C::kSoft / 32);
         mbar_init(&sm.o_full, 1);
-        mbar_init(&sm.q_full, C::kSoft);
+        mbar_init(&sm.q_full, C::kSoft / 32);
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sm.part_full[i], 1);
-            mbar_init(&sm.part_empty[i], 2);
+            mbar_init(&sm.part_empty[i], 1 + C::kSoft / 32);
         }
         mbar_init_fence();
     }
@@ -764,6 +802,9 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
     const uint32_t tm = sm.tmem, tS = tm, tO = tm + 2 * R;
     bool dead = false;  // a wait ran out: wait no more, finish, report
     auto wait = [&](uint64_t *bar, int parity) {
+        if (!dead && !poll_barrier(bar, parity)) dead = true;
+    };
+    auto wait_long = [&](uint64_t *bar, int parity) {
         if (!dead && !mbar_wait(bar, parity, kWaitNs)) dead = true;
     };
 
@@ -820,7 +861,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++seq) {
                     const int slot = seq % NS, turn = seq / NS;
-                    if (turn > 0) wait(&sm.empty[slot], (turn - 1) & 1);
+                    if (turn > 0) wait_long(&sm.empty[slot], (turn - 1) & 1);
                     dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
                     if (kv == 0) {
@@ -916,13 +957,14 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         // Every barrier phase is waited for once by a thread, before the arrival of that
         // thread without which the phase after it cannot end: parities never alias.
         wait(&sm.part_full[0], 0);
-        Part x = sm.part[0];
         int g = 0;
-        if (x.b >= 0) {
-            load_queries<R>(p, x, sm, tid, 0);
-            named_sync<C::kSoft>(3);
+        if (sm.part[0].b >= 0) {
+            load_queries<R>(p, sm.part[0], sm, tid, 0);
+            named_sync<C::kSoft>(kAllBar);
         }
-        for (int n = 0; x.b >= 0; ++n) {
+        for (int n = 0; sm.part[n % kParts].b >= 0; ++n) {
+            const Part &x = sm.part[n % kParts], &next = sm.part[(n + 1) % kParts];
+            const int t0 = x.t0, t1 = x.t1;
             float acc[NR], l[NR];
             float m_run = kNegInf;  // lane r: row r's running reference
             bool moved = false, moved_last = false;
@@ -949,11 +991,11 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     acc[r + 3] = b.y;
                 }
             };
-            for (int i = x.t0; i < x.t1; ++i, ++g) {
+            for (int i = t0; i < t1; ++i, ++g) {
                 const int buf = g & 1, inf = g % kInfo, j0 = x.tile(i) * kTile, j = j0 + t128;
-                if (i + 1 == x.t1) {
+                if (i + 1 == t1) {
                     wait(&sm.part_full[(n + 1) % kParts], ((n + 1) / kParts) & 1);
-                    if (sm.part[(n + 1) % kParts].b >= 0) touch_queries<R>(p, sm.part[(n + 1) % kParts], tid);
+                    if (next.b >= 0) touch_queries<R>(p, next, tid);
                 }
                 wait(&sm.info_full[inf], (g / kInfo) & 1);
                 const float ks = sm.ks[inf][t128 >> bs_shift], gv = sm.gv[inf][t128 >> bs_shift], wv = sm.wv[inf];
@@ -1001,7 +1043,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     }
                     __syncwarp();
                     // one group clears; with two, both have looked before it does
-                    if constexpr (C::kGroups > 1) named_sync<C::kSoft>(4);
+                    if constexpr (C::kGroups > 1) named_sync<C::kSoft>(kLookBar);
                     if ((!any || spoilt) && grp == 0) {
 #pragma unroll
                         for (int c = 0; c < 8; ++c) row[(c + lane) & 7] = make_uint4(0, 0, 0, 0);
@@ -1068,7 +1110,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     }
                     split_e4m3x4(z[0], z[1], first[r / 4], rest[r / 4]);
                 }
-                if (i > x.t0) wait(&sm.o_full, (g - 1) & 1);  // the last tile's product has read P
+                if (i > t0) wait(&sm.o_full, (g - 1) & 1);  // the last tile's product has read P
 #pragma unroll
                 for (int k = 0; k < NR / 16; ++k) {
                     *(uint4 *)(sm.p[0][r0 / 16 + k] + t128 * 16) = make_uint4(first[4 * k], first[4 * k + 1], first[4 * k + 2], first[4 * k + 3]);
@@ -1076,14 +1118,14 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                 }
                 fence_async_shared();
                 tc_fence_before();
-                mbar_arrive(&sm.p_full);
-                if (i > x.t0) add_values(g - 1, moved_last);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full);
+                if (i > t0) add_values(g - 1, moved_last);
             }
-            // the next part's queries go out before this part's last product is waited for
-            const Part done = x;
-            x = sm.part[(n + 1) % kParts];  // waited for at the last tile
-            named_sync<C::kSoft>(3);  // every warp has the last scores: the queries may go
-            if (x.b >= 0) load_queries<R>(p, x, sm, tid, (n + 1) & 1);
+            // the next part (told before the last tile) sends its queries before this part's
+            // last product is waited for
+            named_sync<C::kSoft>(kAllBar);  // every warp has the last scores: the queries may go
+            if (next.b >= 0) load_queries<R>(p, next, sm, tid, (n + 1) & 1);
             wait(&sm.o_full, (g - 1) & 1);
             add_values(g - 1, moved);
             tc_fence_before();
@@ -1094,30 +1136,31 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                 const int r = r0 + lane;
                 const float sum = sm.red[0][0][r] + sm.red[0][1][r] + sm.red[0][2][r] + sm.red[0][3][r];
                 sm.m[r] = m_run;
-                sm.l[r] = done.whole ? inverse_sum(sum) : sum;
-                if (p.lse && done.whole && r < done.nrows) store_lse(p, done, done.rt * R + r, m_run, sum);
+                sm.l[r] = x.whole ? inverse_sum(sum) : sum;
+                if (p.lse && x.whole && r < x.nrows) store_lse(p, x, x.rt * R + r, m_run, sum);
             }
             named_sync<128>(bar);
-            if (dead) p.status[done.b] = SPEC_STATUS_INTERNAL;
-            if (done.whole) {
+            if (dead) p.status[x.b] = SPEC_STATUS_INTERNAL;
+            if (x.whole) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
-                    if (r0 + r < done.nrows && t128 < D)
+                    if (r0 + r < x.nrows && t128 < D)
                         ((uint16_t *)p.out)[(int64_t)sm.orow[n & 1][r0 + r] * D + t128] =
                             (uint16_t)pack_bf16x2(acc[r] * sm.l[r0 + r], 0.f);
             } else {
-                float *slot = slot_of(p, blockIdx.x, done.t0 == 0, R);
+                float *slot = slot_of(p, blockIdx.x, x.t0 == 0, R);
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
-                    if (r0 + r < done.nrows && t128 < D) slot[(r0 + r) * D + t128] = acc[r];
-                if (t128 < NR && r0 + t128 < done.nrows) {
+                    if (r0 + r < x.nrows && t128 < D) slot[(r0 + r) * D + t128] = acc[r];
+                if (t128 < NR && r0 + t128 < x.nrows) {
                     slot[R * D + r0 + t128] = sm.m[r0 + t128];
                     slot[R * D + R + r0 + t128] = sm.l[r0 + t128];
                 }
-                if (arrive_last<C::kSoft>(p, done.c0, done.c1 - done.c0 + 1, &sm.flag, 3))
-                    join_parts<uint16_t, C::kSoft, R>(p, done, sm.join, 3);
+                if (arrive_last<C::kSoft>(p, x.c0, x.c1 - x.c0 + 1, &sm.flag, kAllBar))
+                    join_parts<uint16_t, C::kSoft, R, 1>(p, x, sm.join, kAllBar);
             }
-            if (tid == 0) mbar_arrive(&sm.part_empty[n % kParts]);
+            __syncwarp();  // this warp reads the part no more
+            if (lane == 0) mbar_arrive(&sm.part_empty[n % kParts]);
         }
     }
     tc_fence_before();
@@ -1203,7 +1246,7 @@ extern "C" int spec_cache_attention(const spec_kv_cache *cache, const void *q, i
     if (!cu_query || !seq_len || !out_status || (ld_table > 0 && !page_table)) return SPEC_EINVAL;
     const int esz = dtype == SPEC_BF16 ? 2 : 4;
     if (n_tokens > 0 && (!q || !out || ld_q < (int64_t)num_query_heads * cache->head_dim)) return SPEC_EINVAL;
-    if (((uintptr_t)q % esz) || ((uintptr_t)out % esz) || ((uintptr_t)out_lse & 3)) return SPEC_EINVAL;
+    if (((uintptr_t)q % esz) || ((uintptr_t)out & 15) || ((uintptr_t)out_lse & 3)) return SPEC_EINVAL;
     if ((int64_t)max_query * (num_query_heads / cache->num_heads) > 0x7fffffff - kMaxRows) return SPEC_EUNSUPPORTED;
     const size_t need = spec_cache_attention_workspace_size(num_query_heads, cache->num_heads, cache->head_dim, dtype);
     if (!ws || ws_bytes < need || ((uintptr_t)ws & 255)) return SPEC_EWORKSPACE;

@@ -99,11 +99,17 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t u, int ctas) {
     return (int)quotient((u + 1) * ctas - 1, total);
 }
 
+struct ShareScratch {  // shared memory of find_share
+    int64_t warp[20];
+    Share share;
+};
+
 // Every thread of the CTA calls it (it synchronises); NT threads.
 template <int NT>
-__device__ __noinline__ Share find_share(const AttnParams &p, int rows) {
-    __shared__ int64_t s_warp[NT / 32];
-    __shared__ Share s_share;
+__device__ __noinline__ Share find_share(const AttnParams &p, int rows, ShareScratch &scratch) {
+    static_assert(NT / 32 <= 20, "a sum a warp");
+    int64_t *s_warp = scratch.warp;
+    Share &s_share = scratch.share;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int64_t sum = 0;
@@ -241,122 +247,110 @@ __device__ __forceinline__ float weight_of(float a, float m) { return a == kNegI
 
 // Counts this CTA's part of a cut item in; true (in every thread) for the part that
 // arrives last, which may then read the other parts.  NT threads call it, `bar` a
-// named barrier of theirs; the barrier orders their stores before thread 0's fence.
+// named barrier of theirs: it orders their stores before thread 0's release, and that
+// thread's acquire before their loads.
 template <int NT>
 __device__ __forceinline__ bool arrive_last(const AttnParams &p, int first_cta, int parts, int *s_flag, int bar) {
     named_sync<NT>(bar);
     if (threadIdx.x == 0) {
-        __threadfence();
-        const int before = atomicAdd(p.tickets + first_cta, 1);
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(p.tickets + first_cta)
+                     : "memory");
         *s_flag = before == parts - 1;
         if (before == parts - 1) p.tickets[first_cta] = 0;  // for the next call
-        __threadfence();
     }
     named_sync<NT>(bar);
     return *s_flag != 0;
 }
 
-// Joins the parts of an item in CTA order and writes its rows, kJoin parts at a time:
-// a thread a row finds their weights (rescaling what is there where the reference
-// rises), then a warp takes rows, four columns a lane, with several parts' loads in
-// flight.  ND: 128-column blocks of the head.
-constexpr int kJoin = 16;
-template <int R>
-struct JoinSpace {
-    float keep[R], w[kJoin][R];
-};
-
+// Joins the parts of an item in CTA order and writes its rows: a warp takes two rows at
+// a time, four columns a lane, with the statistics and sums of four parts in flight.
+// ND: 128-column blocks of the head.
 template <typename T, int NT, int R, int ND>
-__device__ __noinline__ void join_parts(const AttnParams &p, const Part &x, JoinSpace<R> &sp, int bar) {
-    constexpr int kWarps = NT / 32, kRows = (R + kWarps - 1) / kWarps;  // rows a warp
-    const int D = p.c.head_dim, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nrows = x.nrows;
-    const int parts = x.c1 - x.c0 + 1;
+__device__ __noinline__ void join_parts(const AttnParams &p, const Part &x) {
+    constexpr int kWarps = NT / 32, P = 4;
+    const int D = p.c.head_dim, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nrows = x.nrows, parts = x.c1 - x.c0 + 1;
     const int64_t stride = 2 * (int64_t)R * (D + 2);  // from a CTA's slot to the next one's
     const float *slot0 = slot_of(p, x.c0, true, R), *slots = slot_of(p, x.c0, false, R);  // part 0; part c at c * stride
-    float m = kNegInf, l = 0.f;
-    float4 o[kRows][ND];
+    for (int r0 = warp; r0 < nrows; r0 += 2 * kWarps) {
+        float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+        float4 o[2][ND];
 #pragma unroll
-    for (int k = 0; k < kRows; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int n = 0; n < ND; ++n) o[k][n] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < parts; i0 += kJoin) {
-        const int here = min(kJoin, parts - i0);
-        if (tid < nrows) {
-            float mc[kJoin], lc[kJoin];
-            float top = m;
+            for (int n = 0; n < ND; ++n) o[k][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < parts; c0 += P) {
+            float mc[2][P], lc[2][P];
+            float4 v[2][P][ND];
 #pragma unroll
-            for (int c = 0; c < kJoin; ++c) {
-                const float *s = (i0 + c == 0 ? slot0 : slots + (i0 + c) * stride) + R * D + tid;
-                mc[c] = c < here ? __ldcg(s) : kNegInf;
-                lc[c] = c < here ? __ldcg(s + R) : 0.f;
+            for (int c = 0; c < P; ++c) {
+                const float *s = c0 + c == 0 ? slot0 : slots + (c0 + c) * stride;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = r0 + k * kWarps;
+                    const bool on = c0 + c < parts && r < nrows;
+                    mc[k][c] = on ? __ldcg(s + R * D + r) : kNegInf;
+                    lc[k][c] = on ? __ldcg(s + R * D + R + r) : 0.f;
+#pragma unroll
+                    for (int n = 0; n < ND; ++n) {
+                        const int d = 128 * n + 4 * lane;
+                        v[k][c][n] = on && d < D ? __ldcg((const float4 *)(s + r * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
             }
 #pragma unroll
-            for (int c = 0; c < kJoin; ++c) top = fmaxf(top, mc[c]);
-            const float keep = weight_of(m, top);
-            sp.keep[tid] = keep;
-            l *= keep;
+            for (int k = 0; k < 2; ++k) {
+                float top = m[k];
 #pragma unroll
-            for (int c = 0; c < kJoin; ++c) {
-                const float w = weight_of(mc[c], top);
-                sp.w[c][tid] = w;
-                l = fmaf(lc[c], w, l);
+                for (int c = 0; c < P; ++c) top = fmaxf(top, mc[k][c]);
+                const float keep = weight_of(m[k], top);
+                m[k] = top;
+                l[k] *= keep;
+#pragma unroll
+                for (int n = 0; n < ND; ++n) {
+                    o[k][n].x *= keep;
+                    o[k][n].y *= keep;
+                    o[k][n].z *= keep;
+                    o[k][n].w *= keep;
+                }
+#pragma unroll
+                for (int c = 0; c < P; ++c) {
+                    const float w = weight_of(mc[k][c], top);
+                    l[k] = fmaf(lc[k][c], w, l[k]);
+#pragma unroll
+                    for (int n = 0; n < ND; ++n) {
+                        o[k][n].x = fmaf(v[k][c][n].x, w, o[k][n].x);
+                        o[k][n].y = fmaf(v[k][c][n].y, w, o[k][n].y);
+                        o[k][n].z = fmaf(v[k][c][n].z, w, o[k][n].z);
+                        o[k][n].w = fmaf(v[k][c][n].w, w, o[k][n].w);
+                    }
+                }
             }
-            m = top;
         }
-        named_sync<NT>(bar);
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int r = k * kWarps + warp;
+        for (int k = 0; k < 2; ++k) {
+            const int r = r0 + k * kWarps;
             if (r >= nrows) break;
-            const float keep = sp.keep[r];
+            const float inv = inverse_sum(l[k]);
+            const int row = x.rt * R + r, t = row / p.group, g = row - t * p.group;
+            const int64_t at = ((int64_t)(x.r.row0 + t) * p.Hq + x.h * p.group + g) * D;
+            if (p.lse && lane == 0) store_lse(p, x, row, m[k], l[k]);
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
                 const int d = 128 * n + 4 * lane;
                 if (d >= D) break;
-                float4 a = o[k][n];
-                a.x *= keep;
-                a.y *= keep;
-                a.z *= keep;
-                a.w *= keep;
-#pragma unroll 8
-                for (int c = 0; c < here; ++c) {
-                    const float4 v = __ldcg((const float4 *)((i0 + c == 0 ? slot0 : slots + (i0 + c) * stride) + r * D + d));
-                    const float w = sp.w[c][r];
-                    a.x = fmaf(v.x, w, a.x);
-                    a.y = fmaf(v.y, w, a.y);
-                    a.z = fmaf(v.z, w, a.z);
-                    a.w = fmaf(v.w, w, a.w);
+                const float4 f = make_float4(o[k][n].x * inv, o[k][n].y * inv, o[k][n].z * inv, o[k][n].w * inv);
+                if constexpr (sizeof(T) == 2) {
+                    *(uint2 *)((uint16_t *)p.out + at + d) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+                } else {
+                    *(float4 *)((float *)p.out + at + d) = f;
                 }
-                o[k][n] = a;
-            }
-        }
-        named_sync<NT>(bar);
-    }
-    if (tid < nrows) {
-        sp.keep[tid] = inverse_sum(l);
-        if (p.lse) store_lse(p, x, x.rt * R + tid, m, l);
-    }
-    named_sync<NT>(bar);
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-        const int r = k * kWarps + warp;
-        if (r >= nrows) break;
-        const float inv = sp.keep[r];
-        const int row = x.rt * R + r, t = row / p.group, g = row - t * p.group;
-        const int64_t at = ((int64_t)(x.r.row0 + t) * p.Hq + x.h * p.group + g) * D;
-#pragma unroll
-        for (int n = 0; n < ND; ++n) {
-            const int d = 128 * n + 4 * lane;
-            if (d >= D) break;
-            const float4 v = make_float4(o[k][n].x * inv, o[k][n].y * inv, o[k][n].z * inv, o[k][n].w * inv);
-            if constexpr (sizeof(T) == 2) {
-                *(uint2 *)((uint16_t *)p.out + at + d) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-            } else {
-                *(float4 *)((float *)p.out + at + d) = v;
             }
         }
     }
-    named_sync<NT>(bar);
 }
 
 // ------------------------------------------------------------------ fp32 arithmetic kernel
@@ -372,13 +366,13 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
     __shared__ __align__(16) float s_q[R][128 * ND];
     __shared__ float s_p[4][32][R];
     __shared__ float s_m[4][R], s_l[4][R], s_w[2 * R];
-    __shared__ JoinSpace<R> s_join;
+    __shared__ ShareScratch s_scratch;
     __shared__ __align__(16) float s_o[R][128 * ND];
     __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.c.head_dim, bs = p.c.page_size;
     if (warp == 0) write_statuses(p, lane);
-    Share share = find_share<kSimtThreads>(p, R);
+    Share share = find_share<kSimtThreads>(p, R, s_scratch);
     while (share.u < share.end) {
         const Part x = next_part(p, share, R);
         const int nrows = x.nrows, first = x.r.len - x.r.n;
@@ -540,7 +534,7 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
                 slot[R * D + R + tid] = s_w[R + tid];
             }
             if (arrive_last<kSimtThreads>(p, x.c0, x.c1 - x.c0 + 1, &s_flag, 1))
-                join_parts<T, kSimtThreads, R, ND>(p, x, s_join, 1);
+                join_parts<T, kSimtThreads, R, ND>(p, x);
         }
     }
 }
@@ -618,22 +612,22 @@ __device__ __forceinline__ void split_e4m3x4(float2 x, float2 y, uint32_t &first
 // Waits for the phase of the given parity; false after kWaitNs.  These waits are a few
 // hundred cycles long and on the path of every tile, so the thread polls: one that
 // sleeps in the barrier is woken late.
-__device__ __forceinline__ bool poll_barrier(uint64_t *bar, int parity) {
-    uint64_t t0 = 0;
+__device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+__device__ __noinline__ bool poll_barrier(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
     for (uint32_t n = 0;; ++n) {
-        uint32_t done;
-        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-                     : "=r"(done)
-                     : "r"(smem_addr(bar)), "r"((uint32_t)parity)
-                     : "memory");
-        if (done) return true;
-        if ((n & 255) == 255) {
-            const uint64_t t = global_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kWaitNs) return false;
-        }
+        if (try_barrier(bar, parity)) return true;
+        if ((n & 255) == 255 && global_ns() - t0 > kWaitNs) return false;
     }
 }
+
 template <int R>
 struct TcShape {
     static constexpr int kRowsG = 16;                     // rows of a softmax group
@@ -642,7 +636,7 @@ struct TcShape {
     static constexpr int kThreads = kSoft + 64;
     static constexpr int kPerSM = R < 64 ? 2 : 1;         // CTAs an SM
     static constexpr int kSlots = R == 16 ? 6 : (R == 32 ? 5 : 10);
-    static constexpr uint32_t kCols = 4 * R;              // S^T and O^T, two of each
+    static constexpr uint32_t kCols = 8 * R;              // S^T and O^T, two terms and two buffers each
 };
 
 constexpr int kParts = 4;  // parts known ahead
@@ -653,23 +647,37 @@ struct TcShared {
     using C = TcShape<R>;
     uint8_t ring[C::kSlots][kSlotBytes];
     uint8_t q[2][R * 128];             // two terms, rows of 128 bytes, swizzled
+    uint16_t q_raw[R][128];            // the next part's, as they are stored
     uint8_t p[2][R / 16][kTile * 16];  // two terms, blocks of 16 rows, a token's 16 bytes together
-    uint64_t full[C::kSlots], empty[C::kSlots], info_full[kInfo], s_full[2], p_full, o_full, q_full;
+    uint64_t full[C::kSlots], empty[C::kSlots], s_full[2], p_full, o_full, q_full;
     uint64_t part_full[kParts], part_empty[kParts];
     Part part[kParts];                      // b < 0: no more
     float ks[kInfo][8], gv[kInfo][8], wv[kInfo];  // a tile's scales
+    int pages[8];                                 // and its pages, for the copies
     // every softmax warp's own copy, by the tile's parity: row pairs' score factors and
-    // minus references, weights of the sums, of O^T, and of the sums before
+    // minus references, weights of the row sums and of O^T
     float4 cm[4 * C::kGroups][2][C::kRowsG / 2];
-    float beta[4 * C::kGroups][2][C::kRowsG], w[4 * C::kGroups][2][C::kRowsG], alpha[4 * C::kGroups][2][C::kRowsG];
+    float beta[4 * C::kGroups][2][C::kRowsG], w[4 * C::kGroups][2][C::kRowsG];
     float red[2][4][R];
     float c[R];        // score factor of a row: scale * log2(e) / its power of two
     float m[R], l[R];  // at a part's end
-    int orow[2][R];    // a row's output row (token * query heads + head), by the part's parity
-    JoinSpace<R> join;
+    int64_t out_at[2][R];  // a row's first output element, by the part's parity
+    ShareScratch scratch;
     uint32_t tmem;
     int flag;
 };
+
+// The two terms' products of a tile, as loaded from tensor memory, into one.
+template <int N>
+__device__ __forceinline__ void add_terms(uint32_t (&a)[N], const uint32_t (&b)[N]) {
+#pragma unroll
+    for (int r = 0; r < N; r += 2) {
+        const float2 f = fadd2(make_float2(__uint_as_float(a[r]), __uint_as_float(a[r + 1])),
+                               make_float2(__uint_as_float(b[r]), __uint_as_float(b[r + 1])));
+        a[r] = __float_as_uint(f.x);
+        a[r + 1] = __float_as_uint(f.y);
+    }
+}
 
 // Sum over the warp of each of N <= 32 values a lane: lane i gets value i (mod N).
 template <int N>
@@ -689,81 +697,75 @@ __device__ __forceinline__ float warp_sum_scatter(float (&v)[N], int lane) {
     return x;
 }
 
-// Brings a part's queries into L1 before they are needed.
+// A part's queries: a thread takes kCols columns of one row.  start_queries, a tile
+// ahead, starts their copy to shared memory, where only the same thread reads them;
+// store_queries makes two e4m3 terms of each entry for the products.
 template <int R>
-__device__ __forceinline__ void touch_queries(const AttnParams &p, const Part &x, int tid) {
-    using C = TcShape<R>;
-    constexpr int kCols = C::kRowsG, TPR = 128 / C::kRowsG;
-    const int row = (tid >> 7) * C::kRowsG + (tid & 127) / TPR, c0 = (tid % TPR) * kCols;
-    const int grow = x.rt * R + row, t = grow / p.group, g = grow - t * p.group;
-    if (row < x.nrows && c0 < p.c.head_dim) {
-        const char *src = (const char *)p.q + ((int64_t)(x.r.row0 + t) * p.ld_q + (int64_t)(x.h * p.group + g) * p.c.head_dim + c0) * 2;
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
+struct QueryShape {
+    static constexpr int kCols = R * 128 / TcShape<R>::kSoft, kPerRow = 128 / kCols;
+};
+
+template <int R>
+__device__ __noinline__ void start_queries(const AttnParams &p, const Part &x, TcShared<R> &sm, int tid, int parity) {
+    constexpr int kCols = QueryShape<R>::kCols;
+    const int row = tid / QueryShape<R>::kPerRow, c0 = (tid % QueryShape<R>::kPerRow) * kCols, D = p.c.head_dim;
+    if (row >= x.nrows) return;
+    const uint32_t grow = x.rt * R + row, t = grow / (uint32_t)p.group, head = x.h * p.group + (grow - t * p.group);
+    if (c0 == 0) sm.out_at[parity][row] = ((int64_t)(x.r.row0 + (int)t) * p.Hq + head) * D;
+    const char *src = (const char *)p.q + ((int64_t)(x.r.row0 + (int)t) * p.ld_q + (int64_t)head * D + c0) * 2;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 8) {
+        if (c0 + c >= D) break;
+        uint16_t *dst = &sm.q_raw[row][c0 + c];
+        if (p.q_vec) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src + c * 2) : "memory");
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) dst[i] = __ldg((const unsigned short *)(src + c * 2) + i);
+        }
     }
 }
 
-// The queries of a part as two e4m3 terms, 128 / kRowsG threads a row.
 template <int R>
-__device__ __noinline__ void load_queries(const AttnParams &p, const Part &x, TcShared<R> &sm, int tid, int parity) {
-    using C = TcShape<R>;
-    constexpr int kCols = C::kRowsG;            // 128 columns over 128 / kRowsG threads
-    constexpr int TPR = 128 / C::kRowsG;
-    const int row = (tid >> 7) * C::kRowsG + (tid & 127) / TPR, c0 = (tid % TPR) * kCols;
-    const int grow = x.rt * R + row, t = grow / p.group, g = grow - t * p.group, D = p.c.head_dim;
-    const bool live = row < x.nrows;
-    const int orow = live ? (x.r.row0 + t) * p.Hq + x.h * p.group + g : 0;
-    const char *src = (const char *)p.q + ((int64_t)(x.r.row0 + t) * p.ld_q + (int64_t)(x.h * p.group + g) * D) * 2;
-    float amax = 0.f;
-    bool bad = false;
-    float v[kCols];
+__device__ __noinline__ void store_queries(float scale_log2, int nrows, int D, TcShared<R> &sm, int tid) {
+    constexpr int kCols = QueryShape<R>::kCols, kPerRow = QueryShape<R>::kPerRow;
+    const int row = tid / kPerRow, c0 = (tid % kPerRow) * kCols;
+    uint32_t raw[kCols / 2];
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    uint32_t top = 0;  // magnitudes compare as integers; a NaN or an infinity has 0x7f80 or more
 #pragma unroll
     for (int c = 0; c < kCols; c += 8) {
-        float e[8] = {};
-        if (live && c0 + c < D) {
-            if (p.q_vec) {
-                const uint4 u = __ldg((const uint4 *)(src + (c0 + c) * 2));  // in L1: see touch_queries
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    e[2 * i] = bf16_lo(w[i]);
-                    e[2 * i + 1] = bf16_hi(w[i]);
-                }
-            }
-            else load8<2, false>(src + (c0 + c) * 2, e);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[c + i] = e[i];
-            bad |= !(fabsf(e[i]) < __int_as_float(0x7f800000));
-            amax = fmaxf(amax, fabsf(e[i]));
-        }
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (row < nrows && c0 + c < D) u = *(const uint4 *)&sm.q_raw[row][c0 + c];
+        raw[c / 2] = u.x;
+        raw[c / 2 + 1] = u.y;
+        raw[c / 2 + 2] = u.z;
+        raw[c / 2 + 3] = u.w;
     }
 #pragma unroll
-    for (int s = 1; s < TPR; s <<= 1) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-        bad |= (bool)__shfl_xor_sync(0xffffffffu, (int)bad, s);
-    }
-    // the largest magnitude's exponent becomes 7; a row with a NaN or an infinity is NaN
-    const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -110);
+    for (int i = 0; i < kCols / 2; ++i) top = __vmaxu2(top, raw[i] & 0x7fff7fffu);
+#pragma unroll
+    for (int s = 1; s < kPerRow; s <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, s));
+    top = max(top & 0xffffu, top >> 16);
+    // the row's largest magnitude's exponent becomes 7; a row with a NaN or an infinity is NaN
+    const bool bad = top >= 0x7f80u;
+    const int e = max((int)(top >> 7) - 127, -110);
     const float up = __uint_as_float((uint32_t)(bad ? 127 : 134 - e) << 23);
     const float down = bad ? 1.f : __uint_as_float((uint32_t)(120 + e) << 23);
 #pragma unroll
-    for (int c = 0; c < kCols; c += 16) {
-        uint32_t a[4], b[4];
+    for (int c = 0; c < kCols; c += 8) {
+        uint32_t a[2], b[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            split_e4m3x4(make_float2(v[c + 4 * i] * up, v[c + 4 * i + 1] * up),
-                         make_float2(v[c + 4 * i + 2] * up, v[c + 4 * i + 3] * up), a[i], b[i]);
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w0 = raw[c / 2 + 2 * i], w1 = raw[c / 2 + 2 * i + 1];
+            split_e4m3x4(make_float2(bf16_lo(w0) * up, bf16_hi(w0) * up), make_float2(bf16_lo(w1) * up, bf16_hi(w1) * up), a[i], b[i]);
             if (bad) a[i] = 0x7f7f7f7fu;
         }
-        const int at = row * 128 + (((((c0 + c) >> 4)) ^ (row & 7)) << 4);
-        *(uint4 *)(sm.q[0] + at) = make_uint4(a[0], a[1], a[2], a[3]);
-        *(uint4 *)(sm.q[1] + at) = make_uint4(b[0], b[1], b[2], b[3]);
+        const int col = c0 + c, at = row * 128 + (((col >> 4) ^ (row & 7)) << 4) + (col & 8);
+        *(uint2 *)(sm.q[0] + at) = make_uint2(a[0], a[1]);
+        *(uint2 *)(sm.q[1] + at) = make_uint2(b[0], b[1]);
     }
-    if (c0 == 0) {
-        sm.c[row] = fmaxf(p.scale_log2 * down, 1.1754944e-38f);  // -inf times it stays -inf
-        sm.orow[parity][row] = orow;
-    }
+    if (c0 == 0) sm.c[row] = fmaxf(scale_log2 * down, 1.1754944e-38f);  // -inf times it stays -inf
     fence_async_shared();
     __syncwarp();
     if ((tid & 31) == 0) mbar_arrive(&sm.q_full);
@@ -774,8 +776,8 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
     attention_tc_kernel(AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using C = TcShape<R>;
     constexpr int NR = C::kRowsG, NS = C::kSlots;
-    extern __shared__ uint8_t raw[];
-    TcShared<R> &sm = *reinterpret_cast<TcShared<R> *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t raw[];
+    TcShared<R> &sm = *reinterpret_cast<TcShared<R> *>(raw);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the warp's: roles branch on it
     if (tid == 0) {
@@ -783,9 +785,8 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
         }
-        for (int i = 0; i < kInfo; ++i) mbar_init(&sm.info_full[i], 1);
-        mbar_init(&sm.s_full[0], 1);
-        mbar_init(&sm.s_full[1], 1);
+        mbar_init(&sm.s_full[0], 2);  // the product, and the issuer's word for the tile's scales
+        mbar_init(&sm.s_full[1], 2);
         mbar_init(&sm.p_full, C::kSoft / 32);
         mbar_init(&sm.o_full, 1);
         mbar_init(&sm.q_full, C::kSoft / 32);
@@ -797,15 +798,17 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
     }
     if (warp == C::kSoft / 32 + 1) tmem_alloc(&sm.tmem, C::kCols);
     tc_fence_before();
-    Share share = find_share<C::kThreads>(p, R);  // it synchronises the CTA
+    Share share = find_share<C::kThreads>(p, R, sm.scratch);  // it synchronises the CTA
     tc_fence_after();
-    const uint32_t tm = sm.tmem, tS = tm, tO = tm + 2 * R;
+    const uint32_t tm = sm.tmem, tS = tm, tO = tm + 4 * R;  // a buffer: R columns of each term
     bool dead = false;  // a wait ran out: wait no more, finish, report
     auto wait = [&](uint64_t *bar, int parity) {
-        if (!dead && !poll_barrier(bar, parity)) dead = true;
+        if (!try_barrier(smem_addr(bar), parity) && !dead && !poll_barrier(smem_addr(bar), parity)) dead = true;
+        __syncwarp();
     };
     auto wait_long = [&](uint64_t *bar, int parity) {
         if (!dead && !mbar_wait(bar, parity, kWaitNs)) dead = true;
+        __syncwarp();
     };
 
     if (warp == C::kSoft / 32) {
@@ -867,19 +870,21 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     if (kv == 0) {
                         const int at = g % kInfo;
                         if (lane < ppt) {
+                            sm.pages[lane] = pg >= 0 ? pg : p.c.num_pages;  // past the map's end: reads as zeros
                             sm.ks[at][lane] = tks;
                             sm.gv[at][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
                         }
                         if (lane == 0) sm.wv[at] = top * (1.f / 256.f);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.info_full[at]);
+                        __syncwarp();  // the arrival at `full` below releases them
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kSlotBytes);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&sm.full[slot], kSlotBytes);
+#pragma unroll 4
+                        for (int i = 0; i < ppt; ++i)
+                            tma_load_4d(sm.ring[slot] + i * bs * 128, kv ? &vmap : &kmap, 0, 0, x.h, sm.pages[i],
+                                        &sm.full[slot]);
+                    }
                     __syncwarp();
-                    // a page that is not there reads as zeros: past the map's end
-                    if (lane < ppt)
-                        tma_load_4d(sm.ring[slot] + lane * bs * 128, kv ? &vmap : &kmap, 0, 0, x.h,
-                                    pg >= 0 ? pg : p.c.num_pages, &sm.full[slot]);
                 }
                 if (k == 0) {  // the next batch, of this part or of the next
                     if (i0 + batch < x.t1) {
@@ -898,57 +903,64 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                 }
             }
         }
+        if (dead)  // no copy may be in flight when the CTA ends
+            for (int i = max(0, seq - NS); i < seq; ++i) mbar_wait(&sm.full[i % NS], (i / NS) & 1, kWaitNs);
     } else if (warp == C::kSoft / 32 + 1) {
         // ---------------------------------------------------------------- products
         write_statuses(p, lane);  // while the first tile is on its way
-        if (lane == 0) {
-            constexpr uint32_t iqk = fp8_idesc(R, false, false), ipv = fp8_idesc(R, true, true);
-            const int ksteps = (p.c.head_dim + 31) / 32;
-            const uint32_t ring = smem_addr(sm.ring), q = smem_addr(sm.q), pp = smem_addr(sm.p);
-            auto scores = [&](int g) {
-                const int seq = 2 * g, slot = seq % NS;
-                wait(&sm.full[slot], (seq / NS) & 1);
-                if (dead) return;
-                tc_fence_after();
-                const uint32_t a = ring + slot * kSlotBytes;
-                for (int t = 0; t < 2; ++t)
-                    for (int k = 0; k < ksteps; ++k)
-                        mma_fp8(tS + (g & 1) * R, smem_desc(a + 32 * k, 16, 1024, 2),
-                                smem_desc(q + t * R * 128 + 32 * k, 16, 1024, 2), iqk, (t | k) != 0);
+        constexpr uint32_t iqk = fp8_idesc(2 * R, false, false), ipv = fp8_idesc(2 * R, true, true);
+        const int ksteps = (p.c.head_dim + 31) / 32;
+        const uint64_t dk = smem_desc(smem_addr(sm.ring), 16, 1024, 2), dq = smem_desc(smem_addr(sm.q), 16, 1024, 2);
+        const uint64_t dv = smem_desc(smem_addr(sm.ring), 1024, 1024, 2);
+        const uint64_t dp = smem_desc(smem_addr(sm.p), 128, kTile * 16, 0);
+        auto gone = [&] { return (bool)__any_sync(0xffffffffu, dead); };
+        auto scores = [&](int g) {
+            const int seq = 2 * g, slot = seq % NS;
+            wait(&sm.full[slot], (seq / NS) & 1);
+            if (gone()) return;
+            tc_fence_after();
+            const uint64_t a = dk + slot * (kSlotBytes / 16);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < ksteps) mma_fp8(tS + (g & 1) * 2 * R, a + 2 * k, dq + 2 * k, iqk, k != 0);
                 mma_commit(&sm.s_full[g & 1]);
                 mma_commit(&sm.empty[slot]);
-            };
-            auto values = [&](int g) {
-                const int seq = 2 * g + 1, slot = seq % NS;
-                wait(&sm.full[slot], (seq / NS) & 1);
-                wait(&sm.p_full, g & 1);
-                if (dead) return;
-                tc_fence_after();
-                const uint32_t a = ring + slot * kSlotBytes;
-                for (int t = 0; t < 2; ++t)
+                mbar_arrive(&sm.s_full[g & 1]);  // passes the scales on: `full` acquired them
+            }
+            __syncwarp();
+        };
+        auto values = [&](int g) {
+            const int seq = 2 * g + 1, slot = seq % NS;
+            wait(&sm.full[slot], (seq / NS) & 1);
+            wait(&sm.p_full, g & 1);
+            if (gone()) return;
+            tc_fence_after();
+            const uint64_t a = dv + slot * (kSlotBytes / 16);
+            if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kTile / 32; ++k)
-                        mma_fp8(tO + (g & 1) * R, smem_desc(a + 4096 * k, 1024, 1024, 2),
-                                smem_desc(pp + t * R * kTile + 512 * k, 128, kTile * 16, 0), ipv, (t | k) != 0);
+                for (int k = 0; k < kTile / 32; ++k)
+                    mma_fp8(tO + (g & 1) * 2 * R, a + 256 * k, dp + 32 * k, ipv, k != 0);
                 mma_commit(&sm.o_full);
                 mma_commit(&sm.empty[slot]);
-            };
-            int g = 0;
-            for (int n = 0; !dead; ++n) {
-                const int at = n % kParts;
-                wait(&sm.part_full[at], (n / kParts) & 1);
-                if (dead || sm.part[at].b < 0) break;
-                const int tiles = sm.part[at].t1 - sm.part[at].t0;
-                mbar_arrive(&sm.part_empty[at]);
-                wait(&sm.q_full, n & 1);
-                scores(g);
-                for (int i = 0; i < tiles; ++i, ++g) {
-                    if (i + 1 < tiles) scores(g + 1);
-                    values(g);
-                }
+            }
+            __syncwarp();
+        };
+        int g = 0;
+        for (int n = 0; !gone(); ++n) {
+            const int at = n % kParts;
+            wait(&sm.part_full[at], (n / kParts) & 1);
+            if (gone() || __shfl_sync(0xffffffffu, sm.part[at].b, 0) < 0) break;
+            const int tiles = __shfl_sync(0xffffffffu, sm.part[at].t1 - sm.part[at].t0, 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.part_empty[at]);
+            wait(&sm.q_full, n & 1);
+            scores(g);
+            for (int i = 0; i < tiles; ++i, ++g) {
+                if (i + 1 < tiles) scores(g + 1);
+                values(g);
             }
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax and sums
         const int grp = tid >> 7, t128 = tid & 127, w4 = warp & 3, r0 = grp * NR, D = p.c.head_dim;
@@ -959,25 +971,31 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         wait(&sm.part_full[0], 0);
         int g = 0;
         if (sm.part[0].b >= 0) {
-            load_queries<R>(p, sm.part[0], sm, tid, 0);
+            start_queries<R>(p, sm.part[0], sm, tid, 0);
+            store_queries<R>(p.scale_log2, sm.part[0].nrows, D, sm, tid);
             named_sync<C::kSoft>(kAllBar);
         }
         for (int n = 0; sm.part[n % kParts].b >= 0; ++n) {
             const Part &x = sm.part[n % kParts], &next = sm.part[(n + 1) % kParts];
             const int t0 = x.t0, t1 = x.t1;
+            // tiles within [clear_lo, clear_hi] hide no token from any row
+            const int clear_hi = x.pos0, clear_lo = p.window > 0 ? max(0, x.pos1 - p.window + 1) : 0;
             float acc[NR], l[NR];
             float m_run = kNegInf;  // lane r: row r's running reference
+            float alpha = 1.f, alpha_last = 1.f;  // lane r: what row r's sums so far are multiplied by
             bool moved = false, moved_last = false;
 #pragma unroll
             for (int r = 0; r < NR; ++r) acc[r] = l[r] = 0.f;
-            auto add_values = [&](int gg, bool rescale) {  // O^T of tile gg into the sums
+            auto add_values = [&](int gg, bool rescale, float alpha) {  // O^T of tile gg into the sums
                 tc_fence_after();
-                uint32_t o[NR];
-                tmem_ld<NR>(tO + (gg & 1) * R + r0 + lanes, o);
+                uint32_t o[NR], o1[NR];
+                tmem_ld<NR>(tO + (gg & 1) * 2 * R + r0 + lanes, o);
+                tmem_ld<NR>(tO + (gg & 1) * 2 * R + R + r0 + lanes, o1);
                 tmem_wait_ld();
+                add_terms<NR>(o, o1);
                 if (rescale) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) acc[r] *= sm.alpha[warp][gg & 1][r];
+                    for (int r = 0; r < NR; ++r) acc[r] *= __shfl_sync(0xffffffffu, alpha, r);
                 }
 #pragma unroll
                 for (int r = 0; r < NR; r += 4) {
@@ -995,15 +1013,16 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                 const int buf = g & 1, inf = g % kInfo, j0 = x.tile(i) * kTile, j = j0 + t128;
                 if (i + 1 == t1) {
                     wait(&sm.part_full[(n + 1) % kParts], ((n + 1) / kParts) & 1);
-                    if (next.b >= 0) touch_queries<R>(p, next, tid);
+                    if (next.b >= 0) start_queries<R>(p, next, sm, tid, (n + 1) & 1);
                 }
-                wait(&sm.info_full[inf], (g / kInfo) & 1);
-                const float ks = sm.ks[inf][t128 >> bs_shift], gv = sm.gv[inf][t128 >> bs_shift], wv = sm.wv[inf];
                 wait(&sm.s_full[buf], (g >> 1) & 1);
+                const float ks = sm.ks[inf][t128 >> bs_shift], gv = sm.gv[inf][t128 >> bs_shift], wv = sm.wv[inf];
                 tc_fence_after();
-                uint32_t s[NR];
-                tmem_ld<NR>(tS + buf * R + r0 + lanes, s);
+                uint32_t s[NR], s1[NR];
+                tmem_ld<NR>(tS + buf * 2 * R + r0 + lanes, s);
+                tmem_ld<NR>(tS + buf * 2 * R + R + r0 + lanes, s1);
                 tmem_wait_ld();
+                add_terms<NR>(s, s1);
                 float v[NR];
 #pragma unroll
                 for (int r = 0; r < NR; r += 2) {
@@ -1011,7 +1030,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     v[r] = f.x;
                     v[r + 1] = f.y;
                 }
-                if (j0 + kTile - 1 > x.pos0 || (p.window > 0 && j0 <= x.pos1 - p.window && j0 + kTile > p.sinks)) {
+                if (j0 + kTile - 1 > clear_hi || (j0 < clear_lo && j0 + kTile > p.sinks)) {
                     // Some row does not see some token of the tile.  Rows are token-major,
                     // so the rows that see token j are an interval: from the first at a
                     // position >= j to the last at a position < j + window.
@@ -1070,7 +1089,8 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     const bool moves = mm > m_run + kRefStep;  // also from -inf
                     moved_last = moved;
                     moved = __any_sync(0xffffffffu, moves);
-                    float alpha = 1.f;
+                    alpha_last = alpha;
+                    alpha = 1.f;
                     if (moves) {
                         alpha = m_run == kNegInf ? 0.f : ex2_approx(m_run - mm);
                         m_run = mm;
@@ -1082,13 +1102,12 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                         cm[2 + (k & 1)] = -ref;
                         sm.beta[warp][buf][k] = beta;
                         sm.w[warp][buf][k] = beta * wv;
-                        sm.alpha[warp][buf][k] = alpha;
                     }
                     __syncwarp();
                 }
                 if (moved) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) l[r] *= sm.alpha[warp][buf][r];
+                    for (int r = 0; r < NR; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
                 }
                 uint32_t first[NR / 4], rest[NR / 4];
                 const float2 gv2 = make_float2(gv, gv);
@@ -1120,14 +1139,14 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_full);
-                if (i > t0) add_values(g - 1, moved_last);
+                if (i > t0) add_values(g - 1, moved_last, alpha_last);
             }
             // the next part (told before the last tile) sends its queries before this part's
             // last product is waited for
             named_sync<C::kSoft>(kAllBar);  // every warp has the last scores: the queries may go
-            if (next.b >= 0) load_queries<R>(p, next, sm, tid, (n + 1) & 1);
+            if (next.b >= 0) store_queries<R>(p.scale_log2, next.nrows, D, sm, tid);
             wait(&sm.o_full, (g - 1) & 1);
-            add_values(g - 1, moved);
+            add_values(g - 1, moved, alpha);
             tc_fence_before();
             const float lt = warp_sum_scatter<NR>(l, lane);
             if (lane < NR) sm.red[0][w4][r0 + lane] = lt;
@@ -1145,7 +1164,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
                     if (r0 + r < x.nrows && t128 < D)
-                        ((uint16_t *)p.out)[(int64_t)sm.orow[n & 1][r0 + r] * D + t128] =
+                        ((uint16_t *)p.out)[sm.out_at[n & 1][r0 + r] + t128] =
                             (uint16_t)pack_bf16x2(acc[r] * sm.l[r0 + r], 0.f);
             } else {
                 float *slot = slot_of(p, blockIdx.x, x.t0 == 0, R);
@@ -1157,7 +1176,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     slot[R * D + R + r0 + t128] = sm.l[r0 + t128];
                 }
                 if (arrive_last<C::kSoft>(p, x.c0, x.c1 - x.c0 + 1, &sm.flag, kAllBar))
-                    join_parts<uint16_t, C::kSoft, R, 1>(p, x, sm.join, kAllBar);
+                    join_parts<uint16_t, C::kSoft, R, 1>(p, x);
             }
             __syncwarp();  // this warp reads the part no more
             if (lane == 0) mbar_arrive(&sm.part_empty[n % kParts]);
@@ -1200,7 +1219,7 @@ bool codes_map(const spec_kv_cache &c, const void *codes, CUtensorMap *map) {
 template <int R>
 int launch_tc(const AttnParams &p, int dev, int sms, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
     using C = TcShape<R>;
-    constexpr int bytes = (int)sizeof(TcShared<R>) + 1024;
+    constexpr int bytes = (int)sizeof(TcShared<R>);
     static_assert(C::kPerSM * (bytes + 1024) <= 228 * 1024, "shared memory of an SM");
     static std::atomic<bool> set[64];
     if (!set[dev].load()) {

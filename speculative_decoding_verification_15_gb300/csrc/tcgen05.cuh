@@ -65,6 +65,17 @@ __host__ __device__ constexpr uint32_t fp8_idesc(int n, bool a_transposed, bool 
            (8u << 24);
 }
 
+// True in one lane of a converged warp.  The instructions that one thread issues for the
+// warp (products, commits, tiled copies) take their operands from uniform registers: a
+// branch on elect.sync, inside code that the whole warp runs with the same values, tells
+// the compiler so; a branch on the lane's number costs a loop over the lanes around each
+// (130 cycles a product instead of 50).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
 // D (+)= A B, issued by one thread.
 __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(

@@ -72,8 +72,12 @@ __device__ __forceinline__ Request load_request(const AttnParams &p, int b, int 
     return r;
 }
 
-__device__ __forceinline__ int64_t request_tiles(const AttnParams &p, const Request &r) {
-    return (int64_t)p.c.num_heads * r.rt * r.nt;
+// Starting and finishing an item costs a CTA about as much as kItemCost tiles, so on the
+// line an item is that much longer, ahead of its tiles -- where there are enough tiles
+// to go round: with fewer than kTilesEach a CTA, spreading the tiles matters more.
+constexpr int kItemCost = 3, kTilesEach = 4;
+__device__ __forceinline__ int64_t request_items(const AttnParams &p, const Request &r) {
+    return (int64_t)p.c.num_heads * r.rt;
 }
 
 // a / b for a >= 0, b > 0: most quotients here fit 32 bits, where a division is short.
@@ -83,72 +87,88 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return quotient64(a, b);
 }
 
-// A CTA's place on the line of tiles: [u, end), starting `off` tiles into request b.
-// Only as many CTAs as there are tiles take part, so that no share among them is empty
+// A CTA's place on the line: [u, end), starting `off` units into request b.
+// Only as many CTAs as there are units take part, so that no share among them is empty
 // and the parts of a cut item are those of consecutive CTAs.
 struct Share {
     int64_t total, u, end, off;
-    int b, ctas;
+    int b, ctas, cost;  // cost: units of an item ahead of its tiles
 };
 
 __device__ __forceinline__ int64_t share_start(int64_t total, int cta, int ctas) {
     return quotient(total * cta, ctas);
 }
-// The CTA whose share holds tile u.
+// The CTA whose share holds unit u.
 __device__ __forceinline__ int cta_of(int64_t total, int64_t u, int ctas) {
     return (int)quotient((u + 1) * ctas - 1, total);
 }
 
 struct ShareScratch {  // shared memory of find_share
-    int64_t warp[20];
+    int64_t tiles[20], items[20];
     Share share;
 };
 
 // Every thread of the CTA calls it (it synchronises); NT threads.
 template <int NT>
 __device__ __noinline__ Share find_share(const AttnParams &p, int rows, ShareScratch &scratch) {
-    static_assert(NT / 32 <= 20, "a sum a warp");
-    int64_t *s_warp = scratch.warp;
-    Share &s_share = scratch.share;
+    static_assert(NT / 32 <= 20, "sums a warp");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += request_tiles(p, load_request(p, b, rows));
-    int64_t incl = sum;
+    int64_t tiles = 0, items = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = load_request(p, b, rows);
+        const int64_t n = request_items(p, r);
+        items += n;
+        tiles += n * r.nt;
+    }
+    int64_t ti = tiles, it = items;  // sums of the threads up to this one
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const int64_t y = __shfl_up_sync(0xffffffffu, ti, o), z = __shfl_up_sync(0xffffffffu, it, o);
+        if (lane >= o) {
+            ti += y;
+            it += z;
+        }
     }
-    if (lane == 31) s_warp[warp] = incl;
-    if (tid == 0) s_share.b = p.B;
+    if (lane == 31) {
+        scratch.tiles[warp] = ti;
+        scratch.items[warp] = it;
+    }
+    if (tid == 0) scratch.share.b = p.B;
     __syncthreads();
-    int64_t before = incl - sum, total = 0;
+    int64_t all_tiles = 0, all_items = 0;
     for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before += s_warp[w];
-        total += s_warp[w];
+        if (w < warp) {
+            ti += scratch.tiles[w];
+            it += scratch.items[w];
+        }
+        all_tiles += scratch.tiles[w];
+        all_items += scratch.items[w];
     }
+    const int cost = all_tiles >= (int64_t)kTilesEach * gridDim.x ? kItemCost : 0;
+    const int64_t total = all_tiles + cost * all_items, sum = tiles + cost * items, before = ti + cost * it - sum;
     const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
     const int64_t u = cta < ctas ? share_start(total, cta, ctas) : 0;
     const int64_t end = cta < ctas ? share_start(total, cta + 1, ctas) : 0;
-    if (u < end && u >= before && u < before + sum) {  // one thread: its requests hold tile u
+    if (u < end && u >= before && u < before + sum) {  // one thread: its requests hold unit u
         int b = b0;
         int64_t off = u - before;
-        for (;;) {
-            const int64_t t = request_tiles(p, load_request(p, b, rows));
+        for (; b + 1 < b1; ++b) {
+            const Request r = load_request(p, b, rows);
+            const int64_t t = request_items(p, r) * (r.nt + cost);
             if (off < t) break;
             off -= t;
-            ++b;
         }
-        s_share.b = b;
-        s_share.off = off;
+        scratch.share.b = b;
+        scratch.share.off = off;
     }
     __syncthreads();
-    Share s = s_share;
+    Share s = scratch.share;
     s.total = total;
     s.u = u;
     s.end = end;
     s.ctas = ctas;
+    s.cost = cost;
     return s;
 }
 
@@ -162,29 +182,38 @@ struct Part {
     __device__ __forceinline__ int tile(int i) const { return i < r.s1 ? i : r.w0 + (i - r.s1); }
 };
 
-// The share's next part; call while s.u < s.end.
+// The share's next part; b = -1 where there is none.
 __device__ __noinline__ Part next_part(const AttnParams &p, Share &s, int rows) {
     Part x;
+    x.b = -1;
+    int64_t item = 0;
     for (;;) {
+        if (s.u >= s.end) return x;
         x.r = load_request(p, s.b, rows);
-        if (s.off < request_tiles(p, x.r)) break;
-        s.off = 0;  // a share's next request is entered at its first tile
-        ++s.b;
+        if (s.off >= request_items(p, x.r) * (x.r.nt + s.cost)) {
+            s.off = 0;  // a share's next request is entered at its first unit
+            ++s.b;
+            continue;
+        }
+        const int units = x.r.nt + s.cost;
+        const int64_t i = quotient(s.off, units);
+        const int at = (int)(s.off - i * units), to = (int)min((int64_t)units, at + s.end - s.u);
+        item = s.u - at;
+        s.u += to - at;
+        s.off += to - at;
+        if (to <= s.cost) continue;  // none of its tiles are here
+        x.b = s.b;
+        x.t0 = max(0, at - s.cost);
+        x.t1 = to - s.cost;
+        x.h = (int)quotient(i, x.r.rt);
+        x.rt = (int)(i - (int64_t)x.h * x.r.rt);
+        break;
     }
-    x.b = s.b;
-    const int64_t i = quotient(s.off, x.r.nt);
-    x.t0 = (int)(s.off - i * x.r.nt);
-    x.h = (int)quotient(i, x.r.rt);
-    x.rt = (int)(i - (int64_t)x.h * x.r.rt);
-    const int64_t item = s.u - x.t0, left = s.end - s.u;
-    x.t1 = (int)min((int64_t)x.r.nt, x.t0 + left);
-    s.u += x.t1 - x.t0;
-    s.off += x.t1 - x.t0;
     x.whole = x.t0 == 0 && x.t1 == x.r.nt;
     x.c0 = x.c1 = blockIdx.x;
     if (!x.whole) {
-        x.c0 = cta_of(s.total, item, s.ctas);
-        x.c1 = cta_of(s.total, item + x.r.nt - 1, s.ctas);
+        x.c0 = cta_of(s.total, item + s.cost, s.ctas);
+        x.c1 = cta_of(s.total, item + s.cost + x.r.nt - 1, s.ctas);
     }
     const int row0 = x.rt * rows;
     x.nrows = min(rows, x.r.n * p.group - row0);
@@ -373,8 +402,9 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
     const int D = p.c.head_dim, bs = p.c.page_size;
     if (warp == 0) write_statuses(p, lane);
     Share share = find_share<kSimtThreads>(p, R, s_scratch);
-    while (share.u < share.end) {
+    for (;;) {
         const Part x = next_part(p, share, R);
+        if (x.b < 0) break;
         const int nrows = x.nrows, first = x.r.len - x.r.n;
         __syncthreads();  // the part before is done with shared memory
         for (int i = tid; i < R * D; i += kSimtThreads) {
@@ -635,7 +665,7 @@ struct TcShape {
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
     static constexpr int kThreads = kSoft + 64;
     static constexpr int kPerSM = R < 64 ? 2 : 1;         // CTAs an SM
-    static constexpr int kSlots = R == 16 ? 6 : (R == 32 ? 5 : 10);
+    static constexpr int kSlots = R < 64 ? 5 : 10;
     static constexpr uint32_t kCols = 8 * R;              // S^T and O^T, two terms and two buffers each
 };
 
@@ -782,7 +812,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the warp's: roles branch on it
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.full[i], 2);  // the copies, and the copier's word that the tile's scales are there
             mbar_init(&sm.empty[i], 1);
         }
         mbar_init(&sm.s_full[0], 2);  // the product, and the issuer's word for the tile's scales
@@ -838,9 +868,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         auto fetch_scale = [&](const float *s, const Part &x, int page) {
             return page >= 0 ? __ldg(s + (int64_t)page * p.c.num_heads + x.h) : 0.f;
         };
-        Part x, xn;
-        x.b = xn.b = -1;
-        if (share.u < share.end) xn = next_part(p, share, R);
+        Part x, xn = next_part(p, share, R);
         tell_part(xn);
         int i0 = 0, in = xn.t0, page = -1, page_n = -1;
         float ks = 0.f, vs = 0.f, ks_n = 0.f, vs_n = 0.f;
@@ -858,9 +886,6 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
             for (int k = 0; k < batch && i0 + k < x.t1 && !dead; ++k, ++g) {
                 const int from = (k << shift) + (lane & (ppt - 1));
                 const int pg = __shfl_sync(0xffffffffu, page, from);
-                const float tks = __shfl_sync(0xffffffffu, ks, from), tvs = __shfl_sync(0xffffffffu, vs, from);
-                float top = tvs;
-                for (int s = 1; s < ppt; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++seq) {
                     const int slot = seq % NS, turn = seq / NS;
@@ -868,14 +893,8 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
                     if (kv == 0) {
-                        const int at = g % kInfo;
-                        if (lane < ppt) {
-                            sm.pages[lane] = pg >= 0 ? pg : p.c.num_pages;  // past the map's end: reads as zeros
-                            sm.ks[at][lane] = tks;
-                            sm.gv[at][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
-                        }
-                        if (lane == 0) sm.wv[at] = top * (1.f / 256.f);
-                        __syncwarp();  // the arrival at `full` below releases them
+                        if (lane < ppt) sm.pages[lane] = pg >= 0 ? pg : p.c.num_pages;  // past the map's end: reads as zeros
+                        __syncwarp();
                     }
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&sm.full[slot], kSlotBytes);
@@ -884,14 +903,25 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                             tma_load_4d(sm.ring[slot] + i * bs * 128, kv ? &vmap : &kmap, 0, 0, x.h, sm.pages[i],
                                         &sm.full[slot]);
                     }
+                    if (kv == 0) {  // the scales may still be on their way here
+                        const float tks = __shfl_sync(0xffffffffu, ks, from), tvs = __shfl_sync(0xffffffffu, vs, from);
+                        float top = tvs;
+                        for (int s = 1; s < ppt; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                        const int at = g % kInfo;
+                        if (lane < ppt) {
+                            sm.ks[at][lane] = tks;
+                            sm.gv[at][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
+                        }
+                        if (lane == 0) sm.wv[at] = top * (1.f / 256.f);
+                    }
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.full[slot]);
                 }
                 if (k == 0) {  // the next batch, of this part or of the next
                     if (i0 + batch < x.t1) {
                         in = i0 + batch;
                     } else {
-                        xn.b = -1;
-                        if (share.u < share.end) xn = next_part(p, share, R);
+                        xn = next_part(p, share, R);
                         tell_part(xn);
                         in = xn.t0;
                     }

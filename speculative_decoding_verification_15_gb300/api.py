@@ -229,21 +229,31 @@ def verify_sample_host(target_h, draft_h, tokens_h, temperature_h, seed: int, st
 
 # ------------------------------------------------------------------ 8-bit paged key/value cache
 _attn_ws: dict[tuple[int, int], torch.Tensor] = {}
+_HERE = contextlib.nullcontext()
 
 
 def _on(stream):
     """Run what the call itself allocates and converts on the stream it launches on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
-def _attention_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int) -> torch.Tensor:
+def _i32(t, device):
+    """int32 and contiguous on the device; as it is where it already is that."""
+    if t is None or (t.dtype is torch.int32 and t.device == device and t.is_contiguous()):
+        return t
+    return _as_i32(t, device)
+
+
+def _attention_workspace(device: torch.device, stream, nbytes: int) -> torch.Tensor:
     """One zero-filled workspace for each device and stream: calls on one stream run in
     order and may share it, calls on two streams may not."""
-    key = (device.index, stream.cuda_stream)
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     with _ws_lock:
-        ws = _attn_ws.get(key)
+        ws = _attn_ws.get((device.index, raw))
         if ws is None or ws.numel() < nbytes:
-            ws = _attn_ws[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            if not torch.cuda.is_current_stream_capturing():  # a graph's memory and its zeros are the graph's own
+                _attn_ws[(device.index, raw)] = ws
         return ws
 
 
@@ -267,7 +277,7 @@ def kv_append(cache: KVCache, k, v, page_table, cached_len, cu_new, max_new: int
     dev = k.device
     with _on(stream):
         out = dict(status=torch.empty(cu_new.numel() - 1, dtype=torch.int32, device=dev))
-        binding.spec_kv_append(cache, k, v, _as_i32(page_table, dev), _as_i32(cached_len, dev), _as_i32(cu_new, dev),
+        binding.spec_kv_append(cache, k, v, _i32(page_table, dev), _i32(cached_len, dev), _i32(cu_new, dev),
                                max_new, out["status"], stream)
     return out
 
@@ -280,7 +290,7 @@ def kv_gather(cache: KVCache, page_table, cu_out, n_out: int, first=None, dtype=
     with _on(stream):
         out = dict(k=torch.empty(shape, dtype=dtype, device=dev), v=torch.empty(shape, dtype=dtype, device=dev),
                    status=torch.empty(cu_out.numel() - 1, dtype=torch.int32, device=dev))
-        binding.spec_kv_gather(cache, _as_i32(page_table, dev), _as_i32(cu_out, dev), _as_i32(first, dev), out["k"],
+        binding.spec_kv_gather(cache, _i32(page_table, dev), _i32(cu_out, dev), _i32(first, dev), out["k"],
                                out["v"], out["status"], stream)
     return out
 
@@ -298,9 +308,8 @@ def cache_attention(q, cache: KVCache, page_table, seq_len, cu_query, max_query:
         out = dict(out=torch.empty((n, heads, dim), dtype=q.dtype, device=dev),
                    lse=torch.empty((n, heads), dtype=torch.float32, device=dev) if want_lse else None,
                    status=torch.empty(cu_query.numel() - 1, dtype=torch.int32, device=dev))
-        at = stream if stream is not None else torch.cuda.current_stream(dev)
         nbytes = binding.spec_cache_attention_workspace_size(heads, cache.k.shape[1], dim, binding._dtype_code(q))
-        binding.spec_cache_attention(q, cache, _as_i32(page_table, dev), _as_i32(seq_len, dev), _as_i32(cu_query, dev),
+        binding.spec_cache_attention(q, cache, _i32(page_table, dev), _i32(seq_len, dev), _i32(cu_query, dev),
                                      max_query, dim ** -0.5 if scale is None else scale, window, sinks, out["out"],
-                                     out["lse"], out["status"], _attention_workspace(dev, at, nbytes), at)
+                                     out["lse"], out["status"], _attention_workspace(dev, stream, nbytes), stream)
     return out

@@ -40,21 +40,21 @@ class SpecError(RuntimeError):
         self.rc = rc
 
 
-class KVCache(NamedTuple):
-    """The 8-bit paged key/value cache: codes [pages, heads, page_size, head_dim]
-    (float8_e4m3fn, head_dim contiguous, other strides multiples of 16 and the same
-    for keys and values) and one float32 scale for each page and head."""
-    k: torch.Tensor
-    v: torch.Tensor
-    k_scale: torch.Tensor
-    v_scale: torch.Tensor
-
-
 class _CacheStruct(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KVCache(NamedTuple):
+    """The 8-bit paged key/value cache: codes [pages, heads, page_size, head_dim]
+    (float8_e4m3fn or their bytes, head_dim contiguous, other strides multiples of 16
+    and the same for keys and values) and one float32 scale for each page and head."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
 
 
 def lib_path() -> str:
@@ -500,109 +500,127 @@ def spec_schedule_threshold(conf, max_len, threshold: float, out_len, stream=Non
                                      _stream_handle(stream, dev))
 
 
+# The cache calls run once a layer and decoding step, so their checks cost little: each
+# tensor's attributes are read once, and the device is made current only if it is not.
 def _cache_struct(cache, device) -> _CacheStruct:
     k, v, ks, vs = cache
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+    shape, strides, dtype = k.shape, k.stride(), k.dtype
+    if len(shape) != 4 or v.shape != shape or v.stride() != strides or v.dtype is not dtype:
         raise ValueError("cache keys and values must be [pages, heads, page_size, head_dim] of one layout")
-    if k.dtype is not torch.float8_e4m3fn and k.dtype is not torch.uint8:
-        raise TypeError(f"cache codes must be float8_e4m3fn (or their bytes), got {k.dtype}")
-    pages, heads, size, dim = k.shape
-    sp, sh, st, sd = k.stride()
-    if sd != 1:
+    if dtype is not torch.float8_e4m3fn and dtype is not torch.uint8:
+        raise TypeError(f"cache codes must be float8_e4m3fn (or their bytes), got {dtype}")
+    if strides[3] != 1:
         raise ValueError("cache codes must have head_dim contiguous")
     if k.device != device or v.device != device:
         raise ValueError(f"the cache must be on {device}")
-    _need(ks, "k_scale", torch.float32, (pages, heads), device)
-    _need(vs, "v_scale", torch.float32, (pages, heads), device)
-    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), sp, sh, st, pages, size, heads, dim)
+    scales = shape[:2]
+    for t, name in ((ks, "k_scale"), (vs, "v_scale")):
+        if t.shape != scales or t.dtype is not torch.float32 or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 [pages, heads] tensor on {device}")
+    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), strides[0], strides[1], strides[2],
+                        shape[0], shape[2], shape[1], shape[3])
 
 
 def _token_rows(t, name, heads, dim, device) -> int:
     """Row stride of [tokens, heads, dim] rows whose heads are contiguous."""
-    if not t.is_cuda or t.device != device:
+    if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
+    if strides[2] != 1 or (heads > 1 and strides[1] != dim):
         raise ValueError(f"{name} must have heads and head_dim contiguous within a token")
-    ld = t.stride(0) if t.shape[0] > 1 else heads * dim
+    ld = strides[0] if shape[0] > 1 else heads * dim
     if ld < heads * dim:
         raise ValueError(f"{name}: token rows overlap")
     return ld
 
 
-def _page_table(t, B, device) -> int:
+def _ints(t, name, shape, device) -> int:
+    """Address of a contiguous int32 tensor of the given shape."""
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {tuple(shape)} tensor on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _table(t, B, device):
     if t.dim() != 2:
         raise ValueError("page_table must be [B, pages a request]")
-    _need(t, "page_table", torch.int32, (B, t.shape[1]), device)
-    return t.shape[1]
+    return _ints(t, "page_table", (B, t.shape[1]), device), t.shape[1]
+
+
+def _launch(name: str, device, stream, *args) -> None:
+    lib = load()
+    if stream is None:
+        at = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    else:
+        at = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = getattr(lib, name)(*args, at)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib, name)(*args, at)
+    if rc != SPEC_OK:
+        raise SpecError(name, rc, lib)
 
 
 def spec_kv_append(cache, k, v, page_table, cached_len, cu_new, max_new: int, out_status, stream=None) -> None:
     """k, v [tokens, heads, head_dim]; cached_len [B]; cu_new [B + 1]; out_status [B]."""
-    lib = load()
     dev = k.device
     c = _cache_struct(cache, dev)
     ldk = _token_rows(k, "k", c.num_heads, c.head_dim, dev)
     ldv = _token_rows(v, "v", c.num_heads, c.head_dim, dev)
-    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+    n = k.shape[0]
+    if v.dtype is not k.dtype or v.shape[0] != n:
         raise ValueError("k and v must share tokens and dtype")
     B = cu_new.numel() - 1
-    _need(cu_new, "cu_new", torch.int32, (B + 1,), dev)
-    _need(cached_len, "cached_len", torch.int32, (B,), dev)
-    width = _page_table(page_table, B, dev)
-    _need(out_status, "out_status", torch.int32, (B,), dev)
-    _call(lib, "spec_kv_append", dev, ctypes.byref(c), _ptr(k), _ptr(v), _dtype_code(k), ldk, ldv, k.shape[0], B,
-          _ptr(cu_new), int(max_new), _ptr(cached_len), _ptr(page_table), width, _ptr(out_status),
-          _stream_handle(stream, dev))
+    table, width = _table(page_table, B, dev)
+    _launch("spec_kv_append", dev, stream, c, k.data_ptr(), v.data_ptr(), _dtype_code(k), ldk, ldv, n, B,
+            _ints(cu_new, "cu_new", (B + 1,), dev), max_new, _ints(cached_len, "cached_len", (B,), dev), table, width,
+            _ints(out_status, "out_status", (B,), dev))
 
 
 def spec_kv_gather(cache, page_table, cu_out, first, out_k, out_v, out_status, stream=None) -> None:
     """out_k, out_v [rows, heads, head_dim]; cu_out [B + 1]; first [B] or None; out_status [B]."""
-    lib = load()
     dev = out_k.device
     c = _cache_struct(cache, dev)
     n = out_k.shape[0]
     for t, name in ((out_k, "out_k"), (out_v, "out_v")):
         _need(t, name, out_k.dtype, (n, c.num_heads, c.head_dim), dev)
     B = cu_out.numel() - 1
-    _need(cu_out, "cu_out", torch.int32, (B + 1,), dev)
-    if first is not None:
-        _need(first, "first", torch.int32, (B,), dev)
-    width = _page_table(page_table, B, dev)
-    _need(out_status, "out_status", torch.int32, (B,), dev)
-    _call(lib, "spec_kv_gather", dev, ctypes.byref(c), B, _ptr(cu_out), n, _ptr(first), _ptr(page_table), width,
-          _ptr(out_k), _ptr(out_v), _dtype_code(out_k), _ptr(out_status), _stream_handle(stream, dev))
+    table, width = _table(page_table, B, dev)
+    _launch("spec_kv_gather", dev, stream, c, B, _ints(cu_out, "cu_out", (B + 1,), dev), n,
+            None if first is None else _ints(first, "first", (B,), dev), table, width, out_k.data_ptr(),
+            out_v.data_ptr(), _dtype_code(out_k), _ints(out_status, "out_status", (B,), dev))
 
 
 def spec_cache_attention_workspace_size(num_query_heads: int, num_heads: int, head_dim: int, dtype: int) -> int:
-    return int(load().spec_cache_attention_workspace_size(num_query_heads, num_heads, head_dim, dtype))
+    return load().spec_cache_attention_workspace_size(num_query_heads, num_heads, head_dim, dtype)
 
 
 def spec_cache_attention(q, cache, page_table, seq_len, cu_query, max_query: int, scale: float, window: int,
                          sinks: int, out, out_lse, out_status, workspace, stream=None) -> None:
     """q, out [tokens, query heads, head_dim]; seq_len [B]; cu_query [B + 1]; out_lse
     [tokens, query heads] float32 or None; out_status [B]; workspace zeroed once."""
-    lib = load()
     dev = q.device
     c = _cache_struct(cache, dev)
     if q.dim() != 3:
         raise ValueError(f"q must be [tokens, query heads, head_dim], got {tuple(q.shape)}")
-    n, heads = q.shape[0], q.shape[1]
+    n, heads, dim = q.shape
     ldq = _token_rows(q, "q", heads, c.head_dim, dev)
-    _need(out, "out", q.dtype, (n, heads, c.head_dim), dev)
+    _need(out, "out", q.dtype, (n, heads, dim), dev)
     if out_lse is not None:
         _need(out_lse, "out_lse", torch.float32, (n, heads), dev)
     B = cu_query.numel() - 1
-    _need(cu_query, "cu_query", torch.int32, (B + 1,), dev)
-    _need(seq_len, "seq_len", torch.int32, (B,), dev)
-    width = _page_table(page_table, B, dev)
-    _need(out_status, "out_status", torch.int32, (B,), dev)
+    table, width = _table(page_table, B, dev)
     _need(workspace, "workspace", torch.uint8, None, dev)
-    _call(lib, "spec_cache_attention", dev, ctypes.byref(c), _ptr(q), _dtype_code(q), ldq, heads, n, B,
-          _ptr(cu_query), int(max_query), _ptr(seq_len), _ptr(page_table), width, float(scale), int(window),
-          int(sinks), _ptr(out), _ptr(out_lse), _ptr(out_status), _ptr(workspace), workspace.numel(),
-          _stream_handle(stream, dev))
+    _launch("spec_cache_attention", dev, stream, c, q.data_ptr(), _dtype_code(q), ldq, heads, n, B,
+            _ints(cu_query, "cu_query", (B + 1,), dev), max_query, _ints(seq_len, "seq_len", (B,), dev), table, width,
+            scale, window, sinks, out.data_ptr(), None if out_lse is None else out_lse.data_ptr(),
+            _ints(out_status, "out_status", (B,), dev), workspace.data_ptr(), workspace.numel())
 
 
 def profile_enable(on: bool) -> None:

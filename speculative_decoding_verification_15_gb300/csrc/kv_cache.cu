@@ -4,6 +4,13 @@
 namespace specv {
 namespace {
 
+// n / d as the high half of a product: exact for n * d < 2^32, with m = ceil(2^32 / d), d > 1.
+struct Divisor {
+    uint32_t d, m;
+};
+inline Divisor divisor(uint32_t d) { return {d, d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0u}; }
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor &v) { return v.d > 1 ? __umulhi(n, v.m) : n; }
+
 struct KvParams {
     spec_kv_cache c;
     const void *src[2];  // append: new keys, values; rows ld[i] elements apart
@@ -12,6 +19,7 @@ struct KvParams {
     const int32_t *cu, *start, *table;
     int32_t *status;
     int B, ld_table, n_tokens, max_new;
+    Divisor per_token, per_head, per_row;  // vectors of 8 of a head, of 16 of a head, of 16 of a row
 };
 
 constexpr int kExpMin = -100, kExpMax = 119;  // exponents of a written scale
@@ -28,6 +36,7 @@ __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint3
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
+
 // Request b's new tokens, or false where its offsets or lengths are not usable.
 __device__ __forceinline__ bool request_range(const KvParams &p, int b, int &row0, int &n, int &from) {
     row0 = p.cu[b];
@@ -42,12 +51,12 @@ __device__ __forceinline__ bool request_range(const KvParams &p, int b, int &row
 // One CTA per touched page, head and keys | values: the page's scale is one number for
 // all of its tokens, so a CTA sees all of them.  Reading the new entries twice (first
 // for their largest magnitude, then to round them) costs nothing in DRAM: at most
-// 128 x 256 elements, the first kHeld * blockDim vectors held in registers, the rest
+// 128 x 256 elements, the first kHeld vectors a thread held in registers, the rest
 // read again out of L1.
-constexpr int kHeld = 4;
+constexpr int kHeld = 4, kAppendThreads = 128;
 
 template <int ESZ, bool VEC>
-__global__ void __launch_bounds__(256) kv_append_kernel(KvParams p) {
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvParams p) {
     const int b = blockIdx.z >> 1, kv = blockIdx.z & 1, h = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
     const int bs = p.c.page_size, D = p.c.head_dim;
     int row0, n, from;
@@ -57,7 +66,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvParams p) {
         int st = ok ? SPEC_STATUS_OK : SPEC_STATUS_BAD_LENGTH;
         bool bad = false;
         if (ok && n > 0)
-            for (int i = first_page + tid; i <= (from + n - 1) / bs; i += blockDim.x) {
+            for (int i = first_page + tid; i <= (from + n - 1) / bs; i += kAppendThreads) {
                 const int page = p.table[(int64_t)b * p.ld_table + i];
                 bad |= page < 0 || page >= p.c.num_pages;
             }
@@ -76,40 +85,57 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvParams p) {
 
     const char *src = (const char *)p.src[kv] + ((int64_t)src_row * p.ld[kv] + (int64_t)h * D) * ESZ;
     const int64_t src_step = p.ld[kv] * ESZ;
-    const int vpt = D >> 3, nvec = m * vpt;  // vectors of 8 elements
+    const uint32_t vpt = D >> 3;
+    const int nvec = m * (int)vpt;  // vectors of 8 elements, at most 128 * 32
+    auto read = [&](int v, float(&x)[8]) {
+        const uint32_t t = quotient(v, p.per_token);
+        load8<ESZ, VEC>(src + (int64_t)t * src_step + (v - t * vpt) * (8 * ESZ), x);
+    };
     float held[kHeld][8];
-    float amax = 0.f;
+    float amax = 0.f;  // the largest magnitude, an infinity included, a NaN not
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-        const int v = tid + i * blockDim.x;
-        if (v < nvec) load8<ESZ, VEC>(src + (v / vpt) * src_step + (v % vpt) * 8 * ESZ, held[i]);
+        const int v = tid + i * kAppendThreads;
+        if (v < nvec) read(v, held[i]);
     }
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-        if (tid + i * (int)blockDim.x >= nvec) break;
+        if (tid + i * kAppendThreads >= nvec) break;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = fabsf(held[i][e]);
-            if (finite(a)) amax = fmaxf(amax, a);
-        }
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(held[i][e]));
     }
-    for (int v = tid + kHeld * blockDim.x; v < nvec; v += blockDim.x) {
+    for (int v = tid + kHeld * kAppendThreads; v < nvec; v += kAppendThreads) {
         float x[8];
-        load8<ESZ, VEC>(src + (v / vpt) * src_step + (v % vpt) * 8 * ESZ, x);
+        read(v, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = fabsf(x[e]);
-            if (finite(a)) amax = fmaxf(amax, a);
-        }
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
     }
-    __shared__ float s_max[8];
+    __shared__ float s_max[kAppendThreads / 32];
     float *scale_at = (kv ? p.c.v_scale : p.c.k_scale) + (int64_t)page * p.c.num_heads + h;
     const float had = slot0 > 0 ? *scale_at : 0.f;
-    amax = warp_max(amax);
-    if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-    __syncthreads();  // also: every thread has read the present scale
-    amax = s_max[0];
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, s_max[w]);
+    auto block_max = [&](float a) {
+        a = warp_max(a);
+        if ((tid & 31) == 0) s_max[tid >> 5] = a;
+        __syncthreads();  // also: every thread has read the present scale
+        a = s_max[0];
+#pragma unroll
+        for (int w = 1; w < kAppendThreads / 32; ++w) a = fmaxf(a, s_max[w]);
+        return a;
+    };
+    amax = block_max(amax);
+    const bool infinite = !finite(amax);
+    if (infinite) {  // rare: again, over the finite entries
+        amax = 0.f;
+        for (int v = tid; v < nvec; v += kAppendThreads) {
+            float x[8];
+            read(v, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (finite(x[e])) amax = fmaxf(amax, fabsf(x[e]));
+        }
+        __syncthreads();
+        amax = block_max(amax);
+    }
     const float scale = fmaxf(exp2_int(scale_exponent(amax)), had);
     if (tid == 0) *scale_at = scale;
 
@@ -119,29 +145,33 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvParams p) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            // an infinity becomes a NaN: inf - inf
-            const float a = x[2 * e] - x[2 * e] == 0.f ? x[2 * e] * inv : x[2 * e] - x[2 * e];
-            const float c = x[2 * e + 1] - x[2 * e + 1] == 0.f ? x[2 * e + 1] * inv : x[2 * e + 1] - x[2 * e + 1];
+            float a = x[2 * e] * inv, c = x[2 * e + 1] * inv;
+            if (infinite) {  // an infinity becomes a NaN: inf - inf
+                a = finite(x[2 * e]) ? a : x[2 * e] - x[2 * e];
+                c = finite(x[2 * e + 1]) ? c : x[2 * e + 1] - x[2 * e + 1];
+            }
             w[e] = float2_to_e4m3x2(a, c);
         }
-        *(uint2 *)(codes + (int64_t)(slot0 + v / vpt) * p.c.token_stride + (v % vpt) * 8) =
+        const uint32_t t = quotient(v, p.per_token);
+        *(uint2 *)(codes + (int64_t)(slot0 + (int)t) * p.c.token_stride + (v - t * vpt) * 8) =
             make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     };
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-        const int v = tid + i * blockDim.x;
+        const int v = tid + i * kAppendThreads;
         if (v < nvec) put(v, held[i]);
     }
-    for (int v = tid + kHeld * blockDim.x; v < nvec; v += blockDim.x) {
+    for (int v = tid + kHeld * kAppendThreads; v < nvec; v += kAppendThreads) {
         float x[8];
-        load8<ESZ, VEC>(src + (v / vpt) * src_step + (v % vpt) * 8 * ESZ, x);
+        read(v, x);
         put(v, x);
     }
     if (slot0 > 0 && scale > had) {  // the kept tokens, in the grown scale
         const float ratio = had / scale;
         const int kept = slot0 * (D >> 4);
-        for (int v = tid; v < kept; v += blockDim.x) {
-            uint4 *at = (uint4 *)(codes + (int64_t)(v / (D >> 4)) * p.c.token_stride + (v % (D >> 4)) * 16);
+        for (int v = tid; v < kept; v += kAppendThreads) {
+            const uint32_t t = quotient(v, p.per_head);
+            uint4 *at = (uint4 *)(codes + (int64_t)t * p.c.token_stride + (v - t * (D >> 4)) * 16);
             uint4 q = *at;
             uint32_t *w = &q.x;
 #pragma unroll
@@ -161,30 +191,48 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvParams p) {
 // requests' lengths and pages, one warp a request.
 constexpr int kGatherThreads = 256, kGatherRows = 32;
 
-template <int ESZ>
+// 16 values (32 bytes of bf16, 64 of fp32).  WIDE: 32-byte aligned, and stored 32 bytes
+// at a time, so that a thread writes whole sectors.
+template <bool WIDE>
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
+    if constexpr (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        __stcs((uint4 *)dst, make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs((uint4 *)dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    }
+}
+
+template <int ESZ, bool WIDE>
 __device__ __forceinline__ void store16(void *dst, uint4 q, float scale) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint4 *out = (uint4 *)dst;
+    float f[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 a = e4m3x2_to_float2(w[i] & 0xffffu), c = e4m3x2_to_float2(w[i] >> 16);
-        if constexpr (ESZ == 4) {
-            __stcs(out + i, make_uint4(__float_as_uint(a.x * scale), __float_as_uint(a.y * scale),
-                                       __float_as_uint(c.x * scale), __float_as_uint(c.y * scale)));
-        } else {
-            const uint32_t lo = pack_bf16x2(a.x * scale, a.y * scale), hi = pack_bf16x2(c.x * scale, c.y * scale);
-            if (i & 1) {
-                const uint32_t *u = &q.x;  // the pair packed at the step before
-                __stcs(out + (i >> 1), make_uint4(u[0], u[1], lo, hi));
-            } else {
-                q.x = lo;
-                q.y = hi;
-            }
+        f[4 * i] = a.x * scale;
+        f[4 * i + 1] = a.y * scale;
+        f[4 * i + 2] = c.x * scale;
+        f[4 * i + 3] = c.y * scale;
+    }
+    uint32_t o[8];
+    if constexpr (ESZ == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        store32<WIDE>(dst, o);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(f[8 * h + i]);
+            store32<WIDE>((char *)dst + 32 * h, o);
         }
     }
 }
 
-template <int ESZ>
+template <int ESZ, bool WIDE>
 __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvParams p, int rows_per, int check_blocks) {
     const int tid = threadIdx.x, lane = tid & 31, bs = p.c.page_size, D = p.c.head_dim, H = p.c.num_heads;
     if ((int)blockIdx.x < check_blocks) {
@@ -241,7 +289,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvParams p, i
                 const int v = v0 + u * kGatherThreads;
                 page[u] = -2;
                 if (v >= total) continue;
-                const int r = v / vpr, i = v - r * vpr, h = i / vph, c = i - h * vph;
+                const int r = nr > 1 ? quotient(v, p.per_row) : 0, i = v - r * vpr, h = quotient(i, p.per_head), c = i - h * vph;
                 page[u] = s_page[r];
                 if (page[u] >= 0) {
                     q[u] = ld_stream_v4(codes + (int64_t)page[u] * p.c.page_stride + (int64_t)h * p.c.head_stride +
@@ -258,7 +306,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvParams p, i
                     s[u] = 1.f;
                 }
                 // rows, heads and 16-element vectors are contiguous in the output
-                store16<ESZ>((char *)p.dst[kv] + ((int64_t)r0 * vpr + v) * 16 * ESZ, q[u], s[u]);
+                store16<ESZ, WIDE>((char *)p.dst[kv] + ((int64_t)r0 * vpr + v) * 16 * ESZ, q[u], s[u]);
             }
         }
     }
@@ -301,18 +349,18 @@ extern "C" int spec_kv_append(const spec_kv_cache *cache, const void *k, const v
     p.ld_table = ld_table;
     p.n_tokens = n_tokens;
     p.max_new = max_new;
+    p.per_token = divisor(cache->head_dim / 8);
+    p.per_head = divisor(cache->head_dim / 16);
     // pages max_new tokens can touch, whatever slot the first one has
     const int bs = cache->page_size;
     const int pages = (int)(((int64_t)max_new + bs - 2) / bs) + 1;
     const dim3 grid(pages, cache->num_heads, 2 * B);
-    const int most = max_new < bs ? max_new : bs;
-    const int threads = most * cache->head_dim > 128 * 8 * kHeld ? 256 : 128;
     const bool vec = !(((uintptr_t)k | (uintptr_t)v) & 15) && !((ld_k * esz) & 15) && !((ld_v * esz) & 15);
     const cudaStream_t s = (cudaStream_t)cuda_stream;
-    if (esz == 2 && vec) kv_append_kernel<2, true><<<grid, threads, 0, s>>>(p);
-    else if (esz == 2) kv_append_kernel<2, false><<<grid, threads, 0, s>>>(p);
-    else if (vec) kv_append_kernel<4, true><<<grid, threads, 0, s>>>(p);
-    else kv_append_kernel<4, false><<<grid, threads, 0, s>>>(p);
+    if (esz == 2 && vec) kv_append_kernel<2, true><<<grid, kAppendThreads, 0, s>>>(p);
+    else if (esz == 2) kv_append_kernel<2, false><<<grid, kAppendThreads, 0, s>>>(p);
+    else if (vec) kv_append_kernel<4, true><<<grid, kAppendThreads, 0, s>>>(p);
+    else kv_append_kernel<4, false><<<grid, kAppendThreads, 0, s>>>(p);
     return launch_status();
 }
 
@@ -343,6 +391,8 @@ extern "C" int spec_kv_gather(const spec_kv_cache *cache, int B, const int32_t *
     p.ld_table = ld_table;
     p.n_tokens = n_out;
     p.max_new = 0x7fffffff;
+    p.per_head = divisor(cache->head_dim / 16);
+    p.per_row = divisor((uint32_t)cache->num_heads * (cache->head_dim / 16));
     // about 1024 vectors of 16 codes a CTA, keys and values each
     const int vpr = cache->num_heads * (cache->head_dim / 16);
     int rows = 1024 / vpr;
@@ -350,7 +400,10 @@ extern "C" int spec_kv_gather(const spec_kv_cache *cache, int B, const int32_t *
     const int check = (B + 7) / 8;
     const unsigned grid = (unsigned)(check + (n_out + (int64_t)rows - 1) / rows);
     const cudaStream_t s = (cudaStream_t)cuda_stream;
-    if (dtype == SPEC_BF16) kv_gather_kernel<2><<<grid, kGatherThreads, 0, s>>>(p, rows, check);
-    else kv_gather_kernel<4><<<grid, kGatherThreads, 0, s>>>(p, rows, check);
+    const bool wide = !(((uintptr_t)out_k | (uintptr_t)out_v) & 31);
+    if (dtype == SPEC_BF16 && wide) kv_gather_kernel<2, true><<<grid, kGatherThreads, 0, s>>>(p, rows, check);
+    else if (dtype == SPEC_BF16) kv_gather_kernel<2, false><<<grid, kGatherThreads, 0, s>>>(p, rows, check);
+    else if (wide) kv_gather_kernel<4, true><<<grid, kGatherThreads, 0, s>>>(p, rows, check);
+    else kv_gather_kernel<4, false><<<grid, kGatherThreads, 0, s>>>(p, rows, check);
     return launch_status();
 }

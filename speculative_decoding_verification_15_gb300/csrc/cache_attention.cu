@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         auto values = [&](int g) {
             const int seq = 2 * g + 1, slot = seq % NS;
             wait(&sm.full[slot], (seq / NS) & 1);
-            wait(&sm.p_full, g & 1);
+            wait_long(&sm.p_full, g & 1);
             if (gone()) return;
             tc_fence_after();
             const uint64_t a = dv + slot * (kSlotBytes / 16);
@@ -1039,13 +1039,21 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     acc[r + 3] = b.y;
                 }
             };
+            const bool idle = r0 >= x.nrows;  // none of this group's rows: it only keeps step
             for (int i = t0; i < t1; ++i, ++g) {
                 const int buf = g & 1, inf = g % kInfo, j0 = x.tile(i) * kTile, j = j0 + t128;
+                const bool masked = j0 + kTile - 1 > clear_hi || (j0 < clear_lo && j0 + kTile > p.sinks);
                 if (i + 1 == t1) {
                     wait(&sm.part_full[(n + 1) % kParts], ((n + 1) / kParts) & 1);
                     if (next.b >= 0) start_queries<R>(p, next, sm, tid, (n + 1) & 1);
                 }
                 wait(&sm.s_full[buf], (g >> 1) & 1);
+                if (idle) {
+                    if (masked && C::kGroups > 1) named_sync<C::kSoft>(kLookBar);
+                    if (i > t0) wait(&sm.o_full, (g - 1) & 1);
+                    if (lane == 0) mbar_arrive(&sm.p_full);
+                    continue;
+                }
                 const float ks = sm.ks[inf][t128 >> bs_shift], gv = sm.gv[inf][t128 >> bs_shift], wv = sm.wv[inf];
                 tc_fence_after();
                 uint32_t s[NR], s1[NR];
@@ -1060,7 +1068,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     v[r] = f.x;
                     v[r + 1] = f.y;
                 }
-                if (j0 + kTile - 1 > clear_hi || (j0 < clear_lo && j0 + kTile > p.sinks)) {
+                if (masked) {
                     // Some row does not see some token of the tile.  Rows are token-major,
                     // so the rows that see token j are an interval: from the first at a
                     // position >= j to the last at a position < j + window.
@@ -1176,7 +1184,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
             named_sync<C::kSoft>(kAllBar);  // every warp has the last scores: the queries may go
             if (next.b >= 0) store_queries<R>(p.scale_log2, next.nrows, D, sm, tid);
             wait(&sm.o_full, (g - 1) & 1);
-            add_values(g - 1, moved, alpha);
+            if (!idle) add_values(g - 1, moved, alpha);
             tc_fence_before();
             const float lt = warp_sum_scatter<NR>(l, lane);
             if (lane < NR) sm.red[0][w4][r0 + lane] = lt;

@@ -6,7 +6,7 @@ manages tensors.  Shapes follow the C ABI: target logits [B, K+1, V], draft logi
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 import threading
 
 import torch
@@ -229,17 +229,23 @@ def verify_sample_host(target_h, draft_h, tokens_h, temperature_h, seed: int, st
 
 # ------------------------------------------------------------------ 8-bit paged key/value cache
 _attn_ws: dict[tuple[int, int], torch.Tensor] = {}
-_HERE = contextlib.nullcontext()
+_I32, _F32 = torch.int32, torch.float32
 
 
-def _on(stream):
-    """Run what the call itself allocates and converts on the stream it launches on."""
-    return _HERE if stream is None else torch.cuda.stream(stream)
+def _on_its_stream(call):
+    """What the call itself allocates and converts belongs to the stream it launches on."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, stream=None, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, stream=stream, **kw)
+    return run
 
 
 def _i32(t, device):
     """int32 and contiguous on the device; as it is where it already is that."""
-    if t is None or (t.dtype is torch.int32 and t.device == device and t.is_contiguous()):
+    if t is None or (t.dtype is _I32 and t.is_contiguous() and t.device == device):
         return t
     return _as_i32(t, device)
 
@@ -269,32 +275,33 @@ def kv_cache(num_pages: int, num_heads: int, page_size: int, head_dim: int, devi
     return KVCache(*(c.view(torch.float8_e4m3fn) for c in codes), *scales)
 
 
+@_on_its_stream
 def kv_append(cache: KVCache, k, v, page_table, cached_len, cu_new, max_new: int, stream=None) -> dict:
     """Quantise the new tokens' keys and values k, v [tokens, heads, head_dim] (bfloat16
     or float32) into the cache in place: request b's rows cu_new[b] .. cu_new[b+1] - 1
     become its positions cached_len[b] ..; max_new bounds the rows of any request.
     Returns status [B]."""
     dev = k.device
-    with _on(stream):
-        out = dict(status=torch.empty(cu_new.numel() - 1, dtype=torch.int32, device=dev))
-        binding.spec_kv_append(cache, k, v, _i32(page_table, dev), _i32(cached_len, dev), _i32(cu_new, dev),
-                               max_new, out["status"], stream)
-    return out
+    status = torch.empty(page_table.shape[0], dtype=_I32, device=dev)
+    binding.spec_kv_append(cache, k, v, _i32(page_table, dev), _i32(cached_len, dev), _i32(cu_new, dev), max_new, status,
+                           stream)
+    return {"status": status}
 
 
+@_on_its_stream
 def kv_gather(cache: KVCache, page_table, cu_out, n_out: int, first=None, dtype=torch.bfloat16, stream=None) -> dict:
     """Read the cache back: rows cu_out[b] .. cu_out[b+1] - 1 of k and v [n_out, heads,
     head_dim] are request b's positions from first[b] (None: 0).  Returns k, v, status."""
     dev = cache.k.device
-    shape = (n_out, cache.k.shape[1], cache.k.shape[3])
-    with _on(stream):
-        out = dict(k=torch.empty(shape, dtype=dtype, device=dev), v=torch.empty(shape, dtype=dtype, device=dev),
-                   status=torch.empty(cu_out.numel() - 1, dtype=torch.int32, device=dev))
-        binding.spec_kv_gather(cache, _i32(page_table, dev), _i32(cu_out, dev), _i32(first, dev), out["k"],
-                               out["v"], out["status"], stream)
-    return out
+    _, heads, _, dim = cache.k.shape
+    k = torch.empty((n_out, heads, dim), dtype=dtype, device=dev)
+    v = torch.empty((n_out, heads, dim), dtype=dtype, device=dev)
+    status = torch.empty(page_table.shape[0], dtype=_I32, device=dev)
+    binding.spec_kv_gather(cache, _i32(page_table, dev), _i32(cu_out, dev), _i32(first, dev), k, v, status, stream)
+    return {"k": k, "v": v, "status": status}
 
 
+@_on_its_stream
 def cache_attention(q, cache: KVCache, page_table, seq_len, cu_query, max_query: int, scale: float | None = None,
                     window: int = 0, sinks: int = 0, want_lse: bool = False, stream=None) -> dict:
     """Attention of the new tokens' queries q [tokens, query heads, head_dim] over the
@@ -304,12 +311,11 @@ def cache_attention(q, cache: KVCache, page_table, seq_len, cu_query, max_query:
     defaults to head_dim ** -0.5.  Returns out, lse (None unless want_lse), status."""
     dev = q.device
     n, heads, dim = q.shape
-    with _on(stream):
-        out = dict(out=torch.empty((n, heads, dim), dtype=q.dtype, device=dev),
-                   lse=torch.empty((n, heads), dtype=torch.float32, device=dev) if want_lse else None,
-                   status=torch.empty(cu_query.numel() - 1, dtype=torch.int32, device=dev))
-        nbytes = binding.spec_cache_attention_workspace_size(heads, cache.k.shape[1], dim, binding._dtype_code(q))
-        binding.spec_cache_attention(q, cache, _i32(page_table, dev), _i32(seq_len, dev), _i32(cu_query, dev),
-                                     max_query, dim ** -0.5 if scale is None else scale, window, sinks, out["out"],
-                                     out["lse"], out["status"], _attention_workspace(dev, stream, nbytes), stream)
-    return out
+    out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+    lse = torch.empty((n, heads), dtype=_F32, device=dev) if want_lse else None
+    status = torch.empty(page_table.shape[0], dtype=_I32, device=dev)
+    nbytes = binding.spec_cache_attention_workspace_size(heads, cache.k.shape[1], dim, binding._dtype_code(q))
+    binding.spec_cache_attention(q, cache, _i32(page_table, dev), _i32(seq_len, dev), _i32(cu_query, dev), max_query,
+                                 dim ** -0.5 if scale is None else scale, window, sinks, out, lse, status,
+                                 _attention_workspace(dev, stream, nbytes), stream)
+    return {"out": out, "lse": lse, "status": status}

@@ -501,30 +501,33 @@ def spec_schedule_threshold(conf, max_len, threshold: float, out_len, stream=Non
 
 
 # The cache calls run once a layer and decoding step, so their checks cost little: each
-# tensor's attributes are read once, and the device is made current only if it is not.
-def _cache_struct(cache, device) -> _CacheStruct:
+# tensor's attributes are read once, devices are compared by index (-1 is the CPU), and
+# the device is made current only if it is not.
+def _cache_struct(cache, index: int) -> _CacheStruct:
     k, v, ks, vs = cache
     shape, strides, dtype = k.shape, k.stride(), k.dtype
     if len(shape) != 4 or v.shape != shape or v.stride() != strides or v.dtype is not dtype:
         raise ValueError("cache keys and values must be [pages, heads, page_size, head_dim] of one layout")
     if dtype is not torch.float8_e4m3fn and dtype is not torch.uint8:
         raise TypeError(f"cache codes must be float8_e4m3fn (or their bytes), got {dtype}")
-    if strides[3] != 1:
+    pages, heads, size, dim = shape
+    page_stride, head_stride, token_stride, last = strides
+    if last != 1:
         raise ValueError("cache codes must have head_dim contiguous")
-    if k.device != device or v.device != device:
-        raise ValueError(f"the cache must be on {device}")
-    scales = shape[:2]
-    for t, name in ((ks, "k_scale"), (vs, "v_scale")):
-        if t.shape != scales or t.dtype is not torch.float32 or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 [pages, heads] tensor on {device}")
-    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), strides[0], strides[1], strides[2],
-                        shape[0], shape[2], shape[1], shape[3])
+    if index < 0 or not k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == index:
+        raise ValueError("the cache and the call's tensors must be on one CUDA device")
+    scales = (pages, heads)
+    if (ks.shape != scales or vs.shape != scales or ks.dtype is not torch.float32 or vs.dtype is not torch.float32
+            or not ks.is_contiguous() or not vs.is_contiguous()):
+        raise ValueError("k_scale and v_scale must be contiguous float32 [pages, heads]")
+    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), page_stride, head_stride,
+                        token_stride, pages, size, heads, dim)
 
 
-def _token_rows(t, name, heads, dim, device) -> int:
+def _token_rows(t, name, heads, dim, index: int) -> int:
     """Row stride of [tokens, heads, dim] rows whose heads are contiguous."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the cache's device")
     shape, strides = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
@@ -536,91 +539,86 @@ def _token_rows(t, name, heads, dim, device) -> int:
     return ld
 
 
-def _ints(t, name, shape, device) -> int:
-    """Address of a contiguous int32 tensor of the given shape."""
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 {tuple(shape)} tensor on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _flat(t, name, dtype, shape, index: int) -> int:
+    """Address of a contiguous tensor of the given type and shape."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on the cache's device, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _table(t, B, device):
-    if t.dim() != 2:
-        raise ValueError("page_table must be [B, pages a request]")
-    return _ints(t, "page_table", (B, t.shape[1]), device), t.shape[1]
-
-
-def _launch(name: str, device, stream, *args) -> None:
-    lib = load()
+def _launch(name: str, index: int, stream, *args) -> None:
+    lib = _lib or load()
     if stream is None:
-        at = torch._C._cuda_getCurrentRawStream(device.index)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        at = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     else:
         at = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == index:
         rc = getattr(lib, name)(*args, at)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = getattr(lib, name)(*args, at)
     if rc != SPEC_OK:
         raise SpecError(name, rc, lib)
 
 
+_I32 = torch.int32
+
+
 def spec_kv_append(cache, k, v, page_table, cached_len, cu_new, max_new: int, out_status, stream=None) -> None:
     """k, v [tokens, heads, head_dim]; cached_len [B]; cu_new [B + 1]; out_status [B]."""
-    dev = k.device
-    c = _cache_struct(cache, dev)
-    ldk = _token_rows(k, "k", c.num_heads, c.head_dim, dev)
-    ldv = _token_rows(v, "v", c.num_heads, c.head_dim, dev)
-    n = k.shape[0]
+    at = k.get_device()
+    c = _cache_struct(cache, at)
+    heads, dim, n = c.num_heads, c.head_dim, k.shape[0]
+    ldk = _token_rows(k, "k", heads, dim, at)
+    ldv = _token_rows(v, "v", heads, dim, at)
     if v.dtype is not k.dtype or v.shape[0] != n:
         raise ValueError("k and v must share tokens and dtype")
-    B = cu_new.numel() - 1
-    table, width = _table(page_table, B, dev)
-    _launch("spec_kv_append", dev, stream, c, k.data_ptr(), v.data_ptr(), _dtype_code(k), ldk, ldv, n, B,
-            _ints(cu_new, "cu_new", (B + 1,), dev), max_new, _ints(cached_len, "cached_len", (B,), dev), table, width,
-            _ints(out_status, "out_status", (B,), dev))
+    B, width = page_table.shape
+    _launch("spec_kv_append", at, stream, c, k.data_ptr(), v.data_ptr(), _dtype_code(k), ldk, ldv, n, B,
+            _flat(cu_new, "cu_new", _I32, (B + 1,), at), max_new, _flat(cached_len, "cached_len", _I32, (B,), at),
+            _flat(page_table, "page_table", _I32, (B, width), at), width, _flat(out_status, "out_status", _I32, (B,), at))
 
 
 def spec_kv_gather(cache, page_table, cu_out, first, out_k, out_v, out_status, stream=None) -> None:
     """out_k, out_v [rows, heads, head_dim]; cu_out [B + 1]; first [B] or None; out_status [B]."""
-    dev = out_k.device
-    c = _cache_struct(cache, dev)
-    n = out_k.shape[0]
-    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
-        _need(t, name, out_k.dtype, (n, c.num_heads, c.head_dim), dev)
-    B = cu_out.numel() - 1
-    table, width = _table(page_table, B, dev)
-    _launch("spec_kv_gather", dev, stream, c, B, _ints(cu_out, "cu_out", (B + 1,), dev), n,
-            None if first is None else _ints(first, "first", (B,), dev), table, width, out_k.data_ptr(),
-            out_v.data_ptr(), _dtype_code(out_k), _ints(out_status, "out_status", (B,), dev))
+    at = out_k.get_device()
+    c = _cache_struct(cache, at)
+    n, dtype = out_k.shape[0], out_k.dtype
+    rows = (n, c.num_heads, c.head_dim)
+    B, width = page_table.shape
+    _launch("spec_kv_gather", at, stream, c, B, _flat(cu_out, "cu_out", _I32, (B + 1,), at), n,
+            None if first is None else _flat(first, "first", _I32, (B,), at),
+            _flat(page_table, "page_table", _I32, (B, width), at), width, _flat(out_k, "out_k", dtype, rows, at),
+            _flat(out_v, "out_v", dtype, rows, at), _dtype_code(out_k), _flat(out_status, "out_status", _I32, (B,), at))
 
 
 def spec_cache_attention_workspace_size(num_query_heads: int, num_heads: int, head_dim: int, dtype: int) -> int:
-    return load().spec_cache_attention_workspace_size(num_query_heads, num_heads, head_dim, dtype)
+    return (_lib or load()).spec_cache_attention_workspace_size(num_query_heads, num_heads, head_dim, dtype)
 
 
 def spec_cache_attention(q, cache, page_table, seq_len, cu_query, max_query: int, scale: float, window: int,
                          sinks: int, out, out_lse, out_status, workspace, stream=None) -> None:
     """q, out [tokens, query heads, head_dim]; seq_len [B]; cu_query [B + 1]; out_lse
     [tokens, query heads] float32 or None; out_status [B]; workspace zeroed once."""
-    dev = q.device
-    c = _cache_struct(cache, dev)
-    if q.dim() != 3:
-        raise ValueError(f"q must be [tokens, query heads, head_dim], got {tuple(q.shape)}")
-    n, heads, dim = q.shape
-    ldq = _token_rows(q, "q", heads, c.head_dim, dev)
-    _need(out, "out", q.dtype, (n, heads, dim), dev)
-    if out_lse is not None:
-        _need(out_lse, "out_lse", torch.float32, (n, heads), dev)
-    B = cu_query.numel() - 1
-    table, width = _table(page_table, B, dev)
-    _need(workspace, "workspace", torch.uint8, None, dev)
-    _launch("spec_cache_attention", dev, stream, c, q.data_ptr(), _dtype_code(q), ldq, heads, n, B,
-            _ints(cu_query, "cu_query", (B + 1,), dev), max_query, _ints(seq_len, "seq_len", (B,), dev), table, width,
-            scale, window, sinks, out.data_ptr(), None if out_lse is None else out_lse.data_ptr(),
-            _ints(out_status, "out_status", (B,), dev), workspace.data_ptr(), workspace.numel())
+    at = q.get_device()
+    c = _cache_struct(cache, at)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
+        raise ValueError(f"q must be [tokens, query heads, head_dim], got {tuple(shape)}")
+    n, heads, _ = shape
+    ldq = _token_rows(q, "q", heads, c.head_dim, at)
+    B, width = page_table.shape
+    nbytes = workspace.numel()
+    _launch("spec_cache_attention", at, stream, c, q.data_ptr(), _dtype_code(q), ldq, heads, n, B,
+            _flat(cu_query, "cu_query", _I32, (B + 1,), at), max_query, _flat(seq_len, "seq_len", _I32, (B,), at),
+            _flat(page_table, "page_table", _I32, (B, width), at), width, scale, window, sinks,
+            _flat(out, "out", dtype, shape, at),
+            None if out_lse is None else _flat(out_lse, "out_lse", torch.float32, (n, heads), at),
+            _flat(out_status, "out_status", _I32, (B,), at), _flat(workspace, "workspace", torch.uint8, (nbytes,), at),
+            nbytes)
 
 
 def profile_enable(on: bool) -> None:

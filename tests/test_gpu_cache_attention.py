@@ -247,3 +247,71 @@ def test_pages_past_4_gib():
     c = pkg.KVCache(k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), ks, vs)
     out = _run(x, c, table=at.cpu().numpy()[None])
     _check(x, out)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(8, 2, 8), (2, 2, 8), (16, 2, 8)])
+def test_many_tiles_a_cta(Hq, Hkv, n):
+    """Enough tiles for every CTA to hold several items and cut two: row tiles of 16, 32
+    and 64 rows."""
+    lens = 700 + (np.arange(60) * 97) % 900
+    x = U.Inputs(25, lens, np.full(60, n), Hq, Hkv, 64, 64, BF16)
+    c = x.cache()
+    a, b = _run(x, c), _run(x, c)
+    assert torch.equal(a["out"], b["out"])
+    _check(x, a)
+    w = _run(x, c, window=300, sinks=20)
+    _check(x, w, window=300, sinks=20)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_queries_at_any_element(dtype):
+    """Query rows that are not 16-byte aligned."""
+    x = U.Inputs(26, [90, 300], [3, 4], 6, 2, 80, 32, dtype)
+    flat = torch.empty(7 * 491 + 1, dtype=dtype, device="cuda")
+    q = flat[1:].view(7, 491)[:, :480].view(7, 6, 80)
+    q.copy_(x.q)
+    x.q = q
+    _check(x, _run(x))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_any_scales(dtype):
+    """Scales that are not powers of two, as another writer of the cache may have left."""
+    x = U.Inputs(27, [400, 77], [2, 5], 8, 2, 128, 16, dtype)
+    g = np.random.default_rng(27)
+    x.ks = np.float32(x.ks * g.uniform(0.6, 1.7, x.ks.shape)).astype(np.float64)
+    x.vs = np.float32(x.vs * g.uniform(0.6, 1.7, x.vs.shape)).astype(np.float64)
+    _check(x, _run(x))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_query_stays_in_its_row(dtype, bad):
+    x = U.Inputs(28, [300], [5], 8, 2, 64, 64, dtype)
+    clean = x.q64()
+    x.q = x.q.clone()
+    x.q[2, 3, 9] = bad
+    g = _run(x)["out"].double().cpu().numpy()
+    assert np.isnan(g[2, 3]).all()
+    ref, _, tol, _ = U.attention(clean, x.kc, x.vc, x.ks, x.vs, x.table, x.lens, x.cu, 64 ** -0.5, bf16=dtype == BF16)
+    keep = np.ones(g.shape[:2], bool)
+    keep[2, 3] = False
+    assert (np.abs(g - ref)[keep] <= tol[keep]).all()
+
+
+def test_large_and_small_query_rows_together():
+    """Rows of one row tile whose magnitudes differ by 2^40: each keeps its own scale."""
+    x = U.Inputs(29, [200], [4], 8, 1, 128, 64, BF16)
+    x.q = (x.q.float() * (2.0 ** torch.arange(-20, 12, device="cuda").float()).view(4, 8, 1)).to(BF16)
+    x.q[0, 0] = 0
+    _check(x, _run(x))
+
+
+def test_more_requests_than_threads():
+    g = np.random.default_rng(30)
+    new = g.integers(0, 3, 5000)
+    lens = new + g.integers(0, 20, 5000)
+    x = U.Inputs(30, lens, new, 2, 1, 16, 16, BF16)
+    out = _run(x)
+    assert (out["status"] == 0).all()
+    _check(x, out)

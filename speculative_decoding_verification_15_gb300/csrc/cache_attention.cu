@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
 #pragma unroll
                 for (int r = 0; r < NR; r += 4) {
                     const float4 f = make_float4(redux_max(v[r]), redux_max(v[r + 1]), redux_max(v[r + 2]), redux_max(v[r + 3]));
-                    if (lane == 0) *(float4 *)&sm.red[buf][w4][r0 + r] = f;
+                    *(float4 *)&sm.red[buf][w4][r0 + r] = f;  // every lane the same: no branch
                 }
                 named_sync<128>(bar);
                 {
@@ -1126,21 +1126,17 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                     const float ref = some ? mt * c : 0.f, mm = some ? ref : kNegInf;
                     const bool moves = mm > m_run + kRefStep;  // also from -inf
                     moved_last = moved;
-                    moved = __any_sync(0xffffffffu, moves);
                     alpha_last = alpha;
-                    alpha = 1.f;
-                    if (moves) {
-                        alpha = m_run == kNegInf ? 0.f : ex2_approx(m_run - mm);
-                        m_run = mm;
-                    }
+                    moved = __any_sync(0xffffffffu, moves);
+                    alpha = moves ? ex2_approx(m_run - mm) : 1.f;  // 0 from -inf
+                    m_run = moves ? mm : m_run;
                     const float beta = some ? ex2_approx(mm - m_run) : 1.f;
-                    if (lane < NR) {
-                        float *cm = (float *)&sm.cm[warp][buf][k >> 1];
-                        cm[k & 1] = c;
-                        cm[2 + (k & 1)] = -ref;
-                        sm.beta[warp][buf][k] = beta;
-                        sm.w[warp][buf][k] = beta * wv;
-                    }
+                    // with 16 rows, lanes 16 .. 31 write what lanes 0 .. 15 do
+                    float *cm = (float *)&sm.cm[warp][buf][k >> 1];
+                    cm[k & 1] = c;
+                    cm[2 + (k & 1)] = -ref;
+                    sm.beta[warp][buf][k] = beta;
+                    sm.w[warp][buf][k] = beta * wv;
                     __syncwarp();
                 }
                 if (moved) {

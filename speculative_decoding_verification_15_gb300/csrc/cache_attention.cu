@@ -651,19 +651,23 @@ __device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 __device__ __noinline__ bool poll_barrier(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = global_ns();
-    for (uint32_t n = 0;; ++n) {
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
         if (try_barrier(bar, parity)) return true;
-        if ((n & 255) == 255 && global_ns() - t0 > kWaitNs) return false;
+        if ((n & 255) == 0) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > kWaitNs) return false;
+        }
     }
 }
 
-template <int R>
+template <int R, int W>  // rows of a tile, warps that copy
 struct TcShape {
     static constexpr int kRowsG = 16;                     // rows of a softmax group
     static constexpr int kGroups = R / kRowsG;            // groups of 128 threads
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
-    static constexpr int kThreads = kSoft + 64;
+    static constexpr int kThreads = kSoft + 32 * (1 + W);
     static constexpr int kPerSM = R < 64 ? 2 : 1;         // CTAs an SM
     static constexpr int kSlots = R < 64 ? 5 : 10;
     static constexpr uint32_t kCols = 8 * R;              // S^T and O^T, two terms and two buffers each
@@ -674,7 +678,7 @@ constexpr int kAllBar = 8, kLookBar = 9;  // named barriers of all softmax threa
 
 template <int R>
 struct TcShared {
-    using C = TcShape<R>;
+    using C = TcShape<R, 1>;
     uint8_t ring[C::kSlots][kSlotBytes];
     uint8_t q[2][R * 128];             // two terms, rows of 128 bytes, swizzled
     uint16_t q_raw[R][128];            // the next part's, as they are stored
@@ -683,7 +687,7 @@ struct TcShared {
     uint64_t part_full[kParts], part_empty[kParts];
     Part part[kParts];                      // b < 0: no more
     float ks[kInfo][8], gv[kInfo][8], wv[kInfo];  // a tile's scales
-    int pages[8];                                 // and its pages, for the copies
+    int pages[2][8];                              // and its pages, for the copies of keys and of values
     // every softmax warp's own copy, by the tile's parity: row pairs' score factors and
     // minus references, weights of the row sums and of O^T
     float4 cm[4 * C::kGroups][2][C::kRowsG / 2];
@@ -732,7 +736,7 @@ __device__ __forceinline__ float warp_sum_scatter(float (&v)[N], int lane) {
 // store_queries makes two e4m3 terms of each entry for the products.
 template <int R>
 struct QueryShape {
-    static constexpr int kCols = R * 128 / TcShape<R>::kSoft, kPerRow = 128 / kCols;
+    static constexpr int kCols = R * 128 / TcShape<R, 1>::kSoft, kPerRow = 128 / kCols;
 };
 
 template <int R>
@@ -801,10 +805,10 @@ __device__ __noinline__ void store_queries(float scale_log2, int nrows, int D, T
     if ((tid & 31) == 0) mbar_arrive(&sm.q_full);
 }
 
-template <int R>
-__global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
+template <int R, int W>
+__global__ void __launch_bounds__(TcShape<R, W>::kThreads, TcShape<R, W>::kPerSM)
     attention_tc_kernel(AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using C = TcShape<R>;
+    using C = TcShape<R, W>;
     constexpr int NR = C::kRowsG, NS = C::kSlots;
     extern __shared__ __align__(1024) uint8_t raw[];
     TcShared<R> &sm = *reinterpret_cast<TcShared<R> *>(raw);
@@ -822,7 +826,7 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         mbar_init(&sm.q_full, C::kSoft / 32);
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sm.part_full[i], 1);
-            mbar_init(&sm.part_empty[i], 1 + C::kSoft / 32);
+            mbar_init(&sm.part_empty[i], W + C::kSoft / 32);  // the readers
         }
         mbar_init_fence();
     }
@@ -837,16 +841,53 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         __syncwarp();
     };
     auto wait_long = [&](uint64_t *bar, int parity) {
-        if (!dead && !mbar_wait(bar, parity, kWaitNs)) dead = true;
+        if (!try_barrier(smem_addr(bar), parity) && !dead && !poll_barrier(smem_addr(bar), parity)) dead = true;
         __syncwarp();
+    };
+
+    auto gone = [&] {
+        dead = __any_sync(0xffffffffu, dead);
+        return dead;
+    };
+    // The copying warps: a batch is the tiles whose pages fill a warp's lanes.
+    const int bs = p.c.page_size, shift = 31 - __clz(kTile / bs), ppt = 1 << shift, batch = 32 >> shift;
+    auto fetch_page = [&](const Part &x, int i0) {
+        const int i = i0 + (lane >> shift);
+        if (i >= x.t1) return -1;
+        const int j = x.tile(i) * kTile + (lane & (ppt - 1)) * bs;
+        if (j >= x.r.len || (j + bs <= x.r.low && j >= x.r.sinks)) return -1;
+        const int page = p.table[(int64_t)x.b * p.ld_table + j / bs];
+        return page < p.c.num_pages ? page : -1;
+    };
+    int sent = 0;  // past the last slot this warp filled
+    auto copy_tile = [&](const CUtensorMap &map, int seq, int page, int h, int *pages) {
+        const int slot = seq % NS, turn = seq / NS;
+        if (turn > 0) wait_long(&sm.empty[slot], (turn - 1) & 1);
+        if (gone()) return;
+        sent = seq + 1;
+        if (lane < ppt) pages[lane] = page >= 0 ? page : p.c.num_pages;  // past the map's end: reads as zeros
+        __syncwarp();
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&sm.full[slot], kSlotBytes);
+#pragma unroll 4
+            for (int i = 0; i < ppt; ++i)
+                tma_load_4d(sm.ring[slot] + i * bs * 128, &map, 0, 0, h, pages[i], &sm.full[slot]);
+        }
+        __syncwarp();
+    };
+    // After a wait that ran out: none of this warp's copies may be in flight when the CTA ends.
+    auto drain = [&] {
+        if (gone())
+            for (int i = max(0, sent - NS); i < sent; ++i)
+                if (W == 1 || ((sent - i) & 1)) mbar_wait(&sm.full[i % NS], (i / NS) & 1, kWaitNs);
     };
 
     if (warp == C::kSoft / 32) {
         // ---------------------------------------------------------------- copies
-        // This warp also finds the parts and tells the others, one part ahead; page ids
-        // and scales come a batch of 32 pages ahead.
-        const int bs = p.c.page_size, shift = 31 - __clz(kTile / bs), ppt = 1 << shift, batch = 32 >> shift;
-        int seq = 0, g = 0, n = 0;  // slots filled, tiles, parts told
+        // Of the keys, and of the values if no second warp copies.  This warp also finds
+        // the parts and tells the others, one part ahead; page ids and scales come a batch
+        // of 32 pages ahead.
+        int g = 0, n = 0;  // tiles, parts told
         auto tell_part = [&](const Part &x) {
             const int at = n % kParts;
             if (n >= kParts) wait(&sm.part_empty[at], (n / kParts - 1) & 1);
@@ -856,14 +897,6 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                 mbar_arrive(&sm.part_full[at]);
             }
             ++n;
-        };
-        auto fetch_page = [&](const Part &x, int i0) {
-            const int i = i0 + (lane >> shift);
-            if (i >= x.t1) return -1;
-            const int j = x.tile(i) * kTile + (lane & (ppt - 1)) * bs;
-            if (j >= x.r.len || (j + bs <= x.r.low && j >= x.r.sinks)) return -1;
-            const int page = p.table[(int64_t)x.b * p.ld_table + j / bs];
-            return page < p.c.num_pages ? page : -1;
         };
         auto fetch_scale = [&](const float *s, const Part &x, int page) {
             return page >= 0 ? __ldg(s + (int64_t)page * p.c.num_heads + x.h) : 0.f;
@@ -883,39 +916,26 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
             page = page_n;
             ks = ks_n;
             vs = vs_n;
-            for (int k = 0; k < batch && i0 + k < x.t1 && !dead; ++k, ++g) {
-                const int from = (k << shift) + (lane & (ppt - 1));
-                const int pg = __shfl_sync(0xffffffffu, page, from);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++seq) {
-                    const int slot = seq % NS, turn = seq / NS;
-                    if (turn > 0) wait_long(&sm.empty[slot], (turn - 1) & 1);
-                    dead = __any_sync(0xffffffffu, dead);
+            for (int k = 0; k < batch && i0 + k < x.t1; ++k, ++g) {
+                const int from = (k << shift) + (lane & (ppt - 1)), seq = 2 * g, slot = seq % NS;
+                copy_tile(kmap, seq, __shfl_sync(0xffffffffu, page, from), x.h, sm.pages[0]);
+                if (dead) break;
+                // the scales may still be on their way here
+                const float tks = __shfl_sync(0xffffffffu, ks, from), tvs = __shfl_sync(0xffffffffu, vs, from);
+                float top = tvs;
+                for (int s = 1; s < ppt; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                const int at = g % kInfo;
+                if (lane < ppt) {
+                    sm.ks[at][lane] = tks;
+                    sm.gv[at][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
+                }
+                if (lane == 0) sm.wv[at] = top * (1.f / 256.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.full[slot]);
+                if constexpr (W == 1) {
+                    copy_tile(vmap, seq + 1, __shfl_sync(0xffffffffu, page, from), x.h, sm.pages[0]);
                     if (dead) break;
-                    if (kv == 0) {
-                        if (lane < ppt) sm.pages[lane] = pg >= 0 ? pg : p.c.num_pages;  // past the map's end: reads as zeros
-                        __syncwarp();
-                    }
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&sm.full[slot], kSlotBytes);
-#pragma unroll 4
-                        for (int i = 0; i < ppt; ++i)
-                            tma_load_4d(sm.ring[slot] + i * bs * 128, kv ? &vmap : &kmap, 0, 0, x.h, sm.pages[i],
-                                        &sm.full[slot]);
-                    }
-                    if (kv == 0) {  // the scales may still be on their way here
-                        const float tks = __shfl_sync(0xffffffffu, ks, from), tvs = __shfl_sync(0xffffffffu, vs, from);
-                        float top = tvs;
-                        for (int s = 1; s < ppt; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-                        const int at = g % kInfo;
-                        if (lane < ppt) {
-                            sm.ks[at][lane] = tks;
-                            sm.gv[at][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
-                        }
-                        if (lane == 0) sm.wv[at] = top * (1.f / 256.f);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.full[slot]);
+                    if (lane == 0) mbar_arrive(&sm.full[(seq + 1) % NS]);
                 }
                 if (k == 0) {  // the next batch, of this part or of the next
                     if (i0 + batch < x.t1) {
@@ -933,8 +953,37 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
                 }
             }
         }
-        if (dead)  // no copy may be in flight when the CTA ends
-            for (int i = max(0, seq - NS); i < seq; ++i) mbar_wait(&sm.full[i % NS], (i / NS) & 1, kWaitNs);
+        drain();
+    } else if (warp == C::kSoft / 32 + 2) {
+        // ---------------------------------------------------------------- copies of values
+        int g = 0;
+        wait(&sm.part_full[0], 0);
+        int page_n = !gone() && sm.part[0].b >= 0 ? fetch_page(sm.part[0], sm.part[0].t0) : -1;
+        for (int n = 0; !gone() && sm.part[n % kParts].b >= 0; ++n) {
+            const Part &x = sm.part[n % kParts], &next = sm.part[(n + 1) % kParts];
+            const int t1 = x.t1, h = x.h;
+            for (int i0 = x.t0; i0 < t1 && !dead; i0 += batch) {
+                const int page = page_n;
+                for (int k = 0; k < batch && i0 + k < t1; ++k, ++g) {
+                    const int seq = 2 * g + 1, from = (k << shift) + (lane & (ppt - 1));
+                    copy_tile(vmap, seq, __shfl_sync(0xffffffffu, page, from), h, sm.pages[1]);
+                    if (dead) break;
+                    if (lane == 0) mbar_arrive(&sm.full[seq % NS]);
+                    if (k == 0) {  // pages of the next batch, of this part or of the next
+                        if (i0 + batch < t1) {
+                            page_n = fetch_page(x, i0 + batch);
+                        } else {
+                            wait(&sm.part_full[(n + 1) % kParts], ((n + 1) / kParts) & 1);
+                            if (gone()) break;
+                            page_n = next.b >= 0 ? fetch_page(next, next.t0) : -1;
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.part_empty[n % kParts]);
+        }
+        drain();
     } else if (warp == C::kSoft / 32 + 1) {
         // ---------------------------------------------------------------- products
         write_statuses(p, lane);  // while the first tile is on its way
@@ -943,7 +992,6 @@ __global__ void __launch_bounds__(TcShape<R>::kThreads, TcShape<R>::kPerSM)
         const uint64_t dk = smem_desc(smem_addr(sm.ring), 16, 1024, 2), dq = smem_desc(smem_addr(sm.q), 16, 1024, 2);
         const uint64_t dv = smem_desc(smem_addr(sm.ring), 1024, 1024, 2);
         const uint64_t dp = smem_desc(smem_addr(sm.p), 128, kTile * 16, 0);
-        auto gone = [&] { return (bool)__any_sync(0xffffffffu, dead); };
         auto scores = [&](int g) {
             const int seq = 2 * g, slot = seq % NS;
             wait(&sm.full[slot], (seq / NS) & 1);
@@ -1250,14 +1298,14 @@ bool codes_map(const spec_kv_cache &c, const void *codes, CUtensorMap *map) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int R>
+template <int R, int W>
 int launch_tc(const AttnParams &p, int dev, int sms, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
-    using C = TcShape<R>;
+    using C = TcShape<R, W>;
     constexpr int bytes = (int)sizeof(TcShared<R>);
     static_assert(C::kPerSM * (bytes + 1024) <= 228 * 1024, "shared memory of an SM");
     static std::atomic<bool> set[64];
     if (!set[dev].load()) {
-        const cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<R, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) {
             note_cuda_error((int)e);
             return SPEC_ECUDA;
@@ -1265,7 +1313,7 @@ int launch_tc(const AttnParams &p, int dev, int sms, const CUtensorMap &kmap, co
         set[dev].store(true);
     }
     const int ctas = C::kPerSM * sms < kMaxCtas ? C::kPerSM * sms : kMaxCtas;
-    attention_tc_kernel<R><<<ctas, C::kThreads, bytes, st>>>(p, kmap, vmap);
+    attention_tc_kernel<R, W><<<ctas, C::kThreads, bytes, st>>>(p, kmap, vmap);
     return launch_status();
 }
 
@@ -1334,9 +1382,16 @@ extern "C" int spec_cache_attention(const spec_kv_cache *cache, const void *q, i
     alignas(64) CUtensorMap kmap, vmap;
     if (esz == 2 && cache->head_dim <= 128 && codes_map(*cache, cache->k, &kmap) && codes_map(*cache, cache->v, &vmap)) {
         const int64_t rows = (int64_t)max_query * p.group;
-        if (rows <= 16) return launch_tc<16>(p, dev, sms, kmap, vmap, st);
-        if (rows <= 32) return launch_tc<32>(p, dev, sms, kmap, vmap, st);
-        return launch_tc<64>(p, dev, sms, kmap, vmap, st);
+        // One warp's copies go one after another, about 5 cycles a row and 20 a copy, so
+        // with small pages a second warp pays: 512 heads of 64 columns, 8192 tokens in
+        // pages of 16, take 113 us with one and 84 with two.  It costs registers: in pages
+        // of 64 the same takes 78 us with one and 82 with two.  With 32 rows there are none
+        // to spare (121 us with one, 172 with two); with 64 and one CTA an SM there are
+        // (205 us with one, 194 with two).
+        if (rows > 32) return launch_tc<64, 2>(p, dev, sms, kmap, vmap, st);
+        if (rows > 16) return launch_tc<32, 1>(p, dev, sms, kmap, vmap, st);
+        if (cache->page_size > 32) return launch_tc<16, 1>(p, dev, sms, kmap, vmap, st);
+        return launch_tc<16, 2>(p, dev, sms, kmap, vmap, st);
     }
     const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
     if (cache->head_dim <= 128) {

@@ -449,8 +449,9 @@ int spec_kv_gather(const spec_kv_cache *cache, int B, const int32_t *cu_out, int
  *              SPEC_STATUS_INTERNAL; rows of a failed request are unspecified
  *  ws          at least spec_cache_attention_workspace_size bytes, 256-byte aligned,
  *              ZERO-FILLED before its first use; every call leaves its counters zero,
- *              so one workspace serves any number of calls in stream order.  The
- *              workspace of another entry point must not be passed here.
+ *              so one workspace serves any number of calls in stream order (after a
+ *              call that reported SPEC_STATUS_INTERNAL, zero it again).  The workspace
+ *              of another entry point must not be passed here.
  * Results are the same from call to call: partial sums are joined in a fixed order.
  */
 size_t spec_cache_attention_workspace_size(int num_query_heads, int num_heads, int head_dim, int dtype);

@@ -251,6 +251,17 @@ __device__ __forceinline__ void named_sync(int bar) {
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(NT) : "memory");
 }
 
+// A barrier of NT threads that tells whether any of them has x.
+template <int NT>
+__device__ __forceinline__ bool named_any(int bar, bool x) {
+    uint32_t any;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(any)
+                 : "r"(bar), "n"(NT), "r"((uint32_t)x)
+                 : "memory");
+    return any != 0;
+}
+
 // A part's slot: the first part of an item is its CTA's last part, every other part
 // its CTA's first, so two slots a CTA are enough.
 __device__ __forceinline__ float *slot_of(const AttnParams &p, int cta, bool first, int rows) {
@@ -1048,12 +1059,13 @@ __global__ void __launch_bounds__(TcShape<R, W>::kThreads, TcShape<R, W>::kPerSM
         // thread without which the phase after it cannot end: parities never alias.
         wait(&sm.part_full[0], 0);
         int g = 0;
-        if (sm.part[0].b >= 0) {
+        bool more = !named_any<C::kSoft>(kAllBar, dead) && sm.part[0].b >= 0;  // the same in every thread
+        if (more) {
             start_queries<R>(p, sm.part[0], sm, tid, 0);
             store_queries<R>(p.scale_log2, sm.part[0].nrows, D, sm, tid);
             named_sync<C::kSoft>(kAllBar);
         }
-        for (int n = 0; sm.part[n % kParts].b >= 0; ++n) {
+        for (int n = 0; more; ++n) {
             const Part &x = sm.part[n % kParts], &next = sm.part[(n + 1) % kParts];
             const int t0 = x.t0, t1 = x.t1;
             // tiles within [clear_lo, clear_hi] hide no token from any row
@@ -1093,7 +1105,7 @@ __global__ void __launch_bounds__(TcShape<R, W>::kThreads, TcShape<R, W>::kPerSM
                 const bool masked = j0 + kTile - 1 > clear_hi || (j0 < clear_lo && j0 + kTile > p.sinks);
                 if (i + 1 == t1) {
                     wait(&sm.part_full[(n + 1) % kParts], ((n + 1) / kParts) & 1);
-                    if (next.b >= 0) start_queries<R>(p, next, sm, tid, (n + 1) & 1);
+                    if (!dead && next.b >= 0) start_queries<R>(p, next, sm, tid, (n + 1) & 1);
                 }
                 wait(&sm.s_full[buf], (g >> 1) & 1);
                 if (idle) {
@@ -1225,8 +1237,11 @@ __global__ void __launch_bounds__(TcShape<R, W>::kThreads, TcShape<R, W>::kPerSM
             }
             // the next part (told before the last tile) sends its queries before this part's
             // last product is waited for
-            named_sync<C::kSoft>(kAllBar);  // every warp has the last scores: the queries may go
-            if (next.b >= 0) store_queries<R>(p.scale_log2, next.nrows, D, sm, tid);
+            // (every warp has the last scores here: the queries may go); after a wait that
+            // ran out anywhere, this part is the CTA's last and the whole call has failed
+            const bool lost = named_any<C::kSoft>(kAllBar, dead);
+            more = !lost && next.b >= 0;
+            if (more) store_queries<R>(p.scale_log2, next.nrows, D, sm, tid);
             wait(&sm.o_full, (g - 1) & 1);
             if (!idle) add_values(g - 1, moved, alpha);
             tc_fence_before();
@@ -1241,7 +1256,8 @@ __global__ void __launch_bounds__(TcShape<R, W>::kThreads, TcShape<R, W>::kPerSM
                 if (p.lse && x.whole && r < x.nrows) store_lse(p, x, x.rt * R + r, m_run, sum);
             }
             named_sync<128>(bar);
-            if (dead) p.status[x.b] = SPEC_STATUS_INTERNAL;
+            if (lost || dead)
+                for (int b = tid; b < p.B; b += C::kSoft) p.status[b] = SPEC_STATUS_INTERNAL;
             if (x.whole) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r)

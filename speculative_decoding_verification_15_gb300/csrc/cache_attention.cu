@@ -93,6 +93,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 struct Share {
     int64_t total, u, end, off;
     int b, ctas, cost;  // cost: units of an item ahead of its tiles
+    int each;           // > 0: every CTA has one part, of `each` tiles at most
 };
 
 __device__ __forceinline__ int64_t share_start(int64_t total, int cta, int ctas) {
@@ -103,8 +104,16 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t u, int ctas) {
     return (int)quotient((u + 1) * ctas - 1, total);
 }
 
+// Few items: an item takes as many CTAs as it has runs of `each` tiles, and every CTA one
+// part, where that keeps `each` within kEachTries - 1 tiles of a fair share of all tiles;
+// cut by the line, most CTAs would have an end of one item and the start of the next,
+// and pay for both.  256 items of 11 tiles: 31 us so, 37 on the line; 128 of 4 to 5:
+// 21 us and 29; 192 of 20, on the line either way, 45 us.
+constexpr int kEachTries = 4;
+
 struct ShareScratch {  // shared memory of find_share
     int64_t tiles[20], items[20];
+    int counts[20][kEachTries];
     Share share;
 };
 
@@ -145,6 +154,54 @@ __device__ __noinline__ Share find_share(const AttnParams &p, int rows, ShareScr
         all_tiles += scratch.tiles[w];
         all_items += scratch.items[w];
     }
+    if (all_items <= gridDim.x) {
+        const int fair = (int)min((all_tiles + gridDim.x - 1) / gridDim.x, (int64_t)1 << 30);
+        int mine[kEachTries] = {}, upto[kEachTries];  // CTAs that this thread's requests take; and all up to it
+        for (int b = b0; b < b1; ++b) {
+            const Request r = load_request(p, b, rows);
+            const int n = (int)request_items(p, r);
+            if (n > 0)
+#pragma unroll
+                for (int j = 0; j < kEachTries; ++j) mine[j] += n * min(1 << 16, (r.nt - 1) / (fair + j) + 1);
+        }
+#pragma unroll
+        for (int j = 0; j < kEachTries; ++j) {
+            upto[j] = mine[j];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto[j], o);
+                if (lane >= o) upto[j] += y;
+            }
+            if (lane == 31) scratch.counts[warp][j] = upto[j];
+        }
+        __syncthreads();
+        for (int j = 0; j < kEachTries; ++j) {
+            int all = 0, before = upto[j] - mine[j];
+            for (int w = 0; w < NT / 32; ++w) {
+                if (w < warp) before += scratch.counts[w][j];
+                all += scratch.counts[w][j];
+            }
+            if (all > (int)gridDim.x) continue;
+            const int cta = blockIdx.x;
+            if (cta >= before && cta < before + mine[j]) {
+                int b = b0, off = cta - before;
+                for (;; ++b) {
+                    const Request r = load_request(p, b, rows);
+                    const int t = (int)request_items(p, r) * ((r.nt - 1) / (fair + j) + 1);
+                    if (off < t) break;
+                    off -= t;
+                }
+                scratch.share.b = b;
+                scratch.share.off = off;
+            }
+            __syncthreads();
+            Share s = scratch.share;
+            s.u = 0;
+            s.end = cta < all;
+            s.each = fair + j;
+            return s;
+        }
+    }
     const int cost = all_tiles >= (int64_t)kTilesEach * gridDim.x ? kItemCost : 0;
     const int64_t total = all_tiles + cost * all_items, sum = tiles + cost * items, before = ti + cost * it - sum;
     const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
@@ -169,6 +226,7 @@ __device__ __noinline__ Share find_share(const AttnParams &p, int rows, ShareScr
     s.end = end;
     s.ctas = ctas;
     s.cost = cost;
+    s.each = 0;
     return s;
 }
 
@@ -186,34 +244,50 @@ struct Part {
 __device__ __noinline__ Part next_part(const AttnParams &p, Share &s, int rows) {
     Part x;
     x.b = -1;
-    int64_t item = 0;
-    for (;;) {
+    if (s.each > 0) {
         if (s.u >= s.end) return x;
+        s.u = s.end;
         x.r = load_request(p, s.b, rows);
-        if (s.off >= request_items(p, x.r) * (x.r.nt + s.cost)) {
-            s.off = 0;  // a share's next request is entered at its first unit
-            ++s.b;
-            continue;
-        }
-        const int units = x.r.nt + s.cost;
-        const int64_t i = quotient(s.off, units);
-        const int at = (int)(s.off - i * units), to = (int)min((int64_t)units, at + s.end - s.u);
-        item = s.u - at;
-        s.u += to - at;
-        s.off += to - at;
-        if (to <= s.cost) continue;  // none of its tiles are here
+        const int k = (x.r.nt - 1) / s.each + 1, i = (int)s.off / k, j = (int)s.off - i * k;
+        const int q = x.r.nt / k, more = x.r.nt - q * k;
         x.b = s.b;
-        x.t0 = max(0, at - s.cost);
-        x.t1 = to - s.cost;
-        x.h = (int)quotient(i, x.r.rt);
-        x.rt = (int)(i - (int64_t)x.h * x.r.rt);
-        break;
-    }
-    x.whole = x.t0 == 0 && x.t1 == x.r.nt;
-    x.c0 = x.c1 = blockIdx.x;
-    if (!x.whole) {
-        x.c0 = cta_of(s.total, item + s.cost, s.ctas);
-        x.c1 = cta_of(s.total, item + s.cost + x.r.nt - 1, s.ctas);
+        x.t0 = j * q + min(j, more);
+        x.t1 = x.t0 + q + (j < more ? 1 : 0);
+        x.h = i / x.r.rt;
+        x.rt = i - x.h * x.r.rt;
+        x.whole = k == 1;
+        x.c0 = blockIdx.x - j;
+        x.c1 = x.c0 + k - 1;
+    } else {
+        int64_t item = 0;
+        for (;;) {
+            if (s.u >= s.end) return x;
+            x.r = load_request(p, s.b, rows);
+            if (s.off >= request_items(p, x.r) * (x.r.nt + s.cost)) {
+                s.off = 0;  // a share's next request is entered at its first unit
+                ++s.b;
+                continue;
+            }
+            const int units = x.r.nt + s.cost;
+            const int64_t i = quotient(s.off, units);
+            const int at = (int)(s.off - i * units), to = (int)min((int64_t)units, at + s.end - s.u);
+            item = s.u - at;
+            s.u += to - at;
+            s.off += to - at;
+            if (to <= s.cost) continue;  // none of its tiles are here
+            x.b = s.b;
+            x.t0 = max(0, at - s.cost);
+            x.t1 = to - s.cost;
+            x.h = (int)quotient(i, x.r.rt);
+            x.rt = (int)(i - (int64_t)x.h * x.r.rt);
+            break;
+        }
+        x.whole = x.t0 == 0 && x.t1 == x.r.nt;
+        x.c0 = x.c1 = blockIdx.x;
+        if (!x.whole) {
+            x.c0 = cta_of(s.total, item + s.cost, s.ctas);
+            x.c1 = cta_of(s.total, item + s.cost + x.r.nt - 1, s.ctas);
+        }
     }
     const int row0 = x.rt * rows;
     x.nrows = min(rows, x.r.n * p.group - row0);

@@ -11,9 +11,14 @@
 // row = t * group + g), and its length is counted in tiles of kTile tokens.  All tiles
 // of all items in order are one line that is cut into equal parts, one for each CTA,
 // so long and short requests together, one long request alone and a full batch all
-// load every SM alike.  A CTA whose part holds an item whole writes its output; an
-// item cut by a boundary leaves (m, l, o) of each part in the workspace, and the part
-// that arrives last (a counter; nobody waits) joins them in CTA order.
+// load every SM alike; where items are few, an item takes whole CTAs instead.  A CTA
+// whose part holds an item whole writes its output; an item cut by a boundary leaves
+// (m, l, o) of each part in the workspace, and the part that arrives last (a counter;
+// nobody waits) joins them in CTA order.
+//
+// Two kernels: bf16 queries with heads of up to 128 columns take the tensor cores; fp32
+// queries, wider heads and a cache that no tensor map can describe take fp32 arithmetic
+// (the verify batch of 64 requests below: 5480 us there, 121 us on the tensor cores).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -74,7 +79,8 @@ __device__ __forceinline__ Request load_request(const AttnParams &p, int b, int 
 
 // Starting and finishing an item costs a CTA about as much as kItemCost tiles, so on the
 // line an item is that much longer, ahead of its tiles -- where there are enough tiles
-// to go round: with fewer than kTilesEach a CTA, spreading the tiles matters more.
+// to go round: with fewer than kTilesEach a CTA, spreading the tiles matters more.  With
+// no such cost the verify batch measured below takes 142 us instead of 121.
 constexpr int kItemCost = 3, kTilesEach = 4;
 __device__ __forceinline__ int64_t request_items(const AttnParams &p, const Request &r) {
     return (int64_t)p.c.num_heads * r.rt;
@@ -472,6 +478,9 @@ __device__ __noinline__ void join_parts(const AttnParams &p, const Part &x) {
 // rows (its key row read 16 codes at a time, the queries broadcast from shared
 // memory), then the warp walks its tokens with the lanes over the head's columns.
 // Every warp keeps its own (m, l, o); they join in shared memory at the part's end.
+// Bound by instructions: two fp32 products of rows x tokens x columns and eight warp
+// reductions a token block.  9 requests of 1 to 5 fp32 queries, 10 heads on 2 of 80
+// columns, 40 to 1500 tokens: 29 us.
 constexpr int kSimtRows = 8, kSimtThreads = 128;
 
 template <typename T, int ND>
@@ -662,23 +671,41 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
 //   O^T [128 >= D, R rows]  = V^T [D, 128] P^T     (V transposed by the operand's layout)
 // so the rows of a tile, few in a verify step, are the products' narrow side and cost
 // what they are, and a thread of the softmax owns one token in S^T and one column of
-// the head in O^T: R values each.
-//  - e4m3 keeps 4 significant bits, so Q and P are each the sum of two e4m3 terms and
-//    every product runs twice.  A row of Q is scaled by a power of two to a largest
-//    magnitude of 128 .. 256: a bf16 entry (8 bits) is then exact in two terms down to
-//    2^-10 of the row's largest, and off by 2^-18 of it at most below.  P needs a
-//    reference near its own size: every tile has its own, its largest score, so that
-//    a tail of small probabilities next to one large one elsewhere keeps its bits.
+// the head in O^T: 16 rows of each.
+//  - e4m3 keeps 4 significant bits, so Q and P are each the sum of two e4m3 terms.  The
+//    terms lie side by side along N, so that a product is one instruction a step of 32
+//    with 2 R columns (32 columns take 55 cycles, 64 take 69, 128 take 97), and their
+//    results are added as they leave tensor memory.  A row of Q is scaled by a power of
+//    two to a largest magnitude of 128 .. 256: a bf16 entry (8 bits) is then exact in two
+//    terms down to 2^-10 of the row's largest, and off by 2^-18 of it at most below.  P
+//    needs a reference near its own size: every tile has its own, its largest score, so
+//    that a tail of small probabilities next to one large one elsewhere keeps its bits.
 //  - The scale of a key's page multiplies the score; the scale of a value's page, over
 //    the tile's largest, multiplies the probability before it is rounded (2^8 at most,
 //    448 is the type's largest), and the tile's largest joins the weight with which
 //    O^T is added to the fp32 sums, 2^(tile reference - running reference).
 //  - The running reference of a row moves only when a tile's is more than 2^64 above
 //    it, so sums are rescaled at a part's first tile and hardly ever after.
-// Roles: warps of 128 threads a group of up to 32 rows for the softmax and the sums,
-// one warp for the copies (page ids and scales are read a batch ahead), one thread for
-// the products.  S^T and O^T are double-buffered: S^T of the next tile is multiplied
-// while the softmax of this one runs, O^T of this one while the sums take the last.
+//  - exp2 is the hardware's approximation, its error far below the rounding of P.
+// Roles: R / 16 groups of 128 threads for the softmax and the sums, one warp that issues the products, one or two that copy.  The first copying warp also
+// finds the CTA's parts and tells them kParts ahead.  S^T and O^T are double-buffered:
+// S^T of the next tile is multiplied while the softmax of this one runs, O^T of this
+// one while the sums take the last.
+//
+// What bounds it: the chain of one tile through its softmax warps, from tensor memory
+// through maxima, exponentials and two roundings to P and back, about 3000 cycles, of
+// which two (two CTAs) are under way on an SM; the issue slots are half full, the
+// tensor cores at an eighth, DRAM at two thirds.  R = 16 and 32 have two CTAs an SM
+// (with one, the first two batches below take 152 and 106 us instead of 121 and 90),
+// R = 64 has the shared memory and registers for one.  R is the smallest that holds a
+// request's rows: 38 requests of 8192 tokens and 8 key heads of 128 take, with 8 rows,
+// 103 us in R = 16, 107 in 32 and 153 in 64; with 32 rows 116 us in 32 and 167 in 64; with
+// 64 rows 194 us in either.  The bytes alone take 94 us.
+// Measured (time of a launch, codes read): 64 requests, 8 queries, 32 query and 8 key
+// heads of 128, 500 to 8000 tokens, pages of 64: 121 us, 4.6 TB/s.  Two requests of
+// 120000 and 131071 tokens, one query, 64 query heads: 90 us, 5.7 TB/s.  256 requests of
+// 1 to 8 queries, 4 key heads of 64, 60 to 3000 tokens, pages of 16: 108 us, 1.9 TB/s.
+// One request of one query over 1004 tokens: 12 to 14 us.
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kSlotBytes = kTile * 128;  // a tile of keys or values
 constexpr int kInfo = 8;                 // tiles whose scales are held at a time
@@ -747,23 +774,26 @@ __device__ __noinline__ bool poll_barrier(uint32_t bar, uint32_t parity) {
     }
 }
 
-template <int R, int W>  // rows of a tile, warps that copy
+template <int R>
 struct TcShape {
     static constexpr int kRowsG = 16;                     // rows of a softmax group
     static constexpr int kGroups = R / kRowsG;            // groups of 128 threads
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
-    static constexpr int kThreads = kSoft + 32 * (1 + W);
     static constexpr int kPerSM = R < 64 ? 2 : 1;         // CTAs an SM
     static constexpr int kSlots = R < 64 ? 5 : 10;
     static constexpr uint32_t kCols = 8 * R;              // S^T and O^T, two terms and two buffers each
 };
+
+// Softmax threads, the issuer of the products, W warps that copy.
+template <int R, int W>
+constexpr int kTcThreads = TcShape<R>::kSoft + 32 * (1 + W);
 
 constexpr int kParts = 4;  // parts known ahead
 constexpr int kAllBar = 8, kLookBar = 9;  // named barriers of all softmax threads; group g's is 1 + g
 
 template <int R>
 struct TcShared {
-    using C = TcShape<R, 1>;
+    using C = TcShape<R>;
     uint8_t ring[C::kSlots][kSlotBytes];
     uint8_t q[2][R * 128];             // two terms, rows of 128 bytes, swizzled
     uint16_t q_raw[R][128];            // the next part's, as they are stored
@@ -821,7 +851,7 @@ __device__ __forceinline__ float warp_sum_scatter(float (&v)[N], int lane) {
 // store_queries makes two e4m3 terms of each entry for the products.
 template <int R>
 struct QueryShape {
-    static constexpr int kCols = R * 128 / TcShape<R, 1>::kSoft, kPerRow = 128 / kCols;
+    static constexpr int kCols = R * 128 / TcShape<R>::kSoft, kPerRow = 128 / kCols;
 };
 
 template <int R>
@@ -891,9 +921,9 @@ __device__ __noinline__ void store_queries(float scale_log2, int nrows, int D, T
 }
 
 template <int R, int W>
-__global__ void __launch_bounds__(TcShape<R, W>::kThreads, TcShape<R, W>::kPerSM)
+__global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
     attention_tc_kernel(AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using C = TcShape<R, W>;
+    using C = TcShape<R>;
     constexpr int NR = C::kRowsG, NS = C::kSlots;
     extern __shared__ __align__(1024) uint8_t raw[];
     TcShared<R> &sm = *reinterpret_cast<TcShared<R> *>(raw);
@@ -917,7 +947,7 @@ __global__ void __launch_bounds__(TcShape<R, W>::kThreads, TcShape<R, W>::kPerSM
     }
     if (warp == C::kSoft / 32 + 1) tmem_alloc(&sm.tmem, C::kCols);
     tc_fence_before();
-    Share share = find_share<C::kThreads>(p, R, sm.scratch);  // it synchronises the CTA
+    Share share = find_share<kTcThreads<R, W>>(p, R, sm.scratch);  // it synchronises the CTA
     tc_fence_after();
     const uint32_t tm = sm.tmem, tS = tm, tO = tm + 4 * R;  // a buffer: R columns of each term
     bool dead = false;  // a wait ran out: wait no more, finish, report
@@ -1390,7 +1420,7 @@ bool codes_map(const spec_kv_cache &c, const void *codes, CUtensorMap *map) {
 
 template <int R, int W>
 int launch_tc(const AttnParams &p, int dev, int sms, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
-    using C = TcShape<R, W>;
+    using C = TcShape<R>;
     constexpr int bytes = (int)sizeof(TcShared<R>);
     static_assert(C::kPerSM * (bytes + 1024) <= 228 * 1024, "shared memory of an SM");
     static std::atomic<bool> set[64];
@@ -1403,7 +1433,7 @@ int launch_tc(const AttnParams &p, int dev, int sms, const CUtensorMap &kmap, co
         set[dev].store(true);
     }
     const int ctas = C::kPerSM * sms < kMaxCtas ? C::kPerSM * sms : kMaxCtas;
-    attention_tc_kernel<R, W><<<ctas, C::kThreads, bytes, st>>>(p, kmap, vmap);
+    attention_tc_kernel<R, W><<<ctas, kTcThreads<R, W>, bytes, st>>>(p, kmap, vmap);
     return launch_status();
 }
 

@@ -315,3 +315,23 @@ def test_more_requests_than_threads():
     out = _run(x)
     assert (out["status"] == 0).all()
     _check(x, out)
+
+
+@pytest.mark.parametrize("group,page", [(1, 16), (1, 64), (4, 32), (8, 16)])  # 6, 6, 24 and 48 rows
+@pytest.mark.parametrize("batch", [30, 75, 151, 153])  # 60 to 306 items of 2 heads, on 304 CTAs of 152 SMs
+def test_few_items_and_some_more(batch, group, page):
+    """Items as many as the CTAs, somewhat fewer and more: whole CTAs an item, or the line."""
+    g = np.random.default_rng(31 + batch)
+    new = g.integers(0, 7, batch)
+    lens = new + np.where(g.random(batch) < 0.2, g.integers(0, 3000, batch), g.integers(300, 900, batch))
+    lens[:2] = new[:2]
+    x = U.Inputs(32, lens, new, 2 * group, 2, 32, page, BF16)
+    _check(x, _run(x))
+    _check(x, _run(x, window=260, sinks=5), window=260, sinks=5)
+
+
+@pytest.mark.parametrize("long", [3000, 20000])
+def test_one_long_item_among_short_ones(long):
+    """A fair share of the tiles that one item passes by far, the others by far below it."""
+    x = U.Inputs(33, [long] + [40] * 60 + [long // 2], [3] * 62, 8, 4, 64, 16, BF16)
+    _check(x, _run(x))

@@ -810,7 +810,11 @@ struct TcShared {
     float red[2][4][R];
     float c[R];        // score factor of a row: scale * log2(e) / its power of two
     float m[R], l[R];  // at a part's end
-    int64_t out_at[2][R];  // a row's first output element, by the part's parity
+    // A row's first output element, by the part's number mod 3: written while the part
+    // before runs, read as the part ends, by each warp in its own time.  Every warp passes
+    // a barrier in the next part, so by the part after that, which may use the same place,
+    // all have read.  (By the next part alone, one of a single tile, they may not have.)
+    int64_t out_at[3][R];
     ShareScratch scratch;
     uint32_t tmem;
     int flag;
@@ -855,12 +859,12 @@ struct QueryShape {
 };
 
 template <int R>
-__device__ __noinline__ void start_queries(const AttnParams &p, const Part &x, TcShared<R> &sm, int tid, int parity) {
+__device__ __noinline__ void start_queries(const AttnParams &p, const Part &x, TcShared<R> &sm, int tid, int at) {
     constexpr int kCols = QueryShape<R>::kCols;
     const int row = tid / QueryShape<R>::kPerRow, c0 = (tid % QueryShape<R>::kPerRow) * kCols, D = p.c.head_dim;
     if (row >= x.nrows) return;
     const uint32_t grow = x.rt * R + row, t = grow / (uint32_t)p.group, head = x.h * p.group + (grow - t * p.group);
-    if (c0 == 0) sm.out_at[parity][row] = ((int64_t)(x.r.row0 + (int)t) * p.Hq + head) * D;
+    if (c0 == 0) sm.out_at[at][row] = ((int64_t)(x.r.row0 + (int)t) * p.Hq + head) * D;
     const char *src = (const char *)p.q + ((int64_t)(x.r.row0 + (int)t) * p.ld_q + (int64_t)head * D + c0) * 2;
 #pragma unroll
     for (int c = 0; c < kCols; c += 8) {
@@ -1169,7 +1173,8 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
             store_queries<R>(p.scale_log2, sm.part[0].nrows, D, sm, tid);
             named_sync<C::kSoft>(kAllBar);
         }
-        for (int n = 0; more; ++n) {
+        int n3 = 0;  // n mod 3
+        for (int n = 0; more; ++n, n3 = n3 == 2 ? 0 : n3 + 1) {
             const Part &x = sm.part[n % kParts], &next = sm.part[(n + 1) % kParts];
             const int t0 = x.t0, t1 = x.t1;
             // tiles within [clear_lo, clear_hi] hide no token from any row
@@ -1209,7 +1214,7 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
                 const bool masked = j0 + kTile - 1 > clear_hi || (j0 < clear_lo && j0 + kTile > p.sinks);
                 if (i + 1 == t1) {
                     wait(&sm.part_full[(n + 1) % kParts], ((n + 1) / kParts) & 1);
-                    if (!dead && next.b >= 0) start_queries<R>(p, next, sm, tid, (n + 1) & 1);
+                    if (!dead && next.b >= 0) start_queries<R>(p, next, sm, tid, n3 == 2 ? 0 : n3 + 1);
                 }
                 wait(&sm.s_full[buf], (g >> 1) & 1);
                 if (idle) {
@@ -1366,7 +1371,7 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
                     if (r0 + r < x.nrows && t128 < D)
-                        ((uint16_t *)p.out)[sm.out_at[n & 1][r0 + r] + t128] =
+                        ((uint16_t *)p.out)[sm.out_at[n3][r0 + r] + t128] =
                             (uint16_t)pack_bf16x2(acc[r] * sm.l[r0 + r], 0.f);
             } else {
                 float *slot = slot_of(p, blockIdx.x, x.t0 == 0, R);

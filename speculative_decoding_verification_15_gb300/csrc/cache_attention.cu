@@ -47,7 +47,7 @@ struct AttnParams {
     float scale_log2;  // scale * log2(e)
     bool q_vec;        // rows of q are 16-byte aligned
     int *tickets;      // [kMaxCtas], zero between calls
-    float *partial;    // [2 * kMaxCtas][rows * (D + 2)]
+    float *partial;    // [2 * kMaxCtas][rows * (D + 3)]
 };
 
 // What a request asks for, with its positions and its tiles.
@@ -343,9 +343,10 @@ __device__ __forceinline__ bool named_any(int bar, bool x) {
 }
 
 // A part's slot: the first part of an item is its CTA's last part, every other part
-// its CTA's first, so two slots a CTA are enough.
+// its CTA's first, so two slots a CTA are enough.  It holds the R rows' sums o [R][D],
+// the references m of their weights' sums, those sums l, and the references of o.
 __device__ __forceinline__ float *slot_of(const AttnParams &p, int cta, bool first, int rows) {
-    return p.partial + (int64_t)(2 * cta + (first ? 1 : 0)) * rows * (p.c.head_dim + 2);
+    return p.partial + (int64_t)(2 * cta + (first ? 1 : 0)) * rows * (p.c.head_dim + 3);
 }
 
 // Output element (row r of the part's row tile, column d).
@@ -361,6 +362,10 @@ __device__ __forceinline__ void store_lse(const AttnParams &p, const Part &x, in
     p.lse[(int64_t)(x.r.row0 + t) * p.Hq + x.h * p.group + g] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
 }
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+// What o, with reference mo, is multiplied by to be divided by l with reference m.
+__device__ __forceinline__ float output_factor(float mo, float m, float l) {
+    return l == 0.f ? 0.f : exp2f(mo - m) / l;
+}
 
 // 2^(a - m), 0 where the part a comes from saw nothing (a = -inf, whatever m is).
 __device__ __forceinline__ float weight_of(float a, float m) { return a == kNegInf ? 0.f : exp2f(a - m); }
@@ -393,17 +398,17 @@ __device__ __noinline__ void join_parts(const AttnParams &p, const Part &x) {
     constexpr int kWarps = NT / 32, P = 4;
     const int D = p.c.head_dim, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nrows = x.nrows, parts = x.c1 - x.c0 + 1;
-    const int64_t stride = 2 * (int64_t)R * (D + 2);  // from a CTA's slot to the next one's
+    const int64_t stride = 2 * (int64_t)R * (D + 3);  // from a CTA's slot to the next one's
     const float *slot0 = slot_of(p, x.c0, true, R), *slots = slot_of(p, x.c0, false, R);  // part 0; part c at c * stride
     for (int r0 = warp; r0 < nrows; r0 += 2 * kWarps) {
-        float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+        float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f}, mo[2] = {kNegInf, kNegInf};
         float4 o[2][ND];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int n = 0; n < ND; ++n) o[k][n] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c0 = 0; c0 < parts; c0 += P) {
-            float mc[2][P], lc[2][P];
+            float mc[2][P], lc[2][P], moc[2][P];
             float4 v[2][P][ND];
 #pragma unroll
             for (int c = 0; c < P; ++c) {
@@ -414,6 +419,7 @@ __device__ __noinline__ void join_parts(const AttnParams &p, const Part &x) {
                     const bool on = c0 + c < parts && r < nrows;
                     mc[k][c] = on ? __ldcg(s + R * D + r) : kNegInf;
                     lc[k][c] = on ? __ldcg(s + R * D + R + r) : 0.f;
+                    moc[k][c] = on ? __ldcg(s + R * D + 2 * R + r) : kNegInf;
 #pragma unroll
                     for (int n = 0; n < ND; ++n) {
                         const int d = 128 * n + 4 * lane;
@@ -423,12 +429,16 @@ __device__ __noinline__ void join_parts(const AttnParams &p, const Part &x) {
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                float top = m[k];
+                float top = m[k], top_o = mo[k];
 #pragma unroll
-                for (int c = 0; c < P; ++c) top = fmaxf(top, mc[k][c]);
-                const float keep = weight_of(m[k], top);
+                for (int c = 0; c < P; ++c) {
+                    top = fmaxf(top, mc[k][c]);
+                    top_o = fmaxf(top_o, moc[k][c]);
+                }
+                l[k] *= weight_of(m[k], top);
                 m[k] = top;
-                l[k] *= keep;
+                const float keep = weight_of(mo[k], top_o);
+                mo[k] = top_o;
 #pragma unroll
                 for (int n = 0; n < ND; ++n) {
                     o[k][n].x *= keep;
@@ -438,8 +448,8 @@ __device__ __noinline__ void join_parts(const AttnParams &p, const Part &x) {
                 }
 #pragma unroll
                 for (int c = 0; c < P; ++c) {
-                    const float w = weight_of(mc[k][c], top);
-                    l[k] = fmaf(lc[k][c], w, l[k]);
+                    l[k] = fmaf(lc[k][c], weight_of(mc[k][c], top), l[k]);
+                    const float w = weight_of(moc[k][c], top_o);
 #pragma unroll
                     for (int n = 0; n < ND; ++n) {
                         o[k][n].x = fmaf(v[k][c][n].x, w, o[k][n].x);
@@ -454,7 +464,7 @@ __device__ __noinline__ void join_parts(const AttnParams &p, const Part &x) {
         for (int k = 0; k < 2; ++k) {
             const int r = r0 + k * kWarps;
             if (r >= nrows) break;
-            const float inv = inverse_sum(l[k]);
+            const float inv = output_factor(mo[k], m[k], l[k]);
             const int row = x.rt * R + r, t = row / p.group, g = row - t * p.group;
             const int64_t at = ((int64_t)(x.r.row0 + t) * p.Hq + x.h * p.group + g) * D;
             if (p.lse && lane == 0) store_lse(p, x, row, m[k], l[k]);
@@ -656,6 +666,7 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
             if (tid < nrows) {
                 slot[R * D + tid] = s_w[tid];
                 slot[R * D + R + tid] = s_w[R + tid];
+                slot[R * D + 2 * R + tid] = s_w[tid];
             }
             if (arrive_last<kSimtThreads>(p, x.c0, x.c1 - x.c0 + 1, &s_flag, 1))
                 join_parts<T, kSimtThreads, R, ND>(p, x);
@@ -677,15 +688,23 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
 //    with 2 R columns (32 columns take 55 cycles, 64 take 69, 128 take 97), and their
 //    results are added as they leave tensor memory.  A row of Q is scaled by a power of
 //    two to a largest magnitude of 128 .. 256: a bf16 entry (8 bits) is then exact in two
-//    terms down to 2^-10 of the row's largest, and off by 2^-18 of it at most below.  P
-//    needs a reference near its own size: every tile has its own, its largest score, so
-//    that a tail of small probabilities next to one large one elsewhere keeps its bits.
-//  - The scale of a key's page multiplies the score; the scale of a value's page, over
-//    the tile's largest, multiplies the probability before it is rounded (2^8 at most,
-//    448 is the type's largest), and the tile's largest joins the weight with which
-//    O^T is added to the fp32 sums, 2^(tile reference - running reference).
-//  - The running reference of a row moves only when a tile's is more than 2^64 above
-//    it, so sums are rescaled at a part's first tile and hardly ever after.
+//    terms down to 2^-9 of the row's largest, and off by 2^-17 of it at most below.
+//  - What P V^T adds for token j is 2^x_j vs_j times its codes, vs_j the scale of its
+//    value's page.  Two e4m3 terms of a number z of 0 .. 256 are off by 2^-8 of it, or by
+//    2^-10 where that is more, so z has to be near 256 where it matters: z_j =
+//    2^(8 + y_j - r) with y_j = x_j + log2(vs_j), r the largest y_j of the tokens of the
+//    tile that the row sees.  Neither pages that a row does not see nor improbable ones
+//    with large values then cost the others their bits, and a tail of small
+//    probabilities next to one large one in another tile keeps its own.
+//  - The weights' sum l needs 2^x_j = z_j 2^(r - 8) / vs_j.  That is one exponential for
+//    both, while the tile's value scales lie within 2^kNearLog2 of each other; where they
+//    do not, z_j may vanish while its weight does not, and l gets its own reference, the
+//    tile's largest x_j, and its own exponentials.  (log2(vs_j) is counted from the
+//    tile's largest, lt, so that it is 0 where all are equal.)
+//  - So a row has two running references, m for l and mo for O, both in fp32; the
+//    output is O 2^(mo - m) / l.
+//  - A running reference moves only when a tile's is more than 2^64 above it, so sums
+//    are rescaled at a part's first tile and hardly ever after.
 //  - exp2 is the hardware's approximation, its error far below the rounding of P.
 // Roles: R / 16 groups of 128 threads for the softmax and the sums, one warp that issues the products, one or two that copy.  The first copying warp also
 // finds the CTA's parts and tells them kParts ahead.  S^T and O^T are double-buffered:
@@ -710,6 +729,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kSlotBytes = kTile * 128;  // a tile of keys or values
 constexpr int kInfo = 8;                 // tiles whose scales are held at a time
 constexpr float kRefStep = 64.f;         // how far (log2) a tile may pass the running reference
+constexpr float kNearLog2 = 16.f;        // spread of a tile's value scales that one exponential serves
 
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
     unsigned long long d;
@@ -801,15 +821,18 @@ struct TcShared {
     uint64_t full[C::kSlots], empty[C::kSlots], s_full[2], p_full, o_full, q_full;
     uint64_t part_full[kParts], part_empty[kParts];
     Part part[kParts];                      // b < 0: no more
-    float ks[kInfo][8], gv[kInfo][8], wv[kInfo];  // a tile's scales
+    // a tile's pages: the key's scale, log2 of the value's over the tile's largest and the
+    // inverse of that (0 if the tile is far), whether it is far (1 or 0); log2 of the largest
+    float4 page_info[kInfo][8];
+    float lt[kInfo];
     int pages[2][8];                              // and its pages, for the copies of keys and of values
-    // every softmax warp's own copy, by the tile's parity: row pairs' score factors and
-    // minus references, weights of the row sums and of O^T
-    float4 cm[4 * C::kGroups][2][C::kRowsG / 2];
+    // every softmax warp's own copy, by the tile's parity: 8 less the rows' references,
+    // weights of the row sums and of O^T
+    alignas(16) float nref[4 * C::kGroups][2][C::kRowsG];
     float beta[4 * C::kGroups][2][C::kRowsG], w[4 * C::kGroups][2][C::kRowsG];
-    float red[2][4][R];
-    float c[R];        // score factor of a row: scale * log2(e) / its power of two
-    float m[R], l[R];  // at a part's end
+    float red[2][4][R], red_far[4][R];
+    float c[R];               // score factor of a row: scale * log2(e) / its power of two
+    float m[R], l[R], mo[R];  // at a part's end
     // A row's first output element, by the part's number mod 3: written while the part
     // before runs, read as the part ends, by each warp in its own time.  Every warp passes
     // a barrier in the next part, so by the part after that, which may use the same place,
@@ -848,6 +871,26 @@ __device__ __forceinline__ float warp_sum_scatter(float (&v)[N], int lane) {
 #pragma unroll
     for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
     return x;
+}
+
+// A far tile's own work, out of the way of the others' registers: the warp's largest x
+// = y - log2(value's scale) of each row, and each row's weight of this lane's token.
+template <int NR>
+__device__ __noinline__ void far_maxima(const float (&y)[NR], float lv, float *red, int lane) {
+#pragma unroll 1
+    for (int r = 0; r < NR; ++r) {
+        const float f = redux_max(y[r] == kNegInf ? kNegInf : y[r] - lv);
+        if (lane == 0) red[r] = f;
+    }
+    __syncwarp();
+}
+template <int NR>
+__device__ __noinline__ void far_weights(float (&y)[NR], float lv, float x_ref, float x_beta) {
+#pragma unroll 1
+    for (int r = 0; r < NR; ++r) {
+        const float x = y[r] == kNegInf ? kNegInf : y[r] - lv;
+        y[r] = ex2_approx(x - __shfl_sync(0xffffffffu, x_ref, r)) * __shfl_sync(0xffffffffu, x_beta, r);
+    }
 }
 
 // A part's queries: a thread takes kCols columns of one row.  start_queries, a tile
@@ -1024,6 +1067,8 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
         tell_part(xn);
         int i0 = 0, in = xn.t0, page = -1, page_n = -1;
         float ks = 0.f, vs = 0.f, ks_n = 0.f, vs_n = 0.f;
+        float lv = 0.f, iv = 0.f, top = 0.f;
+        bool far = false;
         if (xn.b >= 0) {
             page_n = fetch_page(xn, in);
             ks_n = fetch_scale(p.c.k_scale, xn, page_n);
@@ -1039,16 +1084,26 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
                 const int from = (k << shift) + (lane & (ppt - 1)), seq = 2 * g, slot = seq % NS;
                 copy_tile(kmap, seq, __shfl_sync(0xffffffffu, page, from), x.h, sm.pages[0]);
                 if (dead) break;
-                // the scales may still be on their way here
-                const float tks = __shfl_sync(0xffffffffu, ks, from), tvs = __shfl_sync(0xffffffffu, vs, from);
-                float top = tvs;
-                for (int s = 1; s < ppt; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-                const int at = g % kInfo;
-                if (lane < ppt) {
-                    sm.ks[at][lane] = tks;
-                    sm.gv[at][lane] = top > 0.f ? tvs / top * 256.f : 0.f;
+                if (k == 0) {  // the scales may still be on their way here
+                    // Of this lane's page; those below the smallest normal number count as
+                    // that, and a page that is not there has no weight.
+                    const float lvs = page >= 0 ? log2f(fmaxf(vs, 1.1754944e-38f)) : -1e30f;
+                    float low = page >= 0 ? lvs : 1e30f;
+                    top = lvs;
+                    for (int s = 1; s < ppt; s <<= 1) {  // over the pages of a tile
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, s));
+                    }
+                    far = top - low > kNearLog2;
+                    lv = page >= 0 ? lvs - top : -1e30f;
+                    iv = page >= 0 && !far ? exp2f(-lv) : 0.f;
                 }
-                if (lane == 0) sm.wv[at] = top * (1.f / 256.f);
+                const int at = g % kInfo;
+                const float tks = __shfl_sync(0xffffffffu, ks, from), tlv = __shfl_sync(0xffffffffu, lv, from);
+                const float tiv = __shfl_sync(0xffffffffu, iv, from), tlt = __shfl_sync(0xffffffffu, top, from);
+                const float tfar = __shfl_sync(0xffffffffu, far ? 1.f : 0.f, from);
+                if (lane < ppt) sm.page_info[at][lane] = make_float4(tks, tlv, tiv, tfar);
+                if (lane == 0) sm.lt[at] = tlt;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.full[slot]);
                 if constexpr (W == 1) {
@@ -1180,8 +1235,8 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
             // tiles within [clear_lo, clear_hi] hide no token from any row
             const int clear_hi = x.pos0, clear_lo = p.window > 0 ? max(0, x.pos1 - p.window + 1) : 0;
             float acc[NR], l[NR];
-            float m_run = kNegInf;  // lane r: row r's running reference
-            float alpha = 1.f, alpha_last = 1.f;  // lane r: what row r's sums so far are multiplied by
+            float m_run = kNegInf, mo_run = kNegInf;  // lane r: row r's running references
+            float alpha = 1.f, alpha_last = 1.f;      // lane r: what row r's O so far is multiplied by
             bool moved = false, moved_last = false;
 #pragma unroll
             for (int r = 0; r < NR; ++r) acc[r] = l[r] = 0.f;
@@ -1223,19 +1278,26 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
                     if (lane == 0) mbar_arrive(&sm.p_full);
                     continue;
                 }
-                const float ks = sm.ks[inf][t128 >> bs_shift], gv = sm.gv[inf][t128 >> bs_shift], wv = sm.wv[inf];
+                const float4 info = sm.page_info[inf][t128 >> bs_shift];
+                const bool far = info.w != 0.f;  // the same in every thread
                 tc_fence_after();
                 uint32_t s[NR], s1[NR];
                 tmem_ld<NR>(tS + buf * 2 * R + r0 + lanes, s);
                 tmem_ld<NR>(tS + buf * 2 * R + R + r0 + lanes, s1);
                 tmem_wait_ld();
                 add_terms<NR>(s, s1);
-                float v[NR];
+                float v[NR];  // y: log2 scores with the value's scale
+                const float2 ks2 = make_float2(info.x, info.x), lv2 = make_float2(info.y, info.y);
 #pragma unroll
-                for (int r = 0; r < NR; r += 2) {
-                    const float2 f = fmul2(make_float2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), make_float2(ks, ks));
-                    v[r] = f.x;
-                    v[r + 1] = f.y;
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 c = *(const float4 *)&sm.c[r0 + r];
+                    const float2 f0 = fmul2(make_float2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), ks2);
+                    const float2 f1 = fmul2(make_float2(__uint_as_float(s[r + 2]), __uint_as_float(s[r + 3])), ks2);
+                    const float2 y0 = ffma2(f0, make_float2(c.x, c.y), lv2), y1 = ffma2(f1, make_float2(c.z, c.w), lv2);
+                    v[r] = y0.x;
+                    v[r + 1] = y0.y;
+                    v[r + 2] = y1.x;
+                    v[r + 3] = y1.y;
                 }
                 if (masked) {
                     // Some row does not see some token of the tile.  Rows are token-major,
@@ -1279,56 +1341,76 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
 #pragma unroll
                     for (int r = 0; r < NR; ++r) v[r] = (sees >> r) & 1 ? v[r] + put : kNegInf;
                 }
-                // the tile's largest score of every row: over the warp, then over the four
+                // the tile's largest y of every row: over the warp, then over the four
                 // warps, which each keep the rows' references for themselves (lane = row)
 #pragma unroll
                 for (int r = 0; r < NR; r += 4) {
                     const float4 f = make_float4(redux_max(v[r]), redux_max(v[r + 1]), redux_max(v[r + 2]), redux_max(v[r + 3]));
                     *(float4 *)&sm.red[buf][w4][r0 + r] = f;  // every lane the same: no branch
                 }
+                if (far) {  // and the largest x
+                    float y[NR];
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) y[r] = v[r];
+                    far_maxima<NR>(y, sm.page_info[inf][t128 >> bs_shift].y, &sm.red_far[w4][r0], lane);
+                }
                 named_sync<128>(bar);
+                float x_ref = 0.f, x_beta = 0.f;  // lane r, far: row r's largest x, its weight in l
                 {
                     const int k = lane & (NR - 1), r = r0 + k;
                     const float mt = fmaxf(fmaxf(sm.red[buf][0][r], sm.red[buf][1][r]), fmaxf(sm.red[buf][2][r], sm.red[buf][3][r]));
-                    const float c = sm.c[r];
                     const bool some = mt > kNegInf;
-                    const float ref = some ? mt * c : 0.f, mm = some ? ref : kNegInf;
-                    const bool moves = mm > m_run + kRefStep;  // also from -inf
+                    const float ref = some ? mt : 0.f, mo = some ? ref + sm.lt[inf] : kNegInf;
+                    float mm = some ? ref : kNegInf;  // at most the tile's largest x
+                    if (far && some)
+                        mm = fmaxf(fmaxf(sm.red_far[0][r], sm.red_far[1][r]), fmaxf(sm.red_far[2][r], sm.red_far[3][r]));
+                    const bool moves = mm > m_run + kRefStep, moves_o = mo > mo_run + kRefStep;  // also from -inf
                     moved_last = moved;
                     alpha_last = alpha;
-                    moved = __any_sync(0xffffffffu, moves);
-                    alpha = moves ? ex2_approx(m_run - mm) : 1.f;  // 0 from -inf
-                    m_run = moves ? mm : m_run;
-                    const float beta = some ? ex2_approx(mm - m_run) : 1.f;
+                    moved = __any_sync(0xffffffffu, moves || moves_o);
+                    if (moved) {
+                        alpha = moves_o ? ex2_approx(mo_run - mo) : 1.f;  // 0 from -inf
+                        mo_run = moves_o ? mo : mo_run;
+                        const float alpha_l = moves ? ex2_approx(m_run - mm) : 1.f;
+                        m_run = moves ? mm : m_run;
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha_l, r);
+                    }
                     // with 16 rows, lanes 16 .. 31 write what lanes 0 .. 15 do
-                    float *cm = (float *)&sm.cm[warp][buf][k >> 1];
-                    cm[k & 1] = c;
-                    cm[2 + (k & 1)] = -ref;
-                    sm.beta[warp][buf][k] = beta;
-                    sm.w[warp][buf][k] = beta * wv;
+                    sm.nref[warp][buf][k] = 8.f - ref;
+                    sm.beta[warp][buf][k] = some ? ex2_approx(ref - m_run - 8.f) : 1.f;
+                    sm.w[warp][buf][k] = some ? ex2_approx(mo - mo_run - 8.f) : 1.f;
+                    if (far) {
+                        x_ref = some ? mm : 0.f;
+                        x_beta = some ? ex2_approx(mm - m_run) : 1.f;
+                    }
                     __syncwarp();
                 }
-                if (moved) {
+                if (far) {
+                    float y[NR];
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
+                    for (int r = 0; r < NR; ++r) y[r] = v[r];
+                    far_weights<NR>(y, sm.page_info[inf][t128 >> bs_shift].y, x_ref, x_beta);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) l[r] += y[r];
+                    named_sync<128>(bar);  // every warp has read red_far
                 }
                 uint32_t first[NR / 4], rest[NR / 4];
-                const float2 gv2 = make_float2(gv, gv);
+                const float iv = sm.page_info[inf][t128 >> bs_shift].z;
+                const float2 iv2 = make_float2(iv, iv);
 #pragma unroll
                 for (int r = 0; r < NR; r += 4) {
-                    const float4 b = *(const float4 *)&sm.beta[warp][buf][r];
+                    const float4 b = *(const float4 *)&sm.beta[warp][buf][r], f = *(const float4 *)&sm.nref[warp][buf][r];
                     float2 z[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int k = r + 2 * e;
-                        const float4 f = sm.cm[warp][buf][k >> 1];
-                        z[e] = ffma2(make_float2(v[k], v[k + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
+                        z[e] = fadd2(make_float2(v[k], v[k + 1]), e ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
                         z[e].x = ex2_approx(z[e].x);
                         z[e].y = ex2_approx(z[e].y);
-                        const float2 ll = ffma2(z[e], e ? make_float2(b.z, b.w) : make_float2(b.x, b.y), make_float2(l[k], l[k + 1]));
+                        const float2 ll = ffma2(fmul2(z[e], iv2), e ? make_float2(b.z, b.w) : make_float2(b.x, b.y), make_float2(l[k], l[k + 1]));
                         l[k] = ll.x;
                         l[k + 1] = ll.y;
-                        z[e] = fmul2(z[e], gv2);
                     }
                     split_e4m3x4(z[0], z[1], first[r / 4], rest[r / 4]);
                 }
@@ -1361,7 +1443,8 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
                 const int r = r0 + lane;
                 const float sum = sm.red[0][0][r] + sm.red[0][1][r] + sm.red[0][2][r] + sm.red[0][3][r];
                 sm.m[r] = m_run;
-                sm.l[r] = x.whole ? inverse_sum(sum) : sum;
+                sm.mo[r] = mo_run;
+                sm.l[r] = x.whole ? output_factor(mo_run, m_run, sum) : sum;
                 if (p.lse && x.whole && r < x.nrows) store_lse(p, x, x.rt * R + r, m_run, sum);
             }
             named_sync<128>(bar);
@@ -1381,6 +1464,7 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
                 if (t128 < NR && r0 + t128 < x.nrows) {
                     slot[R * D + r0 + t128] = sm.m[r0 + t128];
                     slot[R * D + R + r0 + t128] = sm.l[r0 + t128];
+                    slot[R * D + 2 * R + r0 + t128] = sm.mo[r0 + t128];
                 }
                 if (arrive_last<C::kSoft>(p, x.c0, x.c1 - x.c0 + 1, &sm.flag, kAllBar))
                     join_parts<uint16_t, C::kSoft, R, 1>(p, x);
@@ -1451,7 +1535,7 @@ extern "C" size_t spec_cache_attention_workspace_size(int num_query_heads, int n
     if (num_query_heads <= 0 || num_heads <= 0 || num_query_heads % num_heads || head_dim <= 0 || (head_dim & 15) ||
         head_dim > SPEC_KV_MAX_HEAD_DIM || (dtype != SPEC_BF16 && dtype != SPEC_F32))
         return 0;
-    const size_t slot = sizeof(float) * kMaxRows * ((size_t)head_dim + 2);
+    const size_t slot = sizeof(float) * kMaxRows * ((size_t)head_dim + 3);
     return sizeof(int) * kMaxCtas + 2 * kMaxCtas * slot;
 }
 

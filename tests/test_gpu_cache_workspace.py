@@ -1,0 +1,98 @@
+"""GPU tests of the workspaces of the attention over the 8-bit cache: graphs, streams."""
+import numpy as np
+import pytest
+import torch
+
+import kv_util as U
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def _args(x):
+    return x.q, x.cache(), x.i32(x.table), x.i32(x.lens), x.i32(x.cu), int(x.new.max())
+
+
+def _cut(seed, D, B=40):
+    """Requests whose items are cut between CTAs, so that counters and slots are used."""
+    return U.Inputs(seed, 900 + (np.arange(B) * 131) % 700, np.full(B, 4), 8, 2, D, 64, BF16)
+
+
+def _capture(args, stream, calls=1):
+    import speculative_decoding_verification_15_gb300 as pkg
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = [pkg.cache_attention(*args, want_lse=True) for _ in range(calls)]
+    return graph, out
+
+
+def test_graph_outlives_its_streams_workspace():
+    """Warm up and capture heads of 64, call heads of 128 on the same stream (a larger
+    workspace), take the freed memory, replay: the graph's results are right and nobody
+    else's memory has changed."""
+    import speculative_decoding_verification_15_gb300 as pkg
+
+    small, large = _args(_cut(60, 64)), _args(_cut(61, 128))
+    want = pkg.cache_attention(*small, want_lse=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        pkg.cache_attention(*small)
+        s.synchronize()
+        graph, (out,) = _capture(small, s)
+        pkg.cache_attention(*large)
+        s.synchronize()
+        taken = [torch.full((4 << 20,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(16)]
+        for _ in range(3):
+            out["out"].fill_(float("nan"))
+            graph.replay()
+            s.synchronize()
+            assert (out["status"] == 0).all()
+            assert torch.equal(out["out"], want["out"]) and torch.equal(out["lse"], want["lse"])
+        assert all((t == 0x55).all() for t in taken)
+
+
+def test_replays_next_to_calls_on_the_capture_stream():
+    """A graph replayed on another stream while its capture stream makes calls of its own,
+    and a second graph captured there: every result is that of a call alone."""
+    import speculative_decoding_verification_15_gb300 as pkg
+
+    a, b = _args(_cut(62, 128)), _args(_cut(63, 128))
+    want_a, want_b = pkg.cache_attention(*a), pkg.cache_attention(*b)
+    s, t, u = (torch.cuda.Stream() for _ in range(3))
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        pkg.cache_attention(*a)
+        s.synchronize()
+        one, out_one = _capture(a, s, calls=3)
+        two, out_two = _capture(b, s, calls=3)
+    torch.cuda.synchronize()
+    eager = []
+    for _ in range(20):
+        with torch.cuda.stream(t):
+            one.replay()
+        with torch.cuda.stream(u):
+            two.replay()
+        eager.append(pkg.cache_attention(*b, stream=s))
+        eager.append(pkg.cache_attention(*a))
+    torch.cuda.synchronize()
+    for got in out_one:
+        assert (got["status"] == 0).all() and torch.equal(got["out"], want_a["out"])
+    for got in out_two:
+        assert (got["status"] == 0).all() and torch.equal(got["out"], want_b["out"])
+    for i, got in enumerate(eager):
+        assert torch.equal(got["out"], (want_a if i % 2 else want_b)["out"])
+
+
+def test_two_streams_at_once():
+    import speculative_decoding_verification_15_gb300 as pkg
+
+    a, b = _args(_cut(64, 64)), _args(_cut(65, 64))
+    want = pkg.cache_attention(*a)["out"], pkg.cache_attention(*b)["out"]
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[pkg.cache_attention(*args, stream=s)["out"] for args, s in zip((a, b), streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for pair in got for o, w in zip(pair, want))

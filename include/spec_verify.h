@@ -447,13 +447,15 @@ int spec_kv_gather(const spec_kv_cache *cache, int B, const int32_t *cu_out, int
  *  out_lse     [n_tokens, num_query_heads] float, or NULL
  *  out_status  [B]: 0, SPEC_STATUS_BAD_LENGTH, SPEC_STATUS_BAD_PAGE or
  *              SPEC_STATUS_INTERNAL; rows of a failed request are unspecified
- *  ws          at least spec_cache_attention_workspace_size bytes, 256-byte aligned,
- *              ZERO-FILLED before its first use; every call leaves its counters zero,
+ *  ws          at least spec_cache_attention_workspace_size bytes, 256-byte aligned, the
+ *              first SPEC_CACHE_ATTENTION_COUNTERS of them ZERO
+ *              before its first use; every call leaves them zero,
  *              so one workspace serves any number of calls in stream order (after a
- *              call that reported SPEC_STATUS_INTERNAL, zero it again).  The workspace
+ *              call that reported SPEC_STATUS_INTERNAL, zero them again).  The workspace
  *              of another entry point must not be passed here.
  * Results are the same from call to call: partial sums are joined in a fixed order.
  */
+#define SPEC_CACHE_ATTENTION_COUNTERS 4096
 size_t spec_cache_attention_workspace_size(int num_query_heads, int num_heads, int head_dim, int dtype);
 int spec_cache_attention(const spec_kv_cache *cache, const void *q, int dtype, int64_t ld_q, int num_query_heads,
                          int n_tokens, int B, const int32_t *cu_query, int max_query, const int32_t *seq_len,

@@ -250,19 +250,25 @@ def _i32(t, device):
     return _as_i32(t, device)
 
 
+def _new_attention_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:binding.CACHE_ATTENTION_COUNTERS].zero_()  # the rest, some 20 MB, is written before it is read
+    return ws
+
+
 def _attention_workspace(device: torch.device, stream, nbytes: int) -> torch.Tensor:
-    """One zero-filled workspace for each device and stream: calls on one stream run in
-    order and may share it, calls on two streams may not.  A call that a graph captures
-    gets its own, out of the graph's memory: the graph keeps its address, and may be
-    replayed on any stream, next to this one's calls and after their workspace has been
-    replaced by a larger one."""
+    """One workspace for each device and stream: calls on one stream run in order and may
+    share it, calls on two streams may not.  A call that a graph captures gets its own,
+    out of the graph's memory: the graph keeps its address, and may be replayed on any
+    stream, next to this one's calls and after their workspace has been replaced by a
+    larger one."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        return _new_attention_workspace(device, nbytes)
     raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     with _ws_lock:
         ws = _attn_ws.get((device.index, raw))
         if ws is None or ws.numel() < nbytes:
-            ws = _attn_ws[(device.index, raw)] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            ws = _attn_ws[(device.index, raw)] = _new_attention_workspace(device, nbytes)
         return ws
 
 

@@ -24,6 +24,7 @@ SPEC_BF16, SPEC_F32 = 0, 1
 STATUS_OK, STATUS_BAD_TOKEN, STATUS_BAD_K, STATUS_BAD_TEMPERATURE, STATUS_NONFINITE = 0, 1, 2, 3, 4
 STATUS_INTERNAL, STATUS_BAD_LENGTH, STATUS_BAD_PAGE = 5, 2, 6
 KV_PAGE_SIZES, KV_MAX_HEAD_DIM = (16, 32, 64, 128), 256
+CACHE_ATTENTION_COUNTERS = 4096  # bytes at a workspace's start that are zero between calls
 
 _lock = threading.Lock()
 _lib = None
@@ -602,7 +603,8 @@ def spec_cache_attention_workspace_size(num_query_heads: int, num_heads: int, he
 def spec_cache_attention(q, cache, page_table, seq_len, cu_query, max_query: int, scale: float, window: int,
                          sinks: int, out, out_lse, out_status, workspace, stream=None) -> None:
     """q, out [tokens, query heads, head_dim]; seq_len [B]; cu_query [B + 1]; out_lse
-    [tokens, query heads] float32 or None; out_status [B]; workspace zeroed once."""
+    [tokens, query heads] float32 or None; out_status [B]; workspace uint8, its first
+    CACHE_ATTENTION_COUNTERS bytes zeroed once."""
     at = q.get_device()
     c = _cache_struct(cache, at)
     shape, dtype = q.shape, q.dtype

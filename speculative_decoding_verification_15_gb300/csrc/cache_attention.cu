@@ -1536,7 +1536,7 @@ extern "C" size_t spec_cache_attention_workspace_size(int num_query_heads, int n
         head_dim > SPEC_KV_MAX_HEAD_DIM || (dtype != SPEC_BF16 && dtype != SPEC_F32))
         return 0;
     const size_t slot = sizeof(float) * kMaxRows * ((size_t)head_dim + 3);
-    return sizeof(int) * kMaxCtas + 2 * kMaxCtas * slot;
+    return SPEC_CACHE_ATTENTION_COUNTERS + 2 * kMaxCtas * slot;
 }
 
 extern "C" int spec_cache_attention(const spec_kv_cache *cache, const void *q, int dtype, int64_t ld_q,
@@ -1583,7 +1583,8 @@ extern "C" int spec_cache_attention(const spec_kv_cache *cache, const void *q, i
     p.sinks = window > 0 ? sinks : 0;
     p.scale_log2 = scale * kLog2e;
     p.tickets = (int *)ws;
-    p.partial = (float *)((char *)ws + sizeof(int) * kMaxCtas);
+    static_assert(sizeof(int) * kMaxCtas <= SPEC_CACHE_ATTENTION_COUNTERS, "counters");
+    p.partial = (float *)((char *)ws + SPEC_CACHE_ATTENTION_COUNTERS);
     const cudaStream_t st = (cudaStream_t)cuda_stream;
     p.q_vec = !((uintptr_t)q & 15) && !((ld_q * esz) & 15);
     // bf16 heads of up to 128 columns (one swizzled row of a tile): the tensor cores, in

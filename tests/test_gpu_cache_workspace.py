@@ -96,3 +96,24 @@ def test_two_streams_at_once():
     got = [[pkg.cache_attention(*args, stream=s)["out"] for args, s in zip((a, b), streams)] for _ in range(20)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for pair in got for o, w in zip(pair, want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_only_the_counters_need_to_be_zero(dtype):
+    """The rest of a workspace may hold anything (here NaN), and a second call finds the
+    counters as the first did."""
+    from speculative_decoding_verification_15_gb300 import binding
+
+    x = U.Inputs(66, 900 + (np.arange(40) * 131) % 700, np.full(40, 4), 8, 2, 64, 64, dtype)
+    q, c, table, seq, cu, n = _args(x)
+    need = binding.spec_cache_attention_workspace_size(8, 2, 64, binding._dtype_code(q))
+    first = None
+    for fill in (0, 0xFF):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        ws[:binding.CACHE_ATTENTION_COUNTERS] = 0
+        for _ in range(2):
+            out, status = torch.empty_like(q), torch.empty(40, dtype=torch.int32, device="cuda")
+            binding.spec_cache_attention(q, c, table, seq, cu, n, 0.125, 0, 0, out, None, status, ws)
+            assert (status == 0).all() and (ws[:binding.CACHE_ATTENTION_COUNTERS] == 0).all()
+            first = out if first is None else first
+            assert torch.equal(out, first)

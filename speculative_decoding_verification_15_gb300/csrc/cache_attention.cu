@@ -47,6 +47,7 @@ struct AttnParams {
     float scale_log2;  // scale * log2(e)
     bool q_vec;        // rows of q are 16-byte aligned
     int *tickets;      // [kMaxCtas], zero between calls
+    int *failed;       // not zero: a call on this workspace has failed
     float *partial;    // [2 * kMaxCtas][rows * (D + 3)]
 };
 
@@ -323,6 +324,25 @@ __device__ __noinline__ void write_statuses(const AttnParams &p, int lane) {
         if (lane == 0)
             p.status[b] = !r.ok ? SPEC_STATUS_BAD_LENGTH : (bad ? SPEC_STATUS_BAD_PAGE : SPEC_STATUS_OK);
     }
+}
+
+// A CTA that cannot answer for its parts fails the whole call: every request, whatever
+// other CTAs wrote or have yet to write.  The word stays for the calls after this one,
+// which may find what this one left behind.  NT threads call it.
+template <int NT>
+__device__ __noinline__ void fail_call(const AttnParams &p) {
+    if (threadIdx.x == 0) *(volatile int *)p.failed = 1;
+    __threadfence();
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.B; b += NT) p.status[b] = SPEC_STATUS_INTERNAL;
+}
+
+// The thread that wrote a CTA's statuses looks at the word after them.  Either it sees
+// the word, or its statuses come before those of the CTA that sets it.
+__device__ __noinline__ void recheck_statuses(const AttnParams &p) {
+    __threadfence();
+    if (*(volatile int *)p.failed == 0) return;
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) p.status[b] = SPEC_STATUS_INTERNAL;
 }
 
 // ------------------------------------------------------------------ joining parts
@@ -672,6 +692,7 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
                 join_parts<T, kSimtThreads, R, ND>(p, x);
         }
     }
+    if (tid == 0) recheck_statuses(p);
 }
 
 // ------------------------------------------------------------------ tensor-core kernel
@@ -1213,6 +1234,8 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
                 values(g);
             }
         }
+        if (lane == 0) recheck_statuses(p);  // while the last tile is on its way out
+        __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax and sums
         const int grp = tid >> 7, t128 = tid & 127, w4 = warp & 3, r0 = grp * NR, D = p.c.head_dim;
@@ -1448,8 +1471,6 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
                 if (p.lse && x.whole && r < x.nrows) store_lse(p, x, x.rt * R + r, m_run, sum);
             }
             named_sync<128>(bar);
-            if (lost || dead)
-                for (int b = tid; b < p.B; b += C::kSoft) p.status[b] = SPEC_STATUS_INTERNAL;
             if (x.whole) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
@@ -1474,8 +1495,9 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    const bool lost = __syncthreads_or(dead);
     if (warp == C::kSoft / 32 + 1) tmem_free(tm, C::kCols);
+    if (lost) fail_call<kTcThreads<R, W>>(p);
 }
 
 // ------------------------------------------------------------------ host
@@ -1583,7 +1605,8 @@ extern "C" int spec_cache_attention(const spec_kv_cache *cache, const void *q, i
     p.sinks = window > 0 ? sinks : 0;
     p.scale_log2 = scale * kLog2e;
     p.tickets = (int *)ws;
-    static_assert(sizeof(int) * kMaxCtas <= SPEC_CACHE_ATTENTION_COUNTERS, "counters");
+    static_assert(sizeof(int) * (kMaxCtas + 1) <= SPEC_CACHE_ATTENTION_COUNTERS, "counters");
+    p.failed = (int *)((char *)ws + SPEC_CACHE_ATTENTION_COUNTERS) - 1;
     p.partial = (float *)((char *)ws + SPEC_CACHE_ATTENTION_COUNTERS);
     const cudaStream_t st = (cudaStream_t)cuda_stream;
     p.q_vec = !((uintptr_t)q & 15) && !((ld_q * esz) & 15);

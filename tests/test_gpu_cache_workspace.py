@@ -117,3 +117,35 @@ def test_only_the_counters_need_to_be_zero(dtype):
             assert (status == 0).all() and (ws[:binding.CACHE_ATTENTION_COUNTERS] == 0).all()
             first = out if first is None else first
             assert torch.equal(out, first)
+
+
+def _call(args, ws, scale=0.125):
+    from speculative_decoding_verification_15_gb300 import binding
+
+    q, c, table, seq, cu, n = args
+    out, status = torch.empty_like(q), torch.full((len(seq),), -1, dtype=torch.int32, device="cuda")
+    binding.spec_cache_attention(q, c, table, seq, cu, n, scale, 0, 0, out, None, status, ws)
+    return out, status
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("B", [1, 40, 1000])
+def test_a_failed_call_fails_for_every_request(dtype, B):
+    """A CTA whose wait ran out sets the word at the end of the counters: CTAs that write
+    their statuses only afterwards do not hide it (here all of them: the word is there
+    before the call), nor does any later call, until the counters are zeroed."""
+    from speculative_decoding_verification_15_gb300 import binding
+
+    x = U.Inputs(67, 300 + (np.arange(B) * 131) % 700, np.full(B, 2), 8, 2, 64, 64, dtype)
+    args = _args(x)
+    ws = torch.zeros(binding.spec_cache_attention_workspace_size(8, 2, 64, binding._dtype_code(x.q)), dtype=torch.uint8,
+                     device="cuda")
+    want, status = _call(args, ws)
+    assert (status == 0).all()
+    counters = ws[:binding.CACHE_ATTENTION_COUNTERS]
+    counters.view(torch.int32)[-1] = 1
+    for _ in range(2):
+        assert (_call(args, ws)[1] == 5).all()
+    counters.zero_()
+    out, status = _call(args, ws)
+    assert (status == 0).all() and torch.equal(out, want)

@@ -452,8 +452,10 @@ int spec_kv_gather(const spec_kv_cache *cache, int B, const int32_t *cu_out, int
  *              before its first use; every call leaves them zero,
  *              so one workspace serves any number of calls in stream order.  After a
  *              call that reported SPEC_STATUS_INTERNAL, zero them again: until then every
- *              call on the workspace reports it, for every request.  The workspace of
- *              another entry point must not be passed here.
+ *              call on the workspace reports it, for every request.  Counters that were not
+ *              zero are reported alike where an item is split between CTAs and its
+ *              counter does not add up.  The workspace of another entry point must not
+ *              be passed here.
  * Results are the same from call to call: partial sums are joined in a fixed order.
  */
 #define SPEC_CACHE_ATTENTION_COUNTERS 4096

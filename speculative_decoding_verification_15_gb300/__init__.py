@@ -4,7 +4,7 @@ The compute path is libspecverify.so (C ABI in include/spec_verify.h); this pack
 only builds it and marshals torch tensors into it.
 """
 from . import _build, binding  # noqa: F401
-from .api import (cache_attention, kv_append, kv_cache, kv_gather, markov_draft, markov_draft_topk,  # noqa: F401
+from .api import (cache_attention, cache_attention_reset, kv_append, kv_cache, kv_gather, markov_draft, markov_draft_topk,  # noqa: F401
                   schedule_threshold, schedule_verify_len, schedule_verify_len_stale,
                   verify_greedy, verify_greedy_early_exit, verify_greedy_flat, verify_sample,
                   verify_sample_early_exit, verify_sample_flat,

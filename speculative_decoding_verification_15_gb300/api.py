@@ -272,6 +272,19 @@ def _attention_workspace(device: torch.device, stream, nbytes: int) -> torch.Ten
         return ws
 
 
+def cache_attention_reset(device=None) -> None:
+    """Forget the workspaces kept for cache_attention's calls on the device (None: on
+    every one).  After a call that reported status 5 (an internal wait ran out) the
+    later calls on its stream report it too, until this one: they get a new workspace.
+    (A graph's calls zero their own in every replay.)"""
+    index = None if device is None else torch.device(device).index
+    if device is not None and index is None:
+        index = torch.cuda.current_device()
+    with _ws_lock:
+        for key in [k for k in _attn_ws if index is None or k[0] == index]:
+            del _attn_ws[key]
+
+
 def kv_cache(num_pages: int, num_heads: int, page_size: int, head_dim: int, device="cuda") -> KVCache:
     """An empty cache: codes [num_pages, num_heads, page_size, head_dim] and scales
     [num_pages, num_heads] for keys and values.  Any tensors of that form serve (a
@@ -317,7 +330,8 @@ def cache_attention(q, cache: KVCache, page_table, seq_len, cu_query, max_query:
     cache, causal among the new tokens: request b's queries are rows cu_query[b] ..
     cu_query[b+1] - 1 and sit at the last of its seq_len[b] cached positions.  window
     limits each query to the last `window` positions and the first `sinks`; scale
-    defaults to head_dim ** -0.5.  Returns out, lse (None unless want_lse), status."""
+    defaults to head_dim ** -0.5.  Returns out, lse (None unless want_lse), status; after
+    a status of 5, see cache_attention_reset."""
     dev = q.device
     n, heads, dim = q.shape
     out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)

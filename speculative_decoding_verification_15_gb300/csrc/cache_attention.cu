@@ -46,7 +46,7 @@ struct AttnParams {
     int B, ld_table, n_tokens, max_query, Hq, group, window, sinks;
     float scale_log2;  // scale * log2(e)
     bool q_vec;        // rows of q are 16-byte aligned
-    int *tickets;      // [kMaxCtas], zero between calls
+    uint64_t *tickets; // [kMaxCtas], zero between calls
     int *failed;       // not zero: a call on this workspace has failed
     float *partial;    // [2 * kMaxCtas][rows * (D + 3)]
 };
@@ -394,20 +394,26 @@ __device__ __forceinline__ float weight_of(float a, float m) { return a == kNegI
 // arrives last, which may then read the other parts.  NT threads call it, `bar` a
 // named barrier of theirs: it orders their stores before thread 0's release, and that
 // thread's acquire before their loads.
+// A counter holds, besides how many parts have arrived (low half), the sum of their
+// numbers from 1: one that does not add up has not started at zero, and fails the call.
 template <int NT>
-__device__ __forceinline__ bool arrive_last(const AttnParams &p, int first_cta, int parts, int *s_flag, int bar) {
+__device__ __forceinline__ bool arrive_last(const AttnParams &p, int first_cta, int parts, int *s_flag, int bar, bool &failed) {
     named_sync<NT>(bar);
     if (threadIdx.x == 0) {
-        int before;
-        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
-                     : "=r"(before)
-                     : "l"(p.tickets + first_cta)
+        const uint64_t mine = 1 + ((uint64_t)(blockIdx.x - first_cta + 1) << 32);
+        const uint64_t all = parts + ((uint64_t)((uint32_t)parts * (parts + 1) / 2) << 32);
+        uint64_t before;
+        asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;"
+                     : "=l"(before)
+                     : "l"(p.tickets + first_cta), "l"(mine)
                      : "memory");
-        *s_flag = before == parts - 1;
-        if (before == parts - 1) p.tickets[first_cta] = 0;  // for the next call
+        const bool last = before + mine == all, sound = last || (uint32_t)before < (uint32_t)parts - 1;
+        *s_flag = last ? 1 : (sound ? 0 : 2);
+        if (last) p.tickets[first_cta] = 0;  // for the next call
     }
     named_sync<NT>(bar);
-    return *s_flag != 0;
+    failed |= *s_flag == 2;
+    return *s_flag == 1;
 }
 
 // Joins the parts of an item in CTA order and writes its rows: a warp takes two rows at
@@ -526,6 +532,7 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
     const int D = p.c.head_dim, bs = p.c.page_size;
     if (warp == 0) write_statuses(p, lane);
     Share share = find_share<kSimtThreads>(p, R, s_scratch);
+    bool failed = false;
     for (;;) {
         const Part x = next_part(p, share, R);
         if (x.b < 0) break;
@@ -688,11 +695,12 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
                 slot[R * D + R + tid] = s_w[R + tid];
                 slot[R * D + 2 * R + tid] = s_w[tid];
             }
-            if (arrive_last<kSimtThreads>(p, x.c0, x.c1 - x.c0 + 1, &s_flag, 1))
+            if (arrive_last<kSimtThreads>(p, x.c0, x.c1 - x.c0 + 1, &s_flag, 1, failed))
                 join_parts<T, kSimtThreads, R, ND>(p, x);
         }
     }
-    if (tid == 0) recheck_statuses(p);
+    if (failed) fail_call<kSimtThreads>(p);  // the same in every thread
+    else if (tid == 0) recheck_statuses(p);
 }
 
 // ------------------------------------------------------------------ tensor-core kernel
@@ -1018,7 +1026,8 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
     Share share = find_share<kTcThreads<R, W>>(p, R, sm.scratch);  // it synchronises the CTA
     tc_fence_after();
     const uint32_t tm = sm.tmem, tS = tm, tO = tm + 4 * R;  // a buffer: R columns of each term
-    bool dead = false;  // a wait ran out: wait no more, finish, report
+    bool dead = false;    // a wait ran out: wait no more, finish, report
+    bool failed = false;  // something else to report
     auto wait = [&](uint64_t *bar, int parity) {
         if (!try_barrier(smem_addr(bar), parity) && !dead && !poll_barrier(smem_addr(bar), parity)) dead = true;
         __syncwarp();
@@ -1487,7 +1496,7 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
                     slot[R * D + R + r0 + t128] = sm.l[r0 + t128];
                     slot[R * D + 2 * R + r0 + t128] = sm.mo[r0 + t128];
                 }
-                if (arrive_last<C::kSoft>(p, x.c0, x.c1 - x.c0 + 1, &sm.flag, kAllBar))
+                if (arrive_last<C::kSoft>(p, x.c0, x.c1 - x.c0 + 1, &sm.flag, kAllBar, failed))
                     join_parts<uint16_t, C::kSoft, R, 1>(p, x);
             }
             __syncwarp();  // this warp reads the part no more
@@ -1495,7 +1504,7 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
         }
     }
     tc_fence_before();
-    const bool lost = __syncthreads_or(dead);
+    const bool lost = __syncthreads_or(dead || failed);
     if (warp == C::kSoft / 32 + 1) tmem_free(tm, C::kCols);
     if (lost) fail_call<kTcThreads<R, W>>(p);
 }
@@ -1604,8 +1613,8 @@ extern "C" int spec_cache_attention(const spec_kv_cache *cache, const void *q, i
     p.window = window < (1 << 30) ? window : (1 << 30);  // positions stay below 2^31
     p.sinks = window > 0 ? sinks : 0;
     p.scale_log2 = scale * kLog2e;
-    p.tickets = (int *)ws;
-    static_assert(sizeof(int) * (kMaxCtas + 1) <= SPEC_CACHE_ATTENTION_COUNTERS, "counters");
+    p.tickets = (uint64_t *)ws;
+    static_assert(sizeof(uint64_t) * kMaxCtas + sizeof(int) <= SPEC_CACHE_ATTENTION_COUNTERS, "counters");
     p.failed = (int *)((char *)ws + SPEC_CACHE_ATTENTION_COUNTERS) - 1;
     p.partial = (float *)((char *)ws + SPEC_CACHE_ATTENTION_COUNTERS);
     const cudaStream_t st = (cudaStream_t)cuda_stream;

@@ -149,3 +149,47 @@ def test_a_failed_call_fails_for_every_request(dtype, B):
     counters.zero_()
     out, status = _call(args, ws)
     assert (status == 0).all() and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("word", [1, 2, 5, 300, 1 << 20, -1, 1 + (1 << 32), (3 << 32) + 2])
+def test_counters_that_were_not_zero_are_reported(dtype, word):
+    """Two long requests, their items split between all CTAs: a counter that starts at
+    anything else would have a part join too early, or never."""
+    from speculative_decoding_verification_15_gb300 import binding
+
+    x = U.Inputs(68, [9000, 7777], [3, 1], 8, 2, 64, 64, dtype)
+    args = _args(x)
+    ws = torch.zeros(binding.spec_cache_attention_workspace_size(8, 2, 64, binding._dtype_code(x.q)), dtype=torch.uint8,
+                     device="cuda")
+    counters = ws[:binding.CACHE_ATTENTION_COUNTERS]
+    want, status = _call(args, ws)
+    assert (status == 0).all() and (counters == 0).all()
+    counters[:320 * 8].view(torch.int64).fill_(word)
+    for _ in range(2):
+        assert (_call(args, ws)[1] == 5).all()
+    counters.zero_()
+    out, status = _call(args, ws)
+    assert (status == 0).all() and torch.equal(out, want)
+
+
+def test_the_package_can_be_told_to_start_over():
+    import speculative_decoding_verification_15_gb300 as pkg
+    from speculative_decoding_verification_15_gb300 import api, binding
+
+    args = _args(_cut(69, 64))
+    want = pkg.cache_attention(*args)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    pkg.cache_attention(*args, stream=s)
+    torch.cuda.synchronize()
+    for ws in api._attn_ws.values():
+        ws[:binding.CACHE_ATTENTION_COUNTERS].fill_(1)
+    torch.cuda.synchronize()
+    for stream in (None, s):
+        assert (pkg.cache_attention(*args, stream=stream)["status"].cpu() == 5).all()
+    pkg.cache_attention_reset("cuda:0")
+    for stream in (None, s):
+        got = pkg.cache_attention(*args, stream=stream)
+        torch.cuda.synchronize()
+        assert (got["status"] == 0).all() and torch.equal(got["out"], want["out"])

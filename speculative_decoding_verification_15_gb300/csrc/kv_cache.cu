@@ -1,4 +1,6 @@
 // kv_cache.cu -- the 8-bit paged key/value cache: writing and reading back (sm_103a).
+#include <type_traits>
+
 #include "kv_common.cuh"
 
 namespace specv {
@@ -33,6 +35,26 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// q, a rounded quotient or product, for rounding to e4m3 as the exact one, which is larger
+// by a number of `rest`'s sign: rounding twice goes wrong only where q is a tie between
+// two codes (its low 19 bits are then zero) and the exact one is not.
+__device__ __forceinline__ float off_tie(float q, float rest) {
+    const uint32_t u = __float_as_uint(q);
+    if ((u & 0x7ffffu) || rest == 0.f || !(fabsf(q) < 500.f) || q == 0.f) return q;
+    return __uint_as_float((rest > 0.f) == (q > 0.f) ? u + 1 : u - 1);
+}
+// x / s for rounding to e4m3, s any positive number.  (It is at least 2^kExpMin; below
+// 2^-40 both are scaled so that the remainder does not underflow.)
+__device__ __noinline__ float quotient_for_e4m3(float x, float s) {
+    const float up = s < 0x1p-40f ? 0x1p60f : 1.f;
+    x *= up;
+    s *= up;
+    const float q = x / s;
+    return off_tie(q, fmaf(-q, s, x));
+}
+// A power of two whose inverse is a normal number.
+__device__ __forceinline__ bool power_of_two(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0 && x < 0x1p126f; }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
@@ -143,12 +165,18 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvParams p) {
     if (tid == 0) *scale_at = scale;
 
     char *codes = (char *)(kv ? p.c.v : p.c.k) + (int64_t)page * p.c.page_stride + (int64_t)h * p.c.head_stride;
-    const float inv = 1.f / scale;  // a power of two within the normal range
-    auto put = [&](int v, const float(&x)[8]) {
+    // A scale that this kernel wrote is a power of two, and multiplying by its inverse
+    // rounds nothing; one kept from another writer of the cache may be any number.
+    const float inv = 1.f / scale;
+    auto put = [&](auto exact, int v, const float(&x)[8]) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float a = x[2 * e] * inv, c = x[2 * e + 1] * inv;
+            if constexpr (!exact.value) {
+                a = quotient_for_e4m3(x[2 * e], scale);
+                c = quotient_for_e4m3(x[2 * e + 1], scale);
+            }
             if (infinite) {  // an infinity becomes a NaN: inf - inf
                 a = finite(x[2 * e]) ? a : x[2 * e] - x[2 * e];
                 c = finite(x[2 * e + 1]) ? c : x[2 * e + 1] - x[2 * e + 1];
@@ -159,18 +187,23 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvParams p) {
         *(uint2 *)(codes + (int64_t)(slot0 + (int)t) * p.c.token_stride + (v - t * vpt) * 8) =
             make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     };
+    auto put_all = [&](auto exact) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int v = tid + i * kAppendThreads;
-        if (v < nvec) put(v, held[i]);
-    }
-    for (int v = tid + kHeld * kAppendThreads; v < nvec; v += kAppendThreads) {
-        float x[8];
-        read(v, x);
-        put(v, x);
-    }
+        for (int i = 0; i < kHeld; ++i) {
+            const int v = tid + i * kAppendThreads;
+            if (v < nvec) put(exact, v, held[i]);
+        }
+        for (int v = tid + kHeld * kAppendThreads; v < nvec; v += kAppendThreads) {
+            float x[8];
+            read(v, x);
+            put(exact, v, x);
+        }
+    };
+    if (power_of_two(scale)) put_all(std::true_type{});
+    else put_all(std::false_type{});
     if (slot0 > 0 && scale > had) {  // the kept tokens, in the grown scale
         const float ratio = had / scale;
+        const bool exact = power_of_two(had);
         const int kept = slot0 * (D >> 4);
         for (int v = tid; v < kept; v += kAppendThreads) {
             const uint32_t t = quotient(v, p.per_head);
@@ -180,7 +213,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvParams p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 a = e4m3x2_to_float2(w[e] & 0xffffu), c = e4m3x2_to_float2(w[e] >> 16);
-                w[e] = float2_to_e4m3x2(a.x * ratio, a.y * ratio) | (float2_to_e4m3x2(c.x * ratio, c.y * ratio) << 16);
+                float p[4] = {a.x * ratio, a.y * ratio, c.x * ratio, c.y * ratio};
+                if (!exact) {
+                    const float f[4] = {a.x, a.y, c.x, c.y};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = off_tie(p[i], fmaf(f[i], ratio, -p[i]));
+                }
+                w[e] = float2_to_e4m3x2(p[0], p[1]) | (float2_to_e4m3x2(p[2], p[3]) << 16);
             }
             *at = q;
         }

@@ -548,6 +548,13 @@ def _flat(t, name, dtype, shape, index: int) -> int:
     return t.data_ptr()
 
 
+def _count(x: int, name: str) -> int:
+    """A count that the C entry takes in 32 bits (ctypes would drop the bits above)."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _launch(name: str, index: int, stream, *args) -> None:
     lib = _lib or load()
     if stream is None:
@@ -570,7 +577,7 @@ _I32 = torch.int32
 
 def spec_kv_append(cache, k, v, page_table, cached_len, cu_new, max_new: int, out_status, stream=None) -> None:
     """k, v [tokens, heads, head_dim]; cached_len [B]; cu_new [B + 1]; out_status [B]."""
-    at = k.get_device()
+    at, max_new = k.get_device(), _count(max_new, "max_new")
     c = _cache_struct(cache, at)
     heads, dim, n = c.num_heads, c.head_dim, k.shape[0]
     ldk = _token_rows(k, "k", heads, dim, at)
@@ -605,7 +612,8 @@ def spec_cache_attention(q, cache, page_table, seq_len, cu_query, max_query: int
     """q, out [tokens, query heads, head_dim]; seq_len [B]; cu_query [B + 1]; out_lse
     [tokens, query heads] float32 or None; out_status [B]; workspace uint8, its first
     CACHE_ATTENTION_COUNTERS bytes zeroed once."""
-    at = q.get_device()
+    at, max_query = q.get_device(), _count(max_query, "max_query")
+    window, sinks = _count(window, "window"), _count(sinks, "sinks")
     c = _cache_struct(cache, at)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3:

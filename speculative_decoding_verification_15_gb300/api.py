@@ -333,6 +333,8 @@ def cache_attention(q, cache: KVCache, page_table, seq_len, cu_query, max_query:
     defaults to head_dim ** -0.5.  Returns out, lse (None unless want_lse), status; after
     a status of 5, see cache_attention_reset."""
     dev = q.device
+    if dev.type != "cuda":  # before its workspace is looked up
+        raise ValueError("the cache and the call's tensors must be on one CUDA device")
     n, heads, dim = q.shape
     out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
     lse = torch.empty((n, heads), dtype=_F32, device=dev) if want_lse else None

@@ -25,3 +25,13 @@ def test_counts_past_32_bits(tensors, value):
     kv = q[:, :2]
     with pytest.raises(ValueError, match="max_new"):
         binding.spec_kv_append(c, kv, kv, table, one, cu, value, one)
+
+
+def test_tensors_that_are_not_on_a_gpu(tensors):
+    """All three calls refuse them alike."""
+    c, q, table, one, cu = tensors
+    kv = q[:, :2]
+    for call in (lambda: pkg.kv_append(c, kv, kv, table, one, cu, 1), lambda: pkg.kv_gather(c, table, cu, 1),
+                 lambda: pkg.cache_attention(q, c, table, one, cu, 1)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()

@@ -608,8 +608,8 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
             }
             __syncwarp();
             const uint32_t any = __ballot_sync(0xffffffffu, sees != 0);
-            uint32_t all = sees;  // rows that see every token some row sees
-            all = __reduce_and_sync(0xffffffffu, sees ? sees : 0xffffffffu);
+            // rows that see every token some row sees
+            const uint32_t all = __reduce_and_sync(0xffffffffu, sees ? sees : 0xffffffffu);
             const uint32_t rows_in = (1u << nrows) - 1;
             const bool uniform = (all & rows_in) == rows_in;
             for (uint32_t todo = any; todo; todo &= todo - 1) {
@@ -735,10 +735,11 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
 //  - A running reference moves only when a tile's is more than 2^64 above it, so sums
 //    are rescaled at a part's first tile and hardly ever after.
 //  - exp2 is the hardware's approximation, its error far below the rounding of P.
-// Roles: R / 16 groups of 128 threads for the softmax and the sums, one warp that issues the products, one or two that copy.  The first copying warp also
-// finds the CTA's parts and tells them kParts ahead.  S^T and O^T are double-buffered:
-// S^T of the next tile is multiplied while the softmax of this one runs, O^T of this
-// one while the sums take the last.
+// Roles: R / 16 groups of 128 threads for the softmax and the sums, one warp that issues
+// the products, one or two that copy.  The first copying warp also finds the CTA's parts
+// and tells the others of each while it copies the one before (kParts places).  S^T and
+// O^T are double-buffered: S^T of the next tile is multiplied while the softmax of this
+// one runs, O^T of this one while the sums take the last.
 //
 // What bounds it: the chain of one tile through its softmax warps, from tensor memory
 // through maxima, exponentials and two roundings to P and back, about 3000 cycles, of
@@ -837,7 +838,7 @@ struct TcShape {
 template <int R, int W>
 constexpr int kTcThreads = TcShape<R>::kSoft + 32 * (1 + W);
 
-constexpr int kParts = 4;  // parts known ahead
+constexpr int kParts = 4;  // places for parts that have been told and are not done with
 constexpr int kAllBar = 8, kLookBar = 9;  // named barriers of all softmax threads; group g's is 1 + g
 
 template <int R>
@@ -1032,11 +1033,6 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
         if (!try_barrier(smem_addr(bar), parity) && !dead && !poll_barrier(smem_addr(bar), parity)) dead = true;
         __syncwarp();
     };
-    auto wait_long = [&](uint64_t *bar, int parity) {
-        if (!try_barrier(smem_addr(bar), parity) && !dead && !poll_barrier(smem_addr(bar), parity)) dead = true;
-        __syncwarp();
-    };
-
     auto gone = [&] {
         dead = __any_sync(0xffffffffu, dead);
         return dead;
@@ -1054,7 +1050,7 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
     int sent = 0;  // past the last slot this warp filled
     auto copy_tile = [&](const CUtensorMap &map, int seq, int page, int h, int *pages) {
         const int slot = seq % NS, turn = seq / NS;
-        if (turn > 0) wait_long(&sm.empty[slot], (turn - 1) & 1);
+        if (turn > 0) wait(&sm.empty[slot], (turn - 1) & 1);
         if (gone()) return;
         sent = seq + 1;
         if (lane < ppt) pages[lane] = page >= 0 ? page : p.c.num_pages;  // past the map's end: reads as zeros
@@ -1077,8 +1073,8 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
     if (warp == C::kSoft / 32) {
         // ---------------------------------------------------------------- copies
         // Of the keys, and of the values if no second warp copies.  This warp also finds
-        // the parts and tells the others, one part ahead; page ids and scales come a batch
-        // of 32 pages ahead.
+        // the parts, and tells the others of the next one early in the last batch of each;
+        // page ids and scales come a batch of 32 pages ahead.
         int g = 0, n = 0;  // tiles, parts told
         auto tell_part = [&](const Part &x) {
             const int at = n % kParts;
@@ -1215,7 +1211,7 @@ __global__ void __launch_bounds__(kTcThreads<R, W>, TcShape<R>::kPerSM)
         auto values = [&](int g) {
             const int seq = 2 * g + 1, slot = seq % NS;
             wait(&sm.full[slot], (seq / NS) & 1);
-            wait_long(&sm.p_full, g & 1);
+            wait(&sm.p_full, g & 1);
             if (gone()) return;
             tc_fence_after();
             const uint64_t a = dv + slot * (kSlotBytes / 16);

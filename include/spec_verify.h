@@ -398,8 +398,11 @@ typedef struct spec_kv_cache {
  *   kept codes become e4m3(code * old / scale) when the scale grew;
  *   new codes are e4m3(entry / scale), round to nearest even, saturating at 448;
  *   a NaN or infinite entry becomes a NaN code.
- * Division by a power of two is exact, so each new entry is rounded once, and a kept
- * code loses bits only where it falls below the new scale's normal range.
+ * Each new entry is rounded once, whatever the scale, and where the scales are powers of
+ * two, as this call writes them, a kept code loses bits only where it falls below the new
+ * scale's normal range.  A scale does not shrink while its page keeps a token, even if the
+ * entries that set it are forgotten (a rejected draft's): the page's later entries are
+ * then rounded more coarsely than they need be, until it is written from its start.
  *
  *  k, v        rows of num_heads * head_dim elements of type dtype, ld_k / ld_v
  *              elements apart (slices of a fused projection's output are fine)
@@ -437,7 +440,14 @@ int spec_kv_gather(const spec_kv_cache *cache, int B, const int32_t *cu_out, int
  *   lse = log sum_j exp(s_j).
  * A query that sees nothing (P < 0) gets out = 0 and lse = -inf.  Pages that no query
  * of the request sees are not read and may hold any id.  A NaN code among a query's
- * visible entries makes its results NaN; unseen entries never matter.
+ * visible entries makes its results NaN; unseen entries never matter (but the scales of
+ * unseen pages next to seen ones may, for the last bits' rounding).
+ * With bf16 queries and heads of up to 128 columns some things are held in fewer than 32
+ * bits on the way: queries to 2^-17 of their row's largest entry (those above 2^-9 of it
+ * are exact), and each probability times its value's scale to 2^-8 of itself, or to 2^-18
+ * of the largest among those of its 128-token tile that the query sees; value scales
+ * below 2^-126 count as that.  Sums and everything else, and all of it for fp32 queries
+ * and wider heads, are in 32 bits.
  *
  *  q           rows of num_query_heads * head_dim elements of type dtype, ld_q
  *              elements apart

@@ -4,7 +4,8 @@
 //   out = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m),
 // computed in one pass over the cache: each part of the tokens keeps (m, l, o) with
 // l = sum 2^(x_j - m), o = sum 2^(x_j - m) v_j, and two parts join as
-//   m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), o likewise.
+//   m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), o likewise
+// (with a reference of its own, so that the values' scales do not cost it its range).
 //
 // Work split.  What has to be read is the cache, once: an item is (request, key head,
 // row tile), its rows the queries of the request that share the key head (token-major:
@@ -13,12 +14,12 @@
 // so long and short requests together, one long request alone and a full batch all
 // load every SM alike; where items are few, an item takes whole CTAs instead.  A CTA
 // whose part holds an item whole writes its output; an item cut by a boundary leaves
-// (m, l, o) of each part in the workspace, and the part that arrives last (a counter;
+// these of each part in the workspace, and the part that arrives last (a counter;
 // nobody waits) joins them in CTA order.
 //
 // Two kernels: bf16 queries with heads of up to 128 columns take the tensor cores; fp32
 // queries, wider heads and a cache that no tensor map can describe take fp32 arithmetic
-// (the verify batch of 64 requests below: 5480 us there, 121 us on the tensor cores).
+// (the verify batch of 64 requests below: 5420 us there, 128 us on the tensor cores).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -81,7 +82,7 @@ __device__ __forceinline__ Request load_request(const AttnParams &p, int b, int 
 // Starting and finishing an item costs a CTA about as much as kItemCost tiles, so on the
 // line an item is that much longer, ahead of its tiles -- where there are enough tiles
 // to go round: with fewer than kTilesEach a CTA, spreading the tiles matters more.  With
-// no such cost the verify batch measured below takes 142 us instead of 121.
+// no such cost the verify batch measured below takes 149 us instead of 128.
 constexpr int kItemCost = 3, kTilesEach = 4;
 __device__ __forceinline__ int64_t request_items(const AttnParams &p, const Request &r) {
     return (int64_t)p.c.num_heads * r.rt;
@@ -114,8 +115,8 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t u, int ctas) {
 // Few items: an item takes as many CTAs as it has runs of `each` tiles, and every CTA one
 // part, where that keeps `each` within kEachTries - 1 tiles of a fair share of all tiles;
 // cut by the line, most CTAs would have an end of one item and the start of the next,
-// and pay for both.  256 items of 11 tiles: 31 us so, 37 on the line; 128 of 4 to 5:
-// 21 us and 29; 192 of 20, on the line either way, 45 us.
+// and pay for both.  256 items of 11 tiles: 32 us so, 39 on the line; 128 of 5: 16 us
+// and 20; 192 of 20, on the line either way, 38 us.
 constexpr int kEachTries = 4;
 
 struct ShareScratch {  // shared memory of find_share
@@ -516,7 +517,7 @@ __device__ __noinline__ void join_parts(const AttnParams &p, const Part &x) {
 // Every warp keeps its own (m, l, o); they join in shared memory at the part's end.
 // Bound by instructions: two fp32 products of rows x tokens x columns and eight warp
 // reductions a token block.  9 requests of 1 to 5 fp32 queries, 10 heads on 2 of 80
-// columns, 40 to 1500 tokens: 29 us.
+// columns, 40 to 1500 tokens: 30 us.
 constexpr int kSimtRows = 8, kSimtThreads = 128;
 
 template <typename T, int ND>
@@ -742,19 +743,22 @@ __global__ void __launch_bounds__(kSimtThreads) attention_simt_kernel(AttnParams
 // one runs, O^T of this one while the sums take the last.
 //
 // What bounds it: the chain of one tile through its softmax warps, from tensor memory
-// through maxima, exponentials and two roundings to P and back, about 3000 cycles, of
+// through maxima, exponentials and two roundings to P and back, about 3200 cycles, of
 // which two (two CTAs) are under way on an SM; the issue slots are half full, the
 // tensor cores at an eighth, DRAM at two thirds.  R = 16 and 32 have two CTAs an SM
-// (with one, the first two batches below take 152 and 106 us instead of 121 and 90),
+// (with one, the first two batches below take 158 and 112 us instead of 128 and 91),
 // R = 64 has the shared memory and registers for one.  R is the smallest that holds a
 // request's rows: 38 requests of 8192 tokens and 8 key heads of 128 take, with 8 rows,
-// 103 us in R = 16, 107 in 32 and 153 in 64; with 32 rows 116 us in 32 and 167 in 64; with
-// 64 rows 194 us in either.  The bytes alone take 94 us.
-// Measured (time of a launch, codes read): 64 requests, 8 queries, 32 query and 8 key
-// heads of 128, 500 to 8000 tokens, pages of 64: 121 us, 4.6 TB/s.  Two requests of
-// 120000 and 131071 tokens, one query, 64 query heads: 90 us, 5.7 TB/s.  256 requests of
-// 1 to 8 queries, 4 key heads of 64, 60 to 3000 tokens, pages of 16: 108 us, 1.9 TB/s.
-// One request of one query over 1004 tokens: 12 to 14 us.
+// 103 us in R = 16, 109 in 32 and 175 in 64; with 32 rows 121 us in 32 and 189 in 64; with
+// 64 rows 217 us in 64, 232 in 32 and 374 in 16.  The bytes alone take 94 us.
+// Measured (a launch among others in a graph, codes read): 64 requests, 8 queries, 32
+// query and 8 key heads of 128, 500 to 8000 tokens, pages of 64: 128 us, 4.4 TB/s.  Two
+// requests of 120000 and 131071 tokens, one query, 64 query heads: 91 us, 5.7 TB/s.  256
+// requests of 1 to 8 queries, 4 key heads of 64, 60 to 3000 tokens, pages of 16: 109 us,
+// 1.9 TB/s.  One request of one query over 1004 tokens: 13.5 us.
+// With probabilities rounded next to the largest value scale of the tile these three took
+// 119, 89 and 107 us, and 64 rows 194, but a page far above the others cost those their
+// probabilities.
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kSlotBytes = kTile * 128;  // a tile of keys or values
 constexpr int kInfo = 8;                 // tiles whose scales are held at a time
@@ -1621,11 +1625,11 @@ extern "C" int spec_cache_attention(const spec_kv_cache *cache, const void *q, i
     if (esz == 2 && cache->head_dim <= 128 && codes_map(*cache, cache->k, &kmap) && codes_map(*cache, cache->v, &vmap)) {
         const int64_t rows = (int64_t)max_query * p.group;
         // One warp's copies go one after another, about 5 cycles a row and 20 a copy, so
-        // with small pages a second warp pays: 512 heads of 64 columns, 8192 tokens in
-        // pages of 16, take 113 us with one and 84 with two.  It costs registers: in pages
-        // of 64 the same takes 78 us with one and 82 with two.  With 32 rows there are none
-        // to spare (121 us with one, 172 with two); with 64 and one CTA an SM there are
-        // (205 us with one, 194 with two).
+        // with small pages a second warp pays: 304 heads of 64 columns, 8192 tokens in
+        // pages of 16, take 107 us with one and 84 with two.  It costs registers: in pages
+        // of 64 the same takes 79 us with one and 84 with two.  With 32 rows there are none
+        // to spare (128 us with one, 204 with two); with 64 and one CTA an SM there are
+        // (222 us with one, 217 with two).
         if (rows > 32) return launch_tc<64, 2>(p, dev, sms, kmap, vmap, st);
         if (rows > 16) return launch_tc<32, 1>(p, dev, sms, kmap, vmap, st);
         if (cache->page_size > 32) return launch_tc<16, 1>(p, dev, sms, kmap, vmap, st);

@@ -75,9 +75,9 @@ __device__ __forceinline__ bool request_range(const KvParams &p, int b, int &row
 // 128 x 256 elements, the first kHeld vectors a thread held in registers, the rest
 // read again out of L1.  A page is at most 4096 vectors of 8 and in a verify step one
 // or a few tokens, so a CTA is small: 128 threads.  64 requests of 8 tokens, 8 heads of
-// 128, bf16, take 6.3 us, launch and three dependent reads; 6 prompts of 700 to 8000
-// tokens, 4 heads of 96, fp32, 18.5 us, 4 TB/s of reading and writing, bound by the
-// instructions of each element's rounding and by the short CTAs' starts.
+// 128, bf16, take 4.0 us in a graph, launch and three dependent reads; 6 prompts of 700
+// to 8000 tokens, 4 heads of 96, fp32, 18.4 us, 4 TB/s of reading and writing (15.0 us
+// where the rows lie in L2): a short CTA waits for its rows with nothing else to do.
 constexpr int kHeld = 4, kAppendThreads = 128;
 
 template <int ESZ, bool VEC>
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvParams p) {
 // the row's request by bisection of the offsets, its page and slot; then all threads
 // stream 16 codes at a time.  The first ceil(B / 8) CTAs instead answer for the
 // requests' lengths and pages, one warp a request.  Bound by DRAM writes: 16 prompts of
-// 2000 to 8000 tokens, 8 heads of 128, read back as bf16 take 82 us, 5.9 TB/s (95 us
-// with two 16-byte stores for each 32 bytes); three short ends of caches 6.2 us.
+// 2000 to 8000 tokens, 8 heads of 128, read back as bf16 take 80 us, 6.1 TB/s (95 us
+// with two 16-byte stores for each 32 bytes); three short ends of caches 3.0 us.
 constexpr int kGatherThreads = 256, kGatherRows = 32;
 
 // 16 values (32 bytes of bf16, 64 of fp32).  WIDE: 32-byte aligned, and stored 32 bytes

@@ -77,6 +77,7 @@ typedef enum { SPEC_BF16 = 0, SPEC_F32 = 1 } spec_dtype;
                                           negative, decreasing or past the arrays or its pages  */
 #define SPEC_STATUS_BAD_PAGE 6         /* cache calls: a page the request needs is not in
                                           [0, num_pages)                                        */
+#define SPEC_STATUS_NO_PAGES 7         /* spec_kv_plan: the free list cannot serve the request  */
 /* Rows read: target and draft rows 0..k_b-1 (target only for greedy requests); the
  * target row k_b only when every draft is accepted (it holds the bonus token).
  * A request with a non-zero status has out_accepted[b] = 0, every token -1 and
@@ -474,6 +475,90 @@ int spec_cache_attention(const spec_kv_cache *cache, const void *q, int dtype, i
                          int n_tokens, int B, const int32_t *cu_query, int max_query, const int32_t *seq_len,
                          const int32_t *page_table, int ld_table, float scale, int window, int sinks, void *out,
                          float *out_lse, int32_t *out_status, void *ws, size_t ws_bytes, void *cuda_stream);
+
+/*
+ * Block tables and slot maps, built on the GPU from the requests' lengths.  Request b
+ * keeps its first keep_len[b] cached tokens (what it holds behind them is forgotten: a
+ * rejected draft, or everything when it has ended) and gets new_len[b] more.  It needs
+ *   need_b = ceil((keep_len[b] + new_len[b]) / page_size)
+ * pages: it gives back its pages need_b .. held[b] - 1, or takes as many as it lacks.
+ *
+ *  free_pages   [num_pages] the free list, a stack of page ids; free_count [1] how many.
+ *               Given pages go on top, request after request in the order of their table
+ *               entries, before any are taken; the pages taken, `all` in this call, are the
+ *               `all` topmost, handed out from the lowest of them up in the same order.  (So
+ *               taking pages and giving the same ones back leaves the list as it was.)
+ *               Entries at and above the count are unspecified.
+ *  page_table   [B, ld_table], held [B]: updated; an entry given back becomes -1.  The
+ *               first held[b] entries are the request's own: a page in two tables would be
+ *               given back twice.
+ *  n_out        rows of out_slot and out_position; request b's new tokens are rows
+ *               out_cu[b] .. out_cu[b+1] - 1, out_cu [B + 1] the sums of new_len
+ *  out_seq_len  [B] keep_len + new_len, or keep_len alone for a request that failed
+ *  out_position [n_out] each new token's position in its request
+ *  out_slot     [n_out] page * page_size + position % page_size, where the token goes; -1
+ *               for a failed request's tokens.  Rows behind the last token hold -1 in both.
+ *  out_status   [B]: 0; SPEC_STATUS_BAD_LENGTH (a negative length, more tokens than ld_table
+ *               pages hold, more kept than held, held outside [0, ld_table], rows past n_out;
+ *               a negative new_len counts as 0 rows); SPEC_STATUS_NO_PAGES (requests are
+ *               served in order: from the first whose pages the list cannot supply, none that
+ *               lacks pages gets any).  A failed request keeps its table and held.
+ * B * ld_table must stay below 2^31.  One kernel, no workspace; it may be captured.  Calls
+ * on one pool must follow one another in stream order.
+ */
+int spec_kv_plan(int32_t *free_pages, int32_t *free_count, int num_pages, int page_size, int32_t *page_table,
+                 int ld_table, int32_t *held, int B, const int32_t *keep_len, const int32_t *new_len, int n_out,
+                 int32_t *out_cu, int32_t *out_seq_len, int64_t *out_slot, int32_t *out_position, int32_t *out_status,
+                 void *cuda_stream);
+
+/*
+ * Rotary positions.  For pair i < pairs of each head's columns, with the angle
+ *   a = position[axis[i], token] * freq[i]   radians,
+ *   (x, y) -> scale * (x cos a - y sin a, y cos a + x sin a),
+ * (x, y) being columns (i, i + pairs), or (2 i, 2 i + 1) if adjacent; columns 2 * pairs ..
+ * are copied.  Angles keep their bits at every position that an int32 holds (off by 2^-25
+ * turns at most, for the value of freq that its 53 bits hold); sines and cosines are in 32
+ * bits.
+ *
+ *  q, k         rows of num_query_heads (num_heads) * head_dim elements of type dtype, ld
+ *               elements apart; num_heads 0: no keys.  out_q, out_k likewise; each may be its
+ *               input (in place), but must not overlap it otherwise.
+ *  position     [num_axes] rows of n_tokens, ld_position apart (unused for one axis)
+ *  freq         [pairs] double; axis [pairs] int32 in [0, num_axes) (others count as the
+ *               nearest), NULL for one axis
+ *  head_dim     at most SPEC_KV_MAX_HEAD_DIM; 2 * pairs <= head_dim; scale finite
+ * One kernel, no workspace.
+ */
+int spec_rotary(const void *q, const void *k, int dtype, int64_t ld_q, int64_t ld_k, int num_query_heads, int num_heads,
+                int head_dim, int n_tokens, const int32_t *position, int64_t ld_position, int num_axes,
+                const double *freq, const int32_t *axis, int pairs, int adjacent, float scale, void *out_q, void *out_k,
+                int64_t ld_out_q, int64_t ld_out_k, void *cuda_stream);
+
+/*
+ * Attention of packed prompts over their own keys and values (before, or instead of,
+ * reading them from the cache).  Request b's n_b = cu_query[b+1] - cu_query[b] queries are
+ * the last n_b of its m_b = cu_key[b+1] - cu_key[b] tokens (cu_key NULL: the same tokens):
+ * query t is at position P = m_b - n_b + t and sees the positions j <= P with
+ *   window == 0,  or  j > P - window,  or  j < sinks.
+ * For query head h, with key head h / (num_query_heads / num_heads):
+ *   s_j = scale * (q . k_j),  out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j).
+ * A query that sees nothing (P < 0) gets out = 0 and lse = -inf.  What a query does not
+ * see never matters, NaN included.  Rows outside every request are not written.
+ *
+ *  q, k, v      rows of heads * head_dim elements of type dtype, ld elements apart (slices
+ *               of a fused projection's output are fine)
+ *  head_dim     a multiple of 16, at most SPEC_KV_MAX_HEAD_DIM
+ *  n_query, n_key  rows of q, out, out_lse and of k, v; max_query a bound on every n_b
+ *  scale        positive and finite; window >= 0; sinks >= 0 (unused when window == 0)
+ *  out          [n_query, num_query_heads, head_dim] of type dtype, 16-byte aligned
+ *  out_lse      [n_query, num_query_heads] float, or NULL
+ *  out_status   [B]: 0 or SPEC_STATUS_BAD_LENGTH (nothing of the request is written)
+ */
+int spec_prompt_attention(const void *q, const void *k, const void *v, int dtype, int64_t ld_q, int64_t ld_k,
+                          int64_t ld_v, int num_query_heads, int num_heads, int head_dim, int n_query, int n_key, int B,
+                          const int32_t *cu_query, int max_query, const int32_t *cu_key, float scale, int window,
+                          int sinks, void *out, float *out_lse, int32_t *out_status, void *cuda_stream);
 
 /* Short text for a return code. */
 const char *spec_error_string(int err);

@@ -13,7 +13,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libspecverify.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
-SOURCES = ["verify.cu", "schedule.cu", "markov.cu", "kv_cache.cu", "cache_attention.cu"]
+SOURCES = ["verify.cu", "schedule.cu", "markov.cu", "kv_cache.cu", "cache_attention.cu", "page_plan.cu", "rotary.cu",
+           "prompt_attention.cu"]
 HEADERS = ["spec_common.cuh", "kv_common.cuh", "tcgen05.cuh"]
 
 NVCC_FLAGS = [

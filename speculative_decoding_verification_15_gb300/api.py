@@ -12,7 +12,7 @@ import threading
 import torch
 
 from . import binding
-from .binding import KVCache
+from .binding import KVCache, PagePool
 
 _ws_lock = threading.Lock()
 _ws_cache: dict[int, torch.Tensor] = {}
@@ -343,4 +343,96 @@ def cache_attention(q, cache: KVCache, page_table, seq_len, cu_query, max_query:
     binding.spec_cache_attention(q, cache, _i32(page_table, dev), _i32(seq_len, dev), _i32(cu_query, dev), max_query,
                                  dim ** -0.5 if scale is None else scale, window, sinks, out, lse, status,
                                  _attention_workspace(dev, stream, nbytes), stream)
+    return {"out": out, "lse": lse, "status": status}
+
+
+# ------------------------------------------------------------------ prompts into the cache
+def kv_pool(num_pages: int, device="cuda") -> PagePool:
+    """A pool in which every page is free; page 0 is handed out last."""
+    free = torch.arange(num_pages, dtype=torch.int32, device=device)
+    return PagePool(free, torch.full((1,), num_pages, dtype=torch.int32, device=device))
+
+
+@_on_its_stream
+def kv_plan(pool: PagePool, page_table, held, keep_len, new_len, page_size: int, n_out: int, stream=None) -> dict:
+    """Build the cache calls' tables on the GPU.  Request b keeps keep_len[b] cached tokens
+    and gets new_len[b] more: it takes pages from the pool, or gives back those it needs no
+    longer (a rejected draft's; all of them for two zeros).  pool, page_table [B, pages] and
+    held [B] (int32, contiguous) are updated in place.  Returns cu_new [B + 1], seq_len [B],
+    slot [n_out] (int64: page * page_size + place in it), position [n_out] and status [B];
+    n_out bounds the new tokens, and rows behind the last one hold -1."""
+    dev = page_table.device
+    B = page_table.shape[0]
+    ints = torch.empty(3 * B + 1 + n_out, dtype=_I32, device=dev)  # one allocation for what is int32
+    cu, seq_len, status, position = ints.split((B + 1, B, B, n_out))
+    slot = torch.empty(n_out, dtype=torch.int64, device=dev)
+    binding.spec_kv_plan(pool, page_table, held, _i32(keep_len, dev), _i32(new_len, dev), page_size, cu, seq_len, slot,
+                         position, status, stream)
+    return {"cu_new": cu, "seq_len": seq_len, "slot": slot, "position": position, "status": status}
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, sections=None, interleaved: bool = False,
+                       per_axis: bool = False, device="cuda"):
+    """freq (float64 [rotary_dim / 2], radians a position) and axis (int32, None for one
+    axis) of each pair for rotary().  sections: how many pairs each axis has, in blocks one
+    after another, or by turns (interleaved: one pair of each axis that has some left).
+    freq is base ** (-i / pairs) of the pair, or with per_axis base ** (-n / section) of the
+    axis's n-th one.  Long contexts' scalings are changes of freq."""
+    pairs = rotary_dim // 2
+    parts = [pairs] if sections is None else [int(n) for n in sections]
+    if rotary_dim % 2 or rotary_dim < 0 or sum(parts) != pairs or min(parts, default=0) < 0:
+        raise ValueError(f"sections must sum to the {rotary_dim} // 2 pairs of columns, got {parts}")
+    if interleaved:
+        axis = [a for turn in range(max(parts)) for a, n in enumerate(parts) if turn < n]
+    else:
+        axis = [a for a, n in enumerate(parts) for _ in range(n)]
+    nth, seen = [], [0] * len(parts)
+    for i, a in enumerate(axis):
+        nth.append(seen[a] / parts[a] if per_axis else i / pairs)
+        seen[a] += 1
+    freq = torch.tensor([float(base) ** -x for x in nth], dtype=torch.float64, device=device)
+    return freq, None if len(parts) == 1 else torch.tensor(axis, dtype=_I32, device=device)
+
+
+@_on_its_stream
+def rotary(q, k, position, freq, axis=None, adjacent: bool = False, scale: float = 1.0, out_q=None, out_k=None,
+           stream=None) -> dict:
+    """Rotate queries q and keys k (or None) [tokens, heads, head_dim] by their positions:
+    position int32 [tokens], or [axes, tokens] with the axis of each pair (see
+    rotary_frequencies).  A pair is columns (i, i + pairs), or (2 i, 2 i + 1) if adjacent;
+    columns past the pairs are copied; scale multiplies what is rotated.  out_q and out_k may
+    be q and k themselves (slices of a fused projection's output, for instance).  Returns q
+    and k."""
+    dev = q.device
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if out_k is None and k is not None:
+        out_k = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    binding.spec_rotary(q, k, _i32_rows(position, dev), freq, axis, adjacent, scale, out_q, out_k, stream)
+    return {"q": out_q, "k": out_k}
+
+
+def _i32_rows(t, device):
+    """int32 with contiguous rows on the device; as it is where it already is that."""
+    if t.dtype is _I32 and t.device == device and (t.stride(-1) == 1 or t.shape[-1] <= 1):
+        return t
+    return _as_i32(t, device)
+
+
+@_on_its_stream
+def prompt_attention(q, k, v, cu_query, max_query: int, cu_key=None, scale: float | None = None, window: int = 0,
+                     sinks: int = 0, want_lse: bool = False, stream=None) -> dict:
+    """Causal attention of packed prompts: q [queries, query heads, head_dim] over k, v
+    [keys, heads, head_dim]; request b's queries are rows cu_query[b] .. cu_query[b+1] - 1,
+    and the last of its keys, rows cu_key[b] .. (None: the same rows).  window limits each
+    query to the last `window` positions and the first `sinks`; scale defaults to
+    head_dim ** -0.5.  Returns out, lse (None unless want_lse), status."""
+    dev = q.device
+    n, heads, dim = q.shape
+    out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+    lse = torch.empty((n, heads), dtype=_F32, device=dev) if want_lse else None
+    cu_query = _i32(cu_query, dev)
+    status = torch.empty(max(0, cu_query.numel() - 1), dtype=_I32, device=dev)
+    binding.spec_prompt_attention(q, k, v, cu_query, max_query, _i32(cu_key, dev), dim ** -0.5 if scale is None else scale,
+                                  window, sinks, out, lse, status, stream)
     return {"out": out, "lse": lse, "status": status}

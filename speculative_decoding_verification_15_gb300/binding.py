@@ -22,7 +22,7 @@ SPEC_OK, SPEC_EINVAL, SPEC_ECUDA, SPEC_EUNSUPPORTED, SPEC_EWORKSPACE = 0, 1, 2, 
 SPEC_ESCRATCH = 5
 SPEC_BF16, SPEC_F32 = 0, 1
 STATUS_OK, STATUS_BAD_TOKEN, STATUS_BAD_K, STATUS_BAD_TEMPERATURE, STATUS_NONFINITE = 0, 1, 2, 3, 4
-STATUS_INTERNAL, STATUS_BAD_LENGTH, STATUS_BAD_PAGE = 5, 2, 6
+STATUS_INTERNAL, STATUS_BAD_LENGTH, STATUS_BAD_PAGE, STATUS_NO_PAGES = 5, 2, 6, 7
 KV_PAGE_SIZES, KV_MAX_HEAD_DIM = (16, 32, 64, 128), 256
 CACHE_ATTENTION_COUNTERS = 4096  # bytes at a workspace's start that are zero between calls
 
@@ -56,6 +56,13 @@ class KVCache(NamedTuple):
     v: torch.Tensor
     k_scale: torch.Tensor
     v_scale: torch.Tensor
+
+
+class PagePool(NamedTuple):
+    """The cache's free pages: a stack of ids [pages] int32 whose first count[0] entries
+    are free, and that count [1] int32."""
+    free: torch.Tensor
+    count: torch.Tensor
 
 
 def lib_path() -> str:
@@ -116,6 +123,14 @@ def load(path: str | None = None):
         lib.spec_cache_attention.argtypes = [C, P, I32, I64, I32, I32, I32, P, I32, P, P, I32, ctypes.c_float, I32,
                                              I32, P, P, P, P, SZ, P]
         lib.spec_cache_attention.restype = I32
+        lib.spec_kv_plan.argtypes = [P, P, I32, I32, P, I32, P, I32, P, P, I32, P, P, P, P, P, P]
+        lib.spec_kv_plan.restype = I32
+        lib.spec_rotary.argtypes = [P, P, I32, I64, I64, I32, I32, I32, I32, P, I64, I32, P, P, I32, I32, ctypes.c_float,
+                                    P, P, I64, I64, P]
+        lib.spec_rotary.restype = I32
+        lib.spec_prompt_attention.argtypes = [P, P, P, I32, I64, I64, I64, I32, I32, I32, I32, I32, I32, P, I32, P,
+                                              ctypes.c_float, I32, I32, P, P, P, P]
+        lib.spec_prompt_attention.restype = I32
         lib.spec_error_string.argtypes = [I32]
         lib.spec_error_string.restype = ctypes.c_char_p
         lib.spec_last_cuda_error.argtypes = []
@@ -629,6 +644,98 @@ def spec_cache_attention(q, cache, page_table, seq_len, cu_query, max_query: int
             None if out_lse is None else _flat(out_lse, "out_lse", torch.float32, (n, heads), at),
             _flat(out_status, "out_status", _I32, (B,), at), _flat(workspace, "workspace", torch.uint8, (nbytes,), at),
             nbytes)
+
+
+def spec_kv_plan(pool, page_table, held, keep_len, new_len, page_size: int, out_cu, out_seq_len, out_slot, out_position,
+                 out_status, stream=None) -> None:
+    """page_table [B, pages] and held [B], updated in place as is the pool; keep_len,
+    new_len [B]; out_cu [B + 1], out_seq_len [B], out_slot [rows] int64, out_position
+    [rows], out_status [B]."""
+    free, count = pool
+    at = free.get_device()
+    if at < 0:
+        raise ValueError("the pool and the call's tensors must be on one CUDA device")
+    (B, width), n = page_table.shape, out_slot.shape[0]
+    one = (B,)
+    _launch("spec_kv_plan", at, stream, _flat(free, "free", _I32, (free.numel(),), at), _flat(count, "count", _I32, (1,), at),
+            free.numel(), _count(page_size, "page_size"), _flat(page_table, "page_table", _I32, (B, width), at), width,
+            _flat(held, "held", _I32, one, at), B, _flat(keep_len, "keep_len", _I32, one, at),
+            _flat(new_len, "new_len", _I32, one, at), n, _flat(out_cu, "out_cu", _I32, (B + 1,), at),
+            _flat(out_seq_len, "out_seq_len", _I32, one, at), _flat(out_slot, "out_slot", torch.int64, (n,), at),
+            _flat(out_position, "out_position", _I32, (n,), at), _flat(out_status, "out_status", _I32, one, at))
+
+
+def _head_rows(t, name, index: int):
+    """Tokens, heads, head_dim and row stride of [tokens, heads, head_dim] rows."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(shape)}")
+    n, heads, dim = shape
+    return n, heads, dim, _token_rows(t, name, heads, dim, index) if n else heads * dim
+
+
+def spec_rotary(q, k, position, freq, axis, adjacent: bool, scale: float, out_q, out_k, stream=None) -> None:
+    """q [tokens, heads, head_dim] and k (or None) into out_q and out_k of the same form
+    (or themselves); position int32 [tokens] or [axes, tokens], freq float64 [pairs], axis
+    int32 [pairs] or None for one axis."""
+    at = q.get_device()
+    if at < 0:
+        raise ValueError("the call's tensors must be on one CUDA device")
+    n, heads, dim, ldq = _head_rows(q, "q", at)
+    dtype, keys, ldk, ldok = q.dtype, 0, 0, 0
+    no, ho, do, ldo = _head_rows(out_q, "out_q", at)
+    if out_q.dtype is not dtype or (no, ho, do) != (n, heads, dim):
+        raise ValueError("out_q must have q's shape and dtype")
+    if k is not None:
+        nk, keys, dk, ldk = _head_rows(k, "k", at)
+        if k.dtype is not dtype or nk != n or dk != dim:
+            raise ValueError("q and k must share tokens, head_dim and dtype")
+        no, ho, do, ldok = _head_rows(out_k, "out_k", at)
+        if out_k.dtype is not dtype or (no, ho, do) != (n, keys, dim):
+            raise ValueError("out_k must have k's shape and dtype")
+    if (position.dtype is not _I32 or position.dim() not in (1, 2) or position.shape[-1] != n or position.get_device() != at
+            or (n > 1 and position.stride(-1) != 1)):
+        raise ValueError(f"position must be int32 [{n}] or [axes, {n}] with contiguous rows on q's device")
+    axes = 1 if position.dim() == 1 else position.shape[0]
+    ldp = position.stride(0) if axes > 1 else 0
+    if axes < 1 or (axes > 1 and ldp < n):
+        raise ValueError("position must have one row or more that do not overlap")
+    pairs = freq.numel()
+    if axes > 1 and axis is None:
+        raise ValueError("positions of several axes need the axis of each pair")
+    _launch("spec_rotary", at, stream, q.data_ptr(), None if k is None else k.data_ptr(), _dtype_code(q), ldq, ldk, heads,
+            keys, dim, n, position.data_ptr(), ldp, axes, _flat(freq, "freq", torch.float64, (pairs,), at),
+            None if axis is None else _flat(axis, "axis", _I32, (pairs,), at), pairs, int(bool(adjacent)), scale,
+            out_q.data_ptr(), None if k is None else out_k.data_ptr(), ldo, ldok)
+
+
+def spec_prompt_attention(q, k, v, cu_query, max_query: int, cu_key, scale: float, window: int, sinks: int, out, out_lse,
+                          out_status, stream=None) -> None:
+    """q, out [queries, query heads, head_dim]; k, v [keys, heads, head_dim]; cu_query
+    [B + 1]; cu_key [B + 1], or None where the keys are the queries' tokens; out_lse
+    [queries, query heads] float32 or None; out_status [B]."""
+    at, max_query = q.get_device(), _count(max_query, "max_query")
+    window, sinks = _count(window, "window"), _count(sinks, "sinks")
+    if at < 0:
+        raise ValueError("the call's tensors must be on one CUDA device")
+    n, heads, dim, ldq = _head_rows(q, "q", at)
+    m, keys, dk, ldk = _head_rows(k, "k", at)
+    mv, keys_v, dv, ldv = _head_rows(v, "v", at)
+    dtype = q.dtype
+    if not dk == dv == dim or mv != m or keys_v != keys or k.dtype is not dtype or v.dtype is not dtype:
+        raise ValueError("q, k and v must share head_dim and dtype, k and v their tokens and heads")
+    offsets = cu_query.shape
+    if len(offsets) != 1 or offsets[0] < 1:
+        raise ValueError("cu_query must be [B + 1]")
+    if cu_key is None and m != n:
+        raise ValueError("without cu_key the keys are the queries' tokens")
+    B = offsets[0] - 1
+    _launch("spec_prompt_attention", at, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), ldq, ldk, ldv,
+            heads, keys, dim, n, m, B, _flat(cu_query, "cu_query", _I32, offsets, at), max_query,
+            None if cu_key is None else _flat(cu_key, "cu_key", _I32, offsets, at), scale, window, sinks,
+            _flat(out, "out", dtype, q.shape, at),
+            None if out_lse is None else _flat(out_lse, "out_lse", torch.float32, (n, heads), at),
+            _flat(out_status, "out_status", _I32, (B,), at))
 
 
 def profile_enable(on: bool) -> None:

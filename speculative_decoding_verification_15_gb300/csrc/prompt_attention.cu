@@ -1,0 +1,375 @@
+// prompt_attention.cu -- causal attention of packed prompts (sm_103a).
+//
+// Mathematics.  With log2 scores x_j = scale * log2(e) * (q . k_j), a row's output is
+//   out = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m)
+// for any reference m; one pass over the keys keeps (m, l, o) and multiplies l and o by
+// 2^(m - m') when the reference moves to m'.
+//
+// Work split.  An item is (request, key head, row tile); a row tile's rows are queries of
+// the request that share the key head, token-major: row = t * group + g, so that grouped
+// heads read a key tile once and a diagonal tile wastes little.  A tile of keys that no row
+// of the item sees is not visited; one that every row sees in full is not masked.
+//
+// fp32 queries, and bf16 where the tensor cores cannot serve (odd strides), take fp32
+// arithmetic throughout: attention_rows_kernel.
+#include <atomic>
+
+#include "kv_common.cuh"
+
+namespace specv {
+namespace {
+
+struct PromptParams {
+    const void *q, *k, *v;
+    void *out;
+    float *lse;
+    const int32_t *cu_q, *cu_k;
+    int32_t *status;
+    int64_t ld_q, ld_k, ld_v;
+    int B, n_q, n_k, max_query, Hq, H, group, D, window, sinks;
+    float scale_log2;
+};
+
+struct Prompt {
+    int row0, n, key0, m;  // first query row, queries, first key row, keys; n = 0 where unusable
+    bool ok;
+};
+
+__device__ __forceinline__ Prompt load_prompt(const PromptParams &p, int b) {
+    Prompt r;
+    r.row0 = p.cu_q[b];
+    const int row1 = p.cu_q[b + 1];
+    r.key0 = p.cu_k[b];
+    const int key1 = p.cu_k[b + 1];
+    r.ok = r.row0 >= 0 && row1 >= r.row0 && row1 <= p.n_q && r.key0 >= 0 && key1 >= r.key0 && key1 <= p.n_k;
+    r.n = row1 - r.row0;
+    r.m = key1 - r.key0;
+    r.ok = r.ok && r.n <= p.max_query;
+    if (!r.ok) r.n = r.m = 0;
+    return r;
+}
+
+__device__ __forceinline__ void write_prompt_statuses(const PromptParams &p, int first, int step) {
+    for (int b = first; b < p.B; b += step) p.status[b] = load_prompt(p, b).ok ? SPEC_STATUS_OK : SPEC_STATUS_BAD_LENGTH;
+}
+
+// Key tiles of a row tile: [0, s1) hold first tokens kept visible, [w0, end) the rest.
+struct Span {
+    int s1, w0, count;
+    __device__ __forceinline__ int tile(int i) const { return i < s1 ? i : w0 + (i - s1); }
+};
+template <int TK>
+__device__ __forceinline__ Span span_of(const PromptParams &p, int pos0, int pos1) {
+    Span s = {0, 0, 0};
+    if (pos1 < 0) return s;
+    const int low = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;  // below it only sinks are seen
+    s.w0 = low / TK;
+    s.s1 = min((min(p.sinks, low) + TK - 1) / TK, s.w0);
+    s.count = s.s1 + pos1 / TK + 1 - s.w0;
+    return s;
+}
+__device__ __forceinline__ bool visible(const PromptParams &p, int pos, int j) {
+    return j <= pos && (p.window == 0 || j > pos - p.window || j < p.sinks);
+}
+
+// ------------------------------------------------------------------ fp32 arithmetic
+// A CTA takes an item of R rows (16 threads down, 16 across: R / 16 rows and 4 keys a thread)
+// and walks over tiles of 64 keys in shared memory.
+constexpr int kRowsThreads = 256, kKeys = 64;
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+
+// ND: columns of the output in 32s.
+template <typename T, int ND>
+struct RowsShape {
+    static constexpr int kEach = ND <= 4 ? 8 : 4;  // rows a thread
+    static constexpr int kRows = 16 * kEach;
+    static constexpr int kStride = 32 * ND + 4;    // floats of a row: 16 bytes of skew
+    static constexpr int kBytes = 4 * (kRows * kStride + 2 * kKeys * kStride + kRows * (kKeys + 4));
+};
+
+template <typename T, int ND>
+__global__ void __launch_bounds__(kRowsThreads) attention_rows_kernel(PromptParams p) {
+    using S = RowsShape<T, ND>;
+    constexpr int E = S::kEach, R = S::kRows, LD = S::kStride, LP = kKeys + 4;
+    extern __shared__ __align__(16) float rows_smem[];
+    float *sq = rows_smem, *sk = sq + R * LD, *sv = sk + kKeys * LD, *sp = sv + kKeys * LD;
+    __shared__ int found[3];
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, D = p.D;
+    if (blockIdx.y == 0) write_prompt_statuses(p, blockIdx.x * kRowsThreads + tid, gridDim.x * kRowsThreads);
+    const int h = blockIdx.y;
+    for (int64_t item = blockIdx.x;; item += gridDim.x) {
+        // the request that holds row tile `item`; its last tiles, the longest, come first
+        if (tid < 32) {
+            int64_t before = 0;
+            int b = -1, tile = 0, tiles_of_b = 0;
+            for (int b0 = 0; b0 < p.B && b < 0; b0 += 32) {
+                const int mine = b0 + lane < p.B ? (int)(((int64_t)load_prompt(p, b0 + lane).n * p.group + R - 1) / R) : 0;
+                int64_t upto = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += x;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, before + upto > item);
+                if (past) {
+                    const int w = __ffs(past) - 1;
+                    b = b0 + w;
+                    tiles_of_b = __shfl_sync(0xffffffffu, mine, w);
+                    tile = (int)(item - before - (__shfl_sync(0xffffffffu, upto, w) - tiles_of_b));
+                }
+                before += __shfl_sync(0xffffffffu, upto, 31);
+            }
+            if (lane == 0) {
+                found[0] = b;
+                found[1] = tiles_of_b - 1 - tile;
+            }
+        }
+        __syncthreads();
+        const int b = found[0], tile = found[1];
+        if (b < 0) return;
+        const Prompt r = load_prompt(p, b);
+        const int first = tile * R, nrows = min(R, r.n * p.group - first);  // the host keeps n * group below 2^31
+        const int off = r.m - r.n;  // position of query 0
+        const int pos0 = off + first / p.group, pos1 = off + (first + nrows - 1) / p.group;
+        const Span span = span_of<kKeys>(p, pos0, pos1);
+        auto global_row = [&](int row) {  // of q and out, in elements without the row stride
+            const int f = first + row;
+            return make_int2(r.row0 + f / p.group, h * p.group + f % p.group);
+        };
+        for (int i = tid; i < R * (LD / 4); i += kRowsThreads) {
+            const int row = i / (LD / 4), c = (i - row * (LD / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < nrows && c < D) {
+                const int2 g = global_row(row);
+                const T *src = (const T *)p.q + g.x * p.ld_q + (int64_t)g.y * D + c;
+                x = make_float4(to_float(src[0]), to_float(src[1]), to_float(src[2]), to_float(src[3]));
+                x.x *= p.scale_log2, x.y *= p.scale_log2, x.z *= p.scale_log2, x.w *= p.scale_log2;
+            }
+            *(float4 *)(sq + row * LD + c) = x;
+        }
+        float m[E], l[E];
+        float2 o[E][ND];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            m[e] = kNegInf;
+            l[e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < ND; ++c) o[e][c] = make_float2(0.f, 0.f);
+        }
+        int pos[E];  // a thread's rows: ty + 16 e
+#pragma unroll
+        for (int e = 0; e < E; ++e) pos[e] = ty + 16 * e < nrows ? off + (first + ty + 16 * e) / p.group : -1;
+        for (int i = 0; i < span.count; ++i) {
+            const int j0 = span.tile(i) * kKeys;
+            const bool masked = j0 + kKeys - 1 > pos0 || (p.window > 0 && j0 <= pos1 - p.window && j0 + kKeys > p.sinks) || nrows < R;
+            int strange = 0;  // values that are not finite
+            for (int x = tid; x < kKeys * (LD / 4); x += kRowsThreads) {
+                const int row = x / (LD / 4), c = (x - row * (LD / 4)) * 4;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
+                if (j0 + row < r.m && c < D) {
+                    const T *ks = (const T *)p.k + (r.key0 + j0 + row) * p.ld_k + (int64_t)h * D + c;
+                    const T *vs = (const T *)p.v + (r.key0 + j0 + row) * p.ld_v + (int64_t)h * D + c;
+                    a = make_float4(to_float(ks[0]), to_float(ks[1]), to_float(ks[2]), to_float(ks[3]));
+                    d = make_float4(to_float(vs[0]), to_float(vs[1]), to_float(vs[2]), to_float(vs[3]));
+                    strange |= !isfinite(d.x) || !isfinite(d.y) || !isfinite(d.z) || !isfinite(d.w);
+                }
+                *(float4 *)(sk + row * LD + c) = a;
+                *(float4 *)(sv + row * LD + c) = d;
+            }
+            strange = __syncthreads_or(strange);
+            // scores: pairs of columns summed side by side
+            float2 s[E][4];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[e][k] = make_float2(0.f, 0.f);
+            for (int c = 0; c < D; c += 4) {
+                float4 a[E], d[4];
+#pragma unroll
+                for (int e = 0; e < E; ++e) a[e] = *(const float4 *)(sq + (ty + 16 * e) * LD + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d[k] = *(const float4 *)(sk + (tx + 16 * k) * LD + c);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        s[e][k] = ffma2(make_float2(a[e].x, a[e].y), make_float2(d[k].x, d[k].y), s[e][k]);
+                        s[e][k] = ffma2(make_float2(a[e].z, a[e].w), make_float2(d[k].z, d[k].w), s[e][k]);
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                float x[4], top = kNegInf;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    x[k] = s[e][k].x + s[e][k].y;
+                    if (masked && !visible(p, pos[e], j0 + tx + 16 * k)) x[k] = kNegInf;
+                    top = fmaxf(top, x[k]);
+                }
+#pragma unroll
+                for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const float now = fmaxf(m[e], top), ref = now == kNegInf ? 0.f : now;
+                const float alpha = ex2_approx(m[e] - ref);  // 0 from -inf
+                m[e] = now;
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float y = ex2_approx(x[k] - ref);
+                    sum += y;
+                    sp[(ty + 16 * e) * LP + tx + 16 * k] = y;
+                }
+                l[e] = l[e] * alpha + sum;
+#pragma unroll
+                for (int c = 0; c < ND; ++c) {
+                    o[e][c].x *= alpha;
+                    o[e][c].y *= alpha;
+                }
+            }
+            __syncwarp();  // a row's 16 threads are of one warp
+            if (masked && strange) {  // a value that a row does not see must not meet its zero
+                for (int k = 0; k < kKeys; ++k)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        if (!visible(p, pos[e], j0 + k)) continue;
+                        const float y = sp[(ty + 16 * e) * LP + k];
+#pragma unroll
+                        for (int c = 0; c < ND; ++c) {
+                            const float2 d = *(const float2 *)(sv + k * LD + tx * 2 + 32 * c);
+                            o[e][c] = ffma2(make_float2(y, y), d, o[e][c]);
+                        }
+                    }
+            } else {
+                for (int k = 0; k < kKeys; k += 4) {
+                    float4 y[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = *(const float4 *)(sp + (ty + 16 * e) * LP + k);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        float2 d[ND];
+#pragma unroll
+                        for (int c = 0; c < ND; ++c) d[c] = *(const float2 *)(sv + (k + kk) * LD + tx * 2 + 32 * c);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const float f = kk == 0 ? y[e].x : kk == 1 ? y[e].y : kk == 2 ? y[e].z : y[e].w;
+#pragma unroll
+                            for (int c = 0; c < ND; ++c) o[e][c] = ffma2(make_float2(f, f), d[c], o[e][c]);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float sum = l[e];
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            const int row = ty + 16 * e;
+            if (row >= nrows) continue;
+            const int2 g = global_row(row);
+            const float f = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: o is 0
+            T *dst = (T *)p.out + ((int64_t)g.x * p.Hq + g.y) * D;
+#pragma unroll
+            for (int c = 0; c < ND; ++c) {
+                const int col = tx * 2 + 32 * c;
+                if (col >= D) continue;
+                if (sizeof(T) == 2) *(uint32_t *)(dst + col) = pack_bf16x2(o[e][c].x * f, o[e][c].y * f);
+                else *(float2 *)(dst + col) = make_float2(o[e][c].x * f, o[e][c].y * f);
+            }
+            if (p.lse && tx == 0) p.lse[(int64_t)g.x * p.Hq + g.y] = sum == 0.f ? kNegInf : (m[e] + log2f(sum)) * 0.6931471805599453f;
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int ND>
+int launch_rows(const PromptParams &p, int dev, int sms, cudaStream_t st) {
+    using S = RowsShape<T, ND>;
+    static std::atomic<bool> set[64];
+    if (!set[dev].load()) {
+        const cudaError_t e = cudaFuncSetAttribute(attention_rows_kernel<T, ND>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+        if (e != cudaSuccess) {
+            note_cuda_error((int)e);
+            return SPEC_ECUDA;
+        }
+        set[dev].store(true);
+    }
+    // row tiles at most: every request's last one may be partial
+    const int64_t tiles = ((int64_t)p.n_q * p.group + S::kRows - 1) / S::kRows + p.B;
+    const dim3 grid((unsigned)(tiles < 1 << 20 ? tiles : 1 << 20), p.H);
+    attention_rows_kernel<T, ND><<<grid, kRowsThreads, S::kBytes, st>>>(p);
+    return launch_status();
+}
+
+template <typename T>
+int launch_rows_any(const PromptParams &p, int dev, int sms, cudaStream_t st) {
+    if (p.D <= 64) return launch_rows<T, 2>(p, dev, sms, st);
+    if (p.D <= 96) return launch_rows<T, 3>(p, dev, sms, st);
+    if (p.D <= 128) return launch_rows<T, 4>(p, dev, sms, st);
+    if (p.D <= 192) return launch_rows<T, 6>(p, dev, sms, st);
+    return launch_rows<T, 8>(p, dev, sms, st);
+}
+
+}  // namespace
+}  // namespace specv
+
+using namespace specv;
+
+extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v, int dtype, int64_t ld_q, int64_t ld_k,
+                                     int64_t ld_v, int num_query_heads, int num_heads, int head_dim, int n_query,
+                                     int n_key, int B, const int32_t *cu_query, int max_query, const int32_t *cu_key,
+                                     float scale, int window, int sinks, void *out, float *out_lse, int32_t *out_status,
+                                     void *cuda_stream) {
+    if (dtype != SPEC_BF16 && dtype != SPEC_F32) return SPEC_EINVAL;
+    if (B < 0 || n_query < 0 || n_key < 0 || max_query < 0 || num_query_heads <= 0 || num_heads <= 0 || head_dim <= 0 ||
+        window < 0 || sinks < 0 || num_query_heads % num_heads)
+        return SPEC_EINVAL;
+    if (!(scale > 0.f) || !(scale * kLog2e < __builtin_huge_valf())) return SPEC_EINVAL;
+    if ((head_dim & 15) || head_dim > SPEC_KV_MAX_HEAD_DIM || num_heads > 65535) return SPEC_EUNSUPPORTED;
+    if (B == 0) return SPEC_OK;
+    if (B > SPEC_MAX_BATCH) return SPEC_EUNSUPPORTED;
+    const int group = num_query_heads / num_heads;
+    if ((int64_t)max_query * group > 0x7fffffff - 256) return SPEC_EUNSUPPORTED;
+    if (!cu_query || !out_status || (!cu_key && n_key != n_query)) return SPEC_EINVAL;
+    const int esz = dtype == SPEC_BF16 ? 2 : 4;
+    const int64_t row = (int64_t)num_heads * head_dim;
+    if (n_query > 0 && (!q || !out || ld_q < row * group)) return SPEC_EINVAL;
+    if (n_key > 0 && (!k || !v || ld_k < row || ld_v < row)) return SPEC_EINVAL;
+    if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v) % esz || ((uintptr_t)out & 15) || ((uintptr_t)out_lse & 3)) return SPEC_EINVAL;
+    if (((uintptr_t)cu_query | (uintptr_t)cu_key | (uintptr_t)out_status) & 3) return SPEC_EINVAL;
+    int dev = 0, sms = 0, rc;
+    if ((rc = kv_device_info(&dev, &sms))) return rc;
+    if (n_query > 0 && (rc = kv_check_device_pointer(q, dev))) return rc;
+    PromptParams p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.out = out;
+    p.lse = out_lse;
+    p.cu_q = cu_query;
+    p.cu_k = cu_key ? cu_key : cu_query;
+    p.status = out_status;
+    p.ld_q = ld_q;
+    p.ld_k = ld_k;
+    p.ld_v = ld_v;
+    p.B = B;
+    p.n_q = n_query;
+    p.n_k = n_key;
+    p.max_query = max_query;
+    p.Hq = num_query_heads;
+    p.H = num_heads;
+    p.group = group;
+    p.D = head_dim;
+    p.window = window < (1 << 30) ? window : (1 << 30);  // positions stay below 2^31
+    p.sinks = window > 0 ? sinks : 0;
+    p.scale_log2 = scale * kLog2e;
+    const cudaStream_t st = (cudaStream_t)cuda_stream;
+    if (esz == 2) return launch_rows_any<uint16_t>(p, dev, sms, st);
+    return launch_rows_any<float>(p, dev, sms, st);
+}

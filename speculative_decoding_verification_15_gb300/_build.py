@@ -14,8 +14,8 @@ LIB_NAME = "libspecverify.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["verify.cu", "schedule.cu", "markov.cu", "kv_cache.cu", "cache_attention.cu", "page_plan.cu", "rotary.cu",
-           "prompt_attention.cu"]
-HEADERS = ["spec_common.cuh", "kv_common.cuh", "tcgen05.cuh"]
+           "prompt_attention.cu", "prompt_tc.cu"]
+HEADERS = ["spec_common.cuh", "kv_common.cuh", "prompt_common.cuh", "tcgen05.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

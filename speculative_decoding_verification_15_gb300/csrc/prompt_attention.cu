@@ -14,63 +14,10 @@
 // arithmetic throughout: attention_rows_kernel.
 #include <atomic>
 
-#include "kv_common.cuh"
+#include "prompt_common.cuh"
 
 namespace specv {
 namespace {
-
-struct PromptParams {
-    const void *q, *k, *v;
-    void *out;
-    float *lse;
-    const int32_t *cu_q, *cu_k;
-    int32_t *status;
-    int64_t ld_q, ld_k, ld_v;
-    int B, n_q, n_k, max_query, Hq, H, group, D, window, sinks;
-    float scale_log2;
-};
-
-struct Prompt {
-    int row0, n, key0, m;  // first query row, queries, first key row, keys; n = 0 where unusable
-    bool ok;
-};
-
-__device__ __forceinline__ Prompt load_prompt(const PromptParams &p, int b) {
-    Prompt r;
-    r.row0 = p.cu_q[b];
-    const int row1 = p.cu_q[b + 1];
-    r.key0 = p.cu_k[b];
-    const int key1 = p.cu_k[b + 1];
-    r.ok = r.row0 >= 0 && row1 >= r.row0 && row1 <= p.n_q && r.key0 >= 0 && key1 >= r.key0 && key1 <= p.n_k;
-    r.n = row1 - r.row0;
-    r.m = key1 - r.key0;
-    r.ok = r.ok && r.n <= p.max_query;
-    if (!r.ok) r.n = r.m = 0;
-    return r;
-}
-
-__device__ __forceinline__ void write_prompt_statuses(const PromptParams &p, int first, int step) {
-    for (int b = first; b < p.B; b += step) p.status[b] = load_prompt(p, b).ok ? SPEC_STATUS_OK : SPEC_STATUS_BAD_LENGTH;
-}
-
-// Key tiles of a row tile: [0, s1) hold first tokens kept visible, [w0, end) the rest.
-struct Span {
-    int s1, w0, count;
-    __device__ __forceinline__ int tile(int i) const { return i < s1 ? i : w0 + (i - s1); }
-};
-template <int TK>
-__device__ __forceinline__ Span span_of(const PromptParams &p, int pos0, int pos1) {
-    Span s = {0, 0, 0};
-    if (pos1 < 0) return s;
-    const int low = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;  // below it only sinks are seen
-    s.w0 = low / TK;
-    s.s1 = min((min(p.sinks, low) + TK - 1) / TK, s.w0);
-    s.count = s.s1 + pos1 / TK + 1 - s.w0;
-    return s;
-}
-__device__ __forceinline__ bool visible(const PromptParams &p, int pos, int j) {
-    return j <= pos && (p.window == 0 || j > pos - p.window || j < p.sinks);
-}
 
 // ------------------------------------------------------------------ fp32 arithmetic
 // A CTA takes an item of R rows (16 threads down, 16 across: R / 16 rows and 4 keys a thread)
@@ -335,7 +282,7 @@ extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v
     if (B == 0) return SPEC_OK;
     if (B > SPEC_MAX_BATCH) return SPEC_EUNSUPPORTED;
     const int group = num_query_heads / num_heads;
-    if ((int64_t)max_query * group > 0x7fffffff - 256) return SPEC_EUNSUPPORTED;
+    if ((int64_t)max_query * group > 0x7fffffff - 256 || n_key > 0x7fffffff - 1024) return SPEC_EUNSUPPORTED;
     if (!cu_query || !out_status || (!cu_key && n_key != n_query)) return SPEC_EINVAL;
     const int esz = dtype == SPEC_BF16 ? 2 : 4;
     const int64_t row = (int64_t)num_heads * head_dim;
@@ -370,6 +317,9 @@ extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v
     p.sinks = window > 0 ? sinks : 0;
     p.scale_log2 = scale * kLog2e;
     const cudaStream_t st = (cudaStream_t)cuda_stream;
-    if (esz == 2) return launch_rows_any<uint16_t>(p, dev, sms, st);
+    if (esz == 2) {
+        rc = launch_prompt_tc(p, dev, sms, st);
+        return rc == SPEC_EUNSUPPORTED ? launch_rows_any<uint16_t>(p, dev, sms, st) : rc;
+    }
     return launch_rows_any<float>(p, dev, sms, st);
 }

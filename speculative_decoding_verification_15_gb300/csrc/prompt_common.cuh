@@ -1,0 +1,65 @@
+// prompt_common.cuh -- what the prompt attention's kernels share (sm_103a): a request's
+// queries and keys, and which tiles of keys a row tile visits.
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace specv {
+
+struct PromptParams {
+    const void *q, *k, *v;
+    void *out;
+    float *lse;
+    const int32_t *cu_q, *cu_k;
+    int32_t *status;
+    int64_t ld_q, ld_k, ld_v;
+    int B, n_q, n_k, max_query, Hq, H, group, D, window, sinks;
+    float scale_log2;
+};
+
+struct Prompt {
+    int row0, n, key0, m;  // first query row, queries, first key row, keys; n = 0 where unusable
+    bool ok;
+};
+
+__device__ __forceinline__ Prompt load_prompt(const PromptParams &p, int b) {
+    Prompt r;
+    r.row0 = p.cu_q[b];
+    const int row1 = p.cu_q[b + 1];
+    r.key0 = p.cu_k[b];
+    const int key1 = p.cu_k[b + 1];
+    r.ok = r.row0 >= 0 && row1 >= r.row0 && row1 <= p.n_q && r.key0 >= 0 && key1 >= r.key0 && key1 <= p.n_k;
+    r.n = row1 - r.row0;
+    r.m = key1 - r.key0;
+    r.ok = r.ok && r.n <= p.max_query;
+    if (!r.ok) r.n = r.m = 0;
+    return r;
+}
+
+__device__ __forceinline__ void write_prompt_statuses(const PromptParams &p, int first, int step) {
+    for (int b = first; b < p.B; b += step) p.status[b] = load_prompt(p, b).ok ? SPEC_STATUS_OK : SPEC_STATUS_BAD_LENGTH;
+}
+
+// Key tiles of a row tile: [0, s1) hold first tokens kept visible, [w0, end) the rest.
+struct Span {
+    int s1, w0, count;
+    __device__ __forceinline__ int tile(int i) const { return i < s1 ? i : w0 + (i - s1); }
+};
+template <int TK>
+__device__ __forceinline__ Span span_of(const PromptParams &p, int pos0, int pos1) {
+    Span s = {0, 0, 0};
+    if (pos1 < 0) return s;
+    const int low = p.window > 0 ? max(0, max(0, pos0) - p.window + 1) : 0;  // below it only sinks are seen
+    s.w0 = low / TK;
+    s.s1 = min((min(p.sinks, low) + TK - 1) / TK, s.w0);
+    s.count = s.s1 + pos1 / TK + 1 - s.w0;
+    return s;
+}
+__device__ __forceinline__ bool visible(const PromptParams &p, int pos, int j) {
+    return j <= pos && (p.window == 0 || j > pos - p.window || j < p.sinks);
+}
+
+// The tensor-core kernel (prompt_tc.cu); SPEC_EUNSUPPORTED where it cannot serve the call.
+int launch_prompt_tc(const PromptParams &p, int dev, int sms, cudaStream_t st);
+
+}  // namespace specv

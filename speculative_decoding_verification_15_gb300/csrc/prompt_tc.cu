@@ -1,0 +1,683 @@
+// prompt_tc.cu -- prompt attention on the tensor cores (bf16, heads of up to 128 columns).
+//
+// An item is a key head's two row tiles of up to 128 rows (queries of consecutive tokens,
+// the group's heads of each) and the tiles of 128 keys that one of them sees.  For each key
+// tile and row tile
+//   S = Q K^T     operands in shared memory, fp32 in tensor memory,
+//   P = 2^(S - m) rounded to bf16, by 128 threads, a row each, back into S's columns,
+//   O += P V      P from tensor memory, V from shared memory, fp32 in tensor memory.
+// The two row tiles take turns: while one's exponentials are computed the tensor cores work
+// for the other.  The reference m of a row moves only when a score exceeds it by more than
+// 2^8 (its weights then stay below 2^8 and keep their relative precision, sums included), so
+// O is rarely rescaled.
+//
+// P's rounding to bf16 (2^-8 of each weight at most) is of the size of the output's own; it
+// lets both products run at the bf16 rate.  Everything else is fp32.
+//
+// Roles: 8 warps of softmax (4 a row tile), one that issues products, one that copies
+// (tensor maps: queries {D, group, heads, tokens}, keys and values {D, heads, tokens}, in
+// panels of 64 columns, zeros past D), one that finds the items.
+//
+// Order.  CTAs stay, and items go to them longest first, forth and back (CTA c takes numbers
+// c, 2 n - 1 - c, 2 n + c, ..): costs fall along the order, so the sums are nearly equal
+// without a counter.
+//
+// What a row does not see has weight 0, but 0 times a NaN or an infinity is NaN: a row whose
+// output is not finite is computed again over its visible keys alone.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "prompt_common.cuh"
+#include "tcgen05.cuh"
+
+namespace specv {
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kKeys = 128, kRows = 128, kPanel = 128 * 128;  // bytes of 64 columns of 128 rows
+constexpr int kThreads = 384, kSoftWarps = 8;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kFindWarp = 10;
+constexpr int kItems = 3;         // places for items that have been told and are not done with
+constexpr int kSortedBatch = 128; // requests whose items are put in order of length
+constexpr float kRefStep = 8.f;   // log2: how far a score may exceed the reference
+
+// Polls: these waits are on the path of every tile.  A wait that ran out anywhere ends the others.
+__device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+__device__ __noinline__ bool poll_barrier(uint32_t bar, uint32_t parity, volatile int *failed) {
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        if (try_barrier(bar, parity)) return true;
+        if ((n & 255) == 0) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (*failed || now - t0 > kWaitNs) {
+                *failed = 1;
+                return false;
+            }
+        }
+    }
+}
+
+struct Item {
+    int b;              // -1: no more
+    int row0, n, key0, off, tok0, h;  // off: position of query 0; tok0: first token of the first row tile
+};
+
+// Key tiles of an item, as indexes into a list: tiles [0, s1) and [w0, ...).  A row tile's
+// own are indexes [0, its s1) and [w, e).
+struct Tiles {
+    int s1, w0, count;
+    struct Sub {
+        int s1, w, e, pos0;  // pos0: position of its first row
+        __device__ __forceinline__ bool active(int i) const { return i < s1 || (i >= w && i < e); }
+        __device__ __forceinline__ int count() const { return s1 + e - w; }
+    } sub[2];
+    __device__ __forceinline__ int tile(int i) const { return i < s1 ? i : w0 + (i - s1); }
+};
+
+__device__ __forceinline__ Tiles tiles_of(const PromptParams &p, const Item &x, int tokens, int subs) {
+    Tiles t;
+    Span s[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const int first = x.tok0 + a * tokens, end = min(x.n, first + tokens);
+        t.sub[a].pos0 = x.off + first;
+        s[a] = a < subs && first < end ? span_of<kKeys>(p, x.off + first, x.off + end - 1) : Span{0, 0, 0};
+    }
+    const bool one = s[0].count > 0, two = s[1].count > 0;
+    t.w0 = one ? (two ? min(s[0].w0, s[1].w0) : s[0].w0) : s[1].w0;
+    t.s1 = min(max(s[0].s1, s[1].s1), t.w0);
+    t.count = 0;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        t.sub[a].s1 = s[a].s1;
+        t.sub[a].w = s[a].count > 0 ? t.s1 + s[a].w0 - t.w0 : 0;
+        t.sub[a].e = t.sub[a].w + s[a].count - s[a].s1;
+        t.count = max(t.count, t.sub[a].e);
+    }
+    return t;
+}
+
+// ------------------------------------------------------------------ the order of the items
+// One warp.  A pair is an item without its head: (request, pair t of its row tiles), its
+// length the position behind its last query, in tiles.  Up to kSortedBatch requests: longest
+// first, found by bisection over the lengths with counts in closed form.  More requests:
+// request after request, each one's last pairs first.
+struct Finder {
+    int tokens;            // of a pair
+    int n[kSortedBatch / 32], off[kSortedBatch / 32];  // a lane's requests
+    int64_t before;        // pairs of the requests below b0 (many requests)
+    int64_t total;         // pairs in all
+    int b0, top;           // top: the longest pair's length
+    bool sorted;
+
+    __device__ __forceinline__ static int pairs_of(int n, int tokens) { return (n + tokens - 1) / tokens; }
+    // The first pair of a request that is at least `level` tiles long (>= 1).
+    __device__ __forceinline__ int first_at(int n, int off, int level) const {
+        if (n <= 0) return 0;
+        const int64_t x = (int64_t)(level - 1) * kKeys + 1 - off;  // tokens it takes
+        if (level <= 1) return 0;
+        if (x > n) return pairs_of(n, tokens);
+        if (x <= tokens) return 0;
+        return (int)((x + tokens - 1) / tokens) - 1;
+    }
+    __device__ __forceinline__ int64_t at_least(int level) const {
+        int64_t c = 0;
+#pragma unroll
+        for (int k = 0; k < kSortedBatch / 32; ++k)
+            if (k == 0 || n[k] > 0) c += pairs_of(n[k], tokens) - first_at(n[k], off[k], level);
+        // 2^31 pairs at most for each request; counts of a warp in 64 bits
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+        return c;
+    }
+    __device__ __forceinline__ void start(const PromptParams &p, int pair_tokens, int lane) {
+        tokens = pair_tokens;
+        sorted = p.B <= kSortedBatch;
+        b0 = 0;
+        before = total = 0;
+        int longest = 0;
+        if (sorted) {
+#pragma unroll
+            for (int k = 0; k < kSortedBatch / 32; ++k) {
+                n[k] = off[k] = 0;
+                const int b = k * 32 + lane;
+                if (b < p.B) {
+                    const Prompt r = load_prompt(p, b);
+                    n[k] = r.n;
+                    off[k] = r.m - r.n;
+                    if (r.n > 0) longest = max(longest, (r.m + kKeys - 1) / kKeys);
+                }
+                total += pairs_of(n[k], tokens);
+            }
+        } else {
+            for (int b = lane; b < p.B; b += 32) total += pairs_of(load_prompt(p, b).n, tokens);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        top = max(1, __reduce_max_sync(0xffffffffu, longest));
+    }
+    // Pair number r of the order (r < total, rising from call to call).
+    __device__ __noinline__ Item find(const PromptParams &p, int64_t r, int lane) {
+        Item x;
+        if (sorted) {
+            int lo = 1, hi = top + 1;  // at_least(lo) > r >= at_least(hi)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (at_least(mid) > r) lo = mid;
+                else hi = mid;
+            }
+            int64_t rest = r - at_least(lo + 1);
+            x.b = -1;
+            for (int k = 0; k < kSortedBatch / 32 && x.b < 0; ++k) {
+                int mine = 0, t0 = 0, nk = 0, ok = 0;
+#pragma unroll
+                for (int i = 0; i < kSortedBatch / 32; ++i)
+                    if (i == k) nk = n[i], ok = off[i];
+                t0 = first_at(nk, ok, lo);
+                mine = first_at(nk, ok, lo + 1) - t0;
+                if (nk <= 0) mine = 0;
+                int64_t upto = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, upto > rest);
+                if (past) {
+                    const int w = __ffs(past) - 1;
+                    x.b = k * 32 + w;
+                    const int64_t start = __shfl_sync(0xffffffffu, upto - mine, w);
+                    x.tok0 = (__shfl_sync(0xffffffffu, t0, w) + (int)(rest - start)) * tokens;
+                } else {
+                    rest -= __shfl_sync(0xffffffffu, upto, 31);
+                }
+            }
+        } else {
+            for (;;) {
+                const int mine = b0 + lane < p.B ? pairs_of(load_prompt(p, b0 + lane).n, tokens) : 0;
+                int64_t upto = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, before + upto > r);
+                if (past || b0 >= p.B) {
+                    const int w = past ? __ffs(past) - 1 : 0;
+                    x.b = past ? b0 + w : -1;
+                    const int64_t start = __shfl_sync(0xffffffffu, upto - mine, w);
+                    x.tok0 = (__shfl_sync(0xffffffffu, mine, w) - 1 - (int)(r - before - start)) * tokens;
+                    break;
+                }
+                before += __shfl_sync(0xffffffffu, upto, 31);
+                b0 += 32;
+            }
+        }
+        if (x.b >= 0) {
+            const Prompt q = load_prompt(p, x.b);
+            x.row0 = q.row0;
+            x.n = q.n;
+            x.key0 = q.key0;
+            x.off = q.m - q.n;
+        }
+        return x;
+    }
+};
+
+// ------------------------------------------------------------------ shared memory
+template <int NP>
+struct PromptShared {
+    static constexpr int kStages = NP == 1 ? 10 : 5;
+    uint8_t q[2][NP * kPanel];
+    uint8_t ring[kStages][NP * kPanel];
+    uint64_t full[kStages], empty[kStages], q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+    uint64_t item_full[kItems], item_empty[kItems];
+    Item items[kItems];
+    uint32_t tmem;
+    int failed;
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A row's output again, over its visible keys alone (one warp; m and l are right as they
+// are: masked scores never enter them).  Stops once every column is NaN.
+__device__ __noinline__ void repair_row(const PromptParams &p, const Item &x, int token, int head, float m, float l, int lane) {
+    constexpr int kMost = SPEC_KV_MAX_HEAD_DIM / 32;
+    const uint16_t *q = (const uint16_t *)p.q + (int64_t)(x.row0 + token) * p.ld_q + (int64_t)head * p.D;
+    float a[kMost], o[kMost];
+#pragma unroll
+    for (int c = 0; c < kMost; ++c) {
+        a[c] = c * 32 + lane < p.D ? ld_elem<2>(q, c * 32 + lane) : 0.f;
+        o[c] = 0.f;
+    }
+    const int pos = x.off + token;
+    const float ref = m == kNegInf ? 0.f : m, inv = l == 0.f ? 0.f : 1.f / l;
+    for (int j = 0; j <= pos; ++j) {
+        if (!visible(p, pos, j)) {
+            j = max(j, pos - p.window);  // on to the window
+            continue;
+        }
+        const int64_t row = (int64_t)(x.key0 + j);
+        const uint16_t *k = (const uint16_t *)p.k + row * p.ld_k + (int64_t)x.h * p.D;
+        const uint16_t *v = (const uint16_t *)p.v + row * p.ld_v + (int64_t)x.h * p.D;
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMost; ++c)
+            if (c * 32 + lane < p.D) s += a[c] * ld_elem<2>(k, c * 32 + lane);
+        s = warp_sum(s);
+        const float w = ex2_approx(fmaf(s, p.scale_log2, -ref)) * inv;
+        bool finite = false;
+#pragma unroll
+        for (int c = 0; c < kMost; ++c)
+            if (c * 32 + lane < p.D) {
+                o[c] = fmaf(w, ld_elem<2>(v, c * 32 + lane), o[c]);
+                finite |= !isnan(o[c]);
+            }
+        if (!__any_sync(0xffffffffu, finite)) break;
+    }
+    uint16_t *dst = (uint16_t *)p.out + ((int64_t)(x.row0 + token) * p.Hq + head) * p.D;
+#pragma unroll
+    for (int c = 0; c < kMost; ++c)
+        if (c * 32 + lane < p.D) dst[c * 32 + lane] = (uint16_t)pack_bf16x2(o[c], 0.f);
+}
+
+template <int NP>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_tc_kernel(const PromptParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, int tokens, int subs) {
+    using SM = PromptShared<NP>;
+    constexpr int NS = SM::kStages;
+    constexpr uint32_t kTileBytes = NP * kPanel;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    SM &sm = *reinterpret_cast<SM *>(raw);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_empty, 1);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&sm.s_full[a], 1);
+            mbar_init(&sm.p_full[a], 4);
+            mbar_init(&sm.o_full[a], 1);
+        }
+        mbar_init(&sm.drain, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sm.item_full[i], 1);
+            mbar_init(&sm.item_empty[i], 2 + kSoftWarps);
+        }
+        sm.failed = 0;
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before();
+    // statuses: a CTA that fails corrects them seconds later, when all have written theirs
+    write_prompt_statuses(p, blockIdx.x * kThreads + tid, gridDim.x * kThreads);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sm.tmem;  // S of the two row tiles at 0 and 128, O at 256 and 384
+    bool dead = false;            // a wait ran out: end
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!dead && !try_barrier(smem_addr(bar), parity)) dead = !poll_barrier(smem_addr(bar), parity, &sm.failed);
+        dead = __any_sync(0xffffffffu, dead);
+    };
+    int told = 0;  // items taken
+    auto take = [&](Item &x) {
+        const int at = told % kItems;
+        wait(&sm.item_full[at], (told / kItems) & 1);
+        x = sm.items[at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_empty[at]);
+        ++told;
+        return !dead && x.b >= 0;
+    };
+
+    if (warp == kFindWarp) {
+        // ---------------------------------------------------------------- items
+        Finder f;
+        f.start(p, tokens * subs, lane);
+        const int64_t total = f.total * p.H;
+        for (int64_t round = 0;; ++round) {
+            const int64_t i = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            const bool last = round * gridDim.x >= total;
+            if (i >= total && !last) continue;
+            Item x;
+            x.b = -1;
+            if (!last) {
+                x = f.find(p, i / p.H, lane);
+                x.h = (int)(i % p.H);
+            }
+            const int at = told % kItems;
+            if (told >= kItems) wait(&sm.item_empty[at], (told / kItems - 1) & 1);
+            if (dead) break;
+            if (lane == 0) {
+                sm.items[at] = x;
+                mbar_arrive(&sm.item_full[at]);
+            }
+            ++told;
+            if (last) break;
+        }
+    } else if (warp == kCopyWarp) {
+        // ---------------------------------------------------------------- copies
+        int sent = 0, nq = 0;
+        Item x;
+        while (take(x)) {
+            const Tiles t = tiles_of(p, x, tokens, subs);
+            if (t.count == 0) continue;
+            if (nq > 0) wait(&sm.q_empty, (nq - 1) & 1);
+            if (dead) break;
+            if (elect_one()) {
+                const uint32_t bytes = (uint32_t)tokens * p.group * 128 * NP;
+                mbar_arrive_expect_tx(&sm.q_full, (t.sub[0].count() > 0 ? bytes : 0) + (t.sub[1].count() > 0 ? bytes : 0));
+                for (int a = 0; a < 2; ++a)
+                    if (t.sub[a].count() > 0)
+                        for (int c = 0; c < NP; ++c)
+                            tma_load_4d(sm.q[a] + c * kPanel, &qmap, 64 * c, 0, x.h, x.row0 + x.tok0 + a * tokens, &sm.q_full);
+            }
+            __syncwarp();
+            ++nq;
+            for (int i = 0; i < t.count && !dead; ++i) {
+                const int key = x.key0 + t.tile(i) * kKeys;
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int slot = sent % NS;
+                    if (sent >= NS) wait(&sm.empty[slot], (sent / NS - 1) & 1);
+                    if (dead) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&sm.full[slot], kTileBytes);
+                        for (int c = 0; c < NP; ++c)
+                            tma_load_3d(sm.ring[slot] + c * kPanel, kv ? &vmap : &kmap, 64 * c, x.h, key, &sm.full[slot]);
+                    }
+                    __syncwarp();
+                    ++sent;
+                }
+            }
+        }
+        // none of the copies may be in flight when the CTA ends
+        for (int i = max(0, sent - NS); i < sent; ++i) mbar_wait(&sm.full[i % NS], (i / NS) & 1, kWaitNs);
+        if (nq > 0) mbar_wait(&sm.q_full, (nq - 1) & 1, kWaitNs);
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- products
+        const uint32_t idesc_s = bf16_idesc(kKeys, false), idesc_o = bf16_idesc(p.D, true);
+        const uint64_t dq = smem_desc(smem_addr(sm.q), 16, 1024, 2), dk = smem_desc(smem_addr(sm.ring), 16, 1024, 2);
+        const uint64_t dv = smem_desc(smem_addr(sm.ring), kPanel, 1024, 2);
+        const int steps = p.D / 16;
+        int got = 0, nq = 0, np[2] = {0, 0};  // ring slots, query tiles, tiles of weights used
+        Item x;
+        while (take(x)) {
+            const Tiles t = tiles_of(p, x, tokens, subs);
+            if (t.count == 0) continue;
+            int done[2] = {0, 0};
+            wait(&sm.q_full, nq & 1);
+            ++nq;
+            for (int i = -1; i < t.count && !dead; ++i) {
+                // the ring holds K0 V0 K1 V1 ..: tile i's values, then tile i + 1's keys
+                const int sv = got + 2 * i + 1, sk = got + 2 * i + 2;
+                if (i >= 0) wait(&sm.full[sv % NS], (sv / NS) & 1);
+                tc_fence_after();
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const uint32_t tS = tm + a * 128, tO = tm + 256 + a * 128;
+                    if (i >= 0 && t.sub[a].active(i)) {
+                        wait(&sm.p_full[a], np[a] & 1);
+                        if (dead) break;
+                        ++np[a];
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t v = dv + (uint64_t)((sv % NS) * (kTileBytes >> 4));
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k) mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
+                        }
+                        __syncwarp();
+                        if (++done[a] == t.sub[a].count() && elect_one()) mma_commit(&sm.o_full[a]);
+                        __syncwarp();
+                    }
+                    if (i + 1 < t.count && t.sub[a].active(i + 1)) {
+                        wait(&sm.full[sk % NS], (sk / NS) & 1);
+                        if (dead) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t q = dq + (uint64_t)(a * (kTileBytes >> 4)), k = dk + (uint64_t)((sk % NS) * (kTileBytes >> 4));
+#pragma unroll
+                            for (int s = 0; s < NP * 4; ++s)
+                                if (s < steps) {
+                                    const uint64_t at = (s >> 2) * (kPanel >> 4) + (s & 3) * 2;
+                                    mma_bf16(tS, q + at, k + at, idesc_s, s > 0);
+                                }
+                            mma_commit(&sm.s_full[a]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (dead) break;
+                if (elect_one()) {
+                    if (i >= 0) mma_commit(&sm.empty[sv % NS]);
+                    if (i + 1 < t.count) mma_commit(&sm.empty[sk % NS]);
+                    if (i + 2 == t.count) mma_commit(&sm.q_empty);
+                }
+                __syncwarp();
+            }
+            got += 2 * t.count;
+        }
+        // no product may be under way when the tensor memory is freed
+        if (elect_one()) mma_commit(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0, kWaitNs);
+    } else if (warp < kSoftWarps) {
+        // ---------------------------------------------------------------- softmax
+        const int a = warp >> 2, w4 = warp & 3, r = w4 * 32 + lane;
+        const uint32_t lanes = (uint32_t)(w4 * 32) << 16, tS = tm + a * 128 + lanes, tO = tm + 256 + a * 128 + lanes;
+        const float scale = p.scale_log2;
+        const float2 scale2 = make_float2(scale, scale);
+        const int tok_r = r / p.group, head_r = r - tok_r * p.group;
+        const bool wide = ((uintptr_t)p.out & 31) == 0;
+        int ns = 0, no = 0;  // tiles of scores, outputs taken
+        Item x;
+        while (take(x)) {
+            const Tiles t = tiles_of(p, x, tokens, subs);
+            const int first = x.tok0 + a * tokens, have = min(tokens, x.n - first);
+            if (a >= subs || have <= 0) continue;
+            const auto sub = t.sub[a];
+            const int todo = sub.count(), token = first + tok_r;
+            const bool mine = tok_r < have;  // also false for rows past the last whole token
+            const int pos = mine ? x.off + token : -1;
+            // positions of the warp's first and last row that counts
+            const int wp0 = x.off + first + (w4 * 32) / p.group, wp1 = x.off + first + min(have - 1, (w4 * 32 + 31) / p.group);
+            float m = kNegInf, ref = 0.f;  // the reference (log2) and what is subtracted
+            float2 l = make_float2(0.f, 0.f);
+            int done = 0;
+            for (int i = 0; done < todo && !dead; ++i) {
+                if (!sub.active(i)) continue;
+                const int j0 = t.tile(i) * kKeys;
+                wait(&sm.s_full[a], ns & 1);
+                ++ns;
+                if (dead) break;
+                tc_fence_after();
+                uint32_t s[kKeys];
+                tmem_ld<kKeys>(tS, s);
+                tmem_wait_ld();
+                if (j0 + kKeys - 1 > wp0 || (p.window > 0 && j0 <= wp1 - p.window && j0 + kKeys > p.sinks)) {
+                    const int hi = pos - j0, lo = p.window > 0 && pos >= 0 ? pos - p.window - j0 : -1, sinks = p.sinks - j0;
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (c > hi || (c <= lo && c >= sinks)) s[c] = 0xff800000u;
+                }
+                float top = kNegInf;
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 2) top = max3(top, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                top *= scale;
+                const bool moves = top > m + kRefStep;  // also from -inf
+                if (__any_sync(0xffffffffu, moves)) {
+                    const float alpha = moves && m > kNegInf ? ex2_approx(m - top) : 1.f;
+                    if (moves) m = ref = top;
+                    l.x *= alpha;
+                    l.y *= alpha;
+                    if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        for (int c = 0; c < p.D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st16(tO + c, o);
+                        }
+                    }
+                }
+                const float2 nref = make_float2(-ref, -ref);
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 y = ffma2(make_float2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), scale2, nref);
+                        y.x = ex2_approx(y.x);
+                        y.y = ex2_approx(y.y);
+                        l = fadd2(l, y);
+                        w[e / 2] = pack_bf16x2(y.x, y.y);
+                    }
+                    tmem_st16(tS + c / 2, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[a]);
+                ++done;
+            }
+            if (todo > 0) {
+                wait(&sm.o_full[a], no & 1);
+                ++no;
+                tc_fence_after();
+            }
+            if (dead) break;
+            const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t row = (int64_t)(x.row0 + token) * p.Hq + x.h * p.group + head_r;
+            uint16_t *dst = (uint16_t *)p.out + row * p.D;
+            bool odd = false;
+            for (int c = 0; c < p.D; c += 16) {
+                uint32_t o[16], w[8];
+                if (todo > 0) {
+                    tmem_ld16(tO + c, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float f = todo > 0 ? __uint_as_float(o[e]) * inv : 0.f, g = todo > 0 ? __uint_as_float(o[e + 1]) * inv : 0.f;
+                    odd |= !isfinite(f) || !isfinite(g);
+                    w[e / 2] = pack_bf16x2(f, g);
+                }
+                if (mine) {
+                    if (wide) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c), "r"(w[0]), "r"(w[1]),
+                                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                     : "memory");
+                    } else {
+                        *(uint4 *)(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *(uint4 *)(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+            }
+            if (mine && p.lse) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
+            tc_fence_before();
+            uint32_t again = __ballot_sync(0xffffffffu, odd && mine && todo > 0);
+            while (again) {
+                const int w = __ffs(again) - 1;
+                again &= again - 1;
+                __syncwarp();
+                repair_row(p, x, __shfl_sync(0xffffffffu, token, w), x.h * p.group + __shfl_sync(0xffffffffu, head_r, w),
+                           __shfl_sync(0xffffffffu, m, w), __shfl_sync(0xffffffffu, sum, w), lane);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_free(tm, 512);
+    if (sm.failed)
+        for (int b = tid; b < p.B; b += kThreads) p.status[b] = SPEC_STATUS_INTERNAL;
+}
+
+// ------------------------------------------------------------------ host
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 got = fn.load();
+    if (!got) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn.store(got = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f));
+        cudaGetLastError();
+    }
+    return got;
+}
+
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NP>
+int launch(const PromptParams &p, const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, int tokens, int subs,
+           int ctas, int dev, cudaStream_t st) {
+    constexpr int bytes = (int)sizeof(PromptShared<NP>);
+    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+    static std::atomic<bool> set[64];
+    if (!set[dev].load()) {
+        const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) {
+            note_cuda_error((int)e);
+            return SPEC_ECUDA;
+        }
+        set[dev].store(true);
+    }
+    prompt_tc_kernel<NP><<<ctas, kThreads, bytes, st>>>(p, qmap, kmap, vmap, tokens, subs);
+    return launch_status();
+}
+
+}  // namespace
+
+int launch_prompt_tc(const PromptParams &p, int dev, int sms, cudaStream_t st) {
+    if (p.D > 128 || p.group > kRows || p.n_q == 0 || p.n_k == 0) return SPEC_EUNSUPPORTED;
+    const int tokens = kRows / p.group;
+    const cuuint64_t head = (cuuint64_t)p.D * 2;
+    alignas(64) CUtensorMap qmap, kmap, vmap;
+    {
+        const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.group, (cuuint64_t)p.H, (cuuint64_t)p.n_q};
+        const cuuint64_t strides[3] = {head, head * p.group, (cuuint64_t)p.ld_q * 2};
+        const cuuint32_t box[4] = {64, (cuuint32_t)p.group, 1, (cuuint32_t)tokens};
+        if (!encode(&qmap, p.q, 4, dims, strides, box)) return SPEC_EUNSUPPORTED;
+    }
+    for (int v = 0; v < 2; ++v) {
+        const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.n_k};
+        const cuuint64_t strides[2] = {head, (cuuint64_t)(v ? p.ld_v : p.ld_k) * 2};
+        const cuuint32_t box[3] = {64, 1, kKeys};
+        if (!encode(v ? &vmap : &kmap, v ? p.v : p.k, 3, dims, strides, box)) return SPEC_EUNSUPPORTED;
+    }
+    // pairs of row tiles, at most; where they are too few for the SMs, single row tiles
+    const int64_t pairs = (((int64_t)p.n_q + 2 * tokens - 1) / (2 * tokens) + p.B) * p.H;
+    const int subs = pairs < sms ? 1 : 2;
+    const int64_t items = (((int64_t)p.n_q + subs * tokens - 1) / (subs * tokens) + p.B) * p.H;
+    const int ctas = (int)(items < sms ? items : sms);
+    if (p.D <= 64) return launch<1>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
+    return launch<2>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
+}
+
+}  // namespace specv

@@ -8,6 +8,9 @@
 //    apart; a 32-element step along K is 32 bytes further into the swizzled row;
 //  - rows are K and the 128 bytes run along M ("M-major", the transposed operand): 8-row
 //    groups 1024 bytes apart; a step of 32 along K is 4096 bytes further.
+// With 16-bit elements a tile row holds 64: a step of 16 along K is 32 bytes in the first
+// layout and 2048 in the second (B along N; more than 64 columns are panels of 64, their
+// distance the leading offset).
 // And one without swizzle for N-major B: blocks of 16 columns, in each the K rows 16
 // bytes apart, so 8-row groups 128 bytes apart and blocks 16 * rows bytes apart.
 #pragma once
@@ -52,6 +55,16 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// The same the other way.
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ------------------------------------------------------------------ descriptors
 // Shared-memory operand: address, leading and stride byte offsets (16-byte units),
 // version 1, swizzle mode (0 none, 2 128 bytes).
@@ -63,6 +76,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
 __host__ __device__ constexpr uint32_t fp8_idesc(int n, bool a_transposed, bool b_transposed) {
     return (1u << 4) | ((a_transposed ? 1u : 0u) << 15) | ((b_transposed ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            (8u << 24);
+}
+
+// bf16 x bf16 into fp32, M = 128.
+__host__ __device__ constexpr uint32_t bf16_idesc(int n, bool b_transposed) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_transposed ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
 // True in one lane of a converged warp.  The instructions that one thread issues for the
@@ -83,6 +101,19 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+// A in tensor memory: two elements a column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
 // The barrier completes a phase's arrival when every product issued so far is done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -90,6 +121,13 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 }
 
 // ------------------------------------------------------------------ tiled copies
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x0, int x1, int x2, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x0), "r"(x1), "r"(x2), "r"(smem_addr(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x0, int x1, int x2, int x3,
                                             uint64_t *bar) {
     asm volatile(

@@ -52,7 +52,7 @@ __device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
                  : "memory");
     return done != 0;
 }
-__device__ __noinline__ bool poll_barrier(uint32_t bar, uint32_t parity, volatile int *failed) {
+__device__ __forceinline__ bool poll_barrier(uint32_t bar, uint32_t parity, volatile int *failed) {
     uint64_t t0 = 0;
     for (uint32_t n = 1;; ++n) {
         if (try_barrier(bar, parity)) return true;
@@ -67,21 +67,22 @@ __device__ __noinline__ bool poll_barrier(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-struct Item {
-    int b;              // -1: no more
-    int row0, n, key0, off, tok0, h;  // off: position of query 0; tok0: first token of the first row tile
-};
-
 // Key tiles of an item, as indexes into a list: tiles [0, s1) and [w0, ...).  A row tile's
 // own are indexes [0, its s1) and [w, e).
 struct Tiles {
     int s1, w0, count;
     struct Sub {
-        int s1, w, e, pos0;  // pos0: position of its first row
+        int s1, w, e;
         __device__ __forceinline__ bool active(int i) const { return i < s1 || (i >= w && i < e); }
         __device__ __forceinline__ int count() const { return s1 + e - w; }
     } sub[2];
     __device__ __forceinline__ int tile(int i) const { return i < s1 ? i : w0 + (i - s1); }
+};
+
+struct Item {
+    int b;                            // -1: no more
+    int row0, n, key0, off, tok0, h;  // off: position of query 0; tok0: first token of the first row tile
+    Tiles t;
 };
 
 __device__ __forceinline__ Tiles tiles_of(const PromptParams &p, const Item &x, int tokens, int subs) {
@@ -90,7 +91,6 @@ __device__ __forceinline__ Tiles tiles_of(const PromptParams &p, const Item &x, 
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
         const int first = x.tok0 + a * tokens, end = min(x.n, first + tokens);
-        t.sub[a].pos0 = x.off + first;
         s[a] = a < subs && first < end ? span_of<kKeys>(p, x.off + first, x.off + end - 1) : Span{0, 0, 0};
     }
     const bool one = s[0].count > 0, two = s[1].count > 0;
@@ -109,128 +109,138 @@ __device__ __forceinline__ Tiles tiles_of(const PromptParams &p, const Item &x, 
 
 // ------------------------------------------------------------------ the order of the items
 // One warp.  A pair is an item without its head: (request, pair t of its row tiles), its
-// length the position behind its last query, in tiles.  Up to kSortedBatch requests: longest
-// first, found by bisection over the lengths with counts in closed form.  More requests:
-// request after request, each one's last pairs first.
+// level the tiles up to its last query.  Up to kSortedBatch requests: highest level first,
+// with counts in closed form; numbers are asked for in rising order, so the level falls by a
+// few steps at a time (and by bisection where it has far to go).  More requests: request
+// after request, each one's last pairs first.
 struct Finder {
-    int tokens;            // of a pair
-    int n[kSortedBatch / 32], off[kSortedBatch / 32];  // a lane's requests
-    int64_t before;        // pairs of the requests below b0 (many requests)
-    int64_t total;         // pairs in all
-    int b0, top;           // top: the longest pair's length
+    static constexpr int kEach = kSortedBatch / 32;
+    uint32_t tokens;               // of a pair
+    int n[kEach], off[kEach];      // a lane's requests
+    int row0[kEach], key0[kEach];
+    int before, upto;              // sorted: pairs above the current level, and down to it
+    int64_t passed;                // not sorted: pairs of the requests below b0
+    int64_t total;                 // pairs in all
+    int each, b0, level;           // each: requests a lane really has, at most
     bool sorted;
 
-    __device__ __forceinline__ static int pairs_of(int n, int tokens) { return (n + tokens - 1) / tokens; }
+    __device__ __forceinline__ int pairs_of(int n) const { return (int)(((uint32_t)n + tokens - 1) / tokens); }
     // The first pair of a request that is at least `level` tiles long (>= 1).
     __device__ __forceinline__ int first_at(int n, int off, int level) const {
-        if (n <= 0) return 0;
-        const int64_t x = (int64_t)(level - 1) * kKeys + 1 - off;  // tokens it takes
         if (level <= 1) return 0;
-        if (x > n) return pairs_of(n, tokens);
+        const int64_t x = (int64_t)(level - 1) * kKeys + 1 - off;  // tokens it takes
+        if (x > n) return pairs_of(n);
         if (x <= tokens) return 0;
-        return (int)((x + tokens - 1) / tokens) - 1;
+        return (int)(((uint32_t)x + tokens - 1) / tokens) - 1;
     }
-    __device__ __forceinline__ int64_t at_least(int level) const {
-        int64_t c = 0;
+    __device__ __forceinline__ int at_least(int level) const {
+        int c = 0;
 #pragma unroll
-        for (int k = 0; k < kSortedBatch / 32; ++k)
-            if (k == 0 || n[k] > 0) c += pairs_of(n[k], tokens) - first_at(n[k], off[k], level);
-        // 2^31 pairs at most for each request; counts of a warp in 64 bits
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-        return c;
+        for (int k = 0; k < kEach; ++k)
+            if (k < each) c += pairs_of(n[k]) - first_at(n[k], off[k], level);
+        return __reduce_add_sync(0xffffffffu, c);
     }
     __device__ __forceinline__ void start(const PromptParams &p, int pair_tokens, int lane) {
         tokens = pair_tokens;
+        each = (p.B + 31) / 32;
         sorted = p.B <= kSortedBatch;
-        b0 = 0;
-        before = total = 0;
-        int longest = 0;
+        b0 = before = upto = 0;
+        passed = total = 0;
+        int longest = 1;
         if (sorted) {
 #pragma unroll
-            for (int k = 0; k < kSortedBatch / 32; ++k) {
-                n[k] = off[k] = 0;
+            for (int k = 0; k < kEach; ++k) {
+                n[k] = off[k] = row0[k] = key0[k] = 0;
                 const int b = k * 32 + lane;
                 if (b < p.B) {
                     const Prompt r = load_prompt(p, b);
                     n[k] = r.n;
                     off[k] = r.m - r.n;
+                    row0[k] = r.row0;
+                    key0[k] = r.key0;
                     if (r.n > 0) longest = max(longest, (r.m + kKeys - 1) / kKeys);
+                    total += pairs_of(r.n);
                 }
-                total += pairs_of(n[k], tokens);
             }
         } else {
-            for (int b = lane; b < p.B; b += 32) total += pairs_of(load_prompt(p, b).n, tokens);
+            for (int b = lane; b < p.B; b += 32) total += pairs_of(load_prompt(p, b).n);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        top = max(1, __reduce_max_sync(0xffffffffu, longest));
+        sorted = sorted && total < 1 << 30;  // more only where offsets overlap
+        level = __reduce_max_sync(0xffffffffu, longest) + 1;
     }
     // Pair number r of the order (r < total, rising from call to call).
-    __device__ __noinline__ Item find(const PromptParams &p, int64_t r, int lane) {
+    __device__ __forceinline__ Item find(const PromptParams &p, int64_t r, int lane) {
         Item x;
+        x.b = -1;
         if (sorted) {
-            int lo = 1, hi = top + 1;  // at_least(lo) > r >= at_least(hi)
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (at_least(mid) > r) lo = mid;
-                else hi = mid;
+            for (int steps = 0; upto <= r && steps < 4; ++steps) {
+                before = upto;
+                upto = at_least(--level);
             }
-            int64_t rest = r - at_least(lo + 1);
-            x.b = -1;
-            for (int k = 0; k < kSortedBatch / 32 && x.b < 0; ++k) {
-                int mine = 0, t0 = 0, nk = 0, ok = 0;
+            if (upto <= r) {
+                int lo = 1, hi = level;  // at_least(lo) > r >= at_least(hi)
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (at_least(mid) > r) lo = mid;
+                    else hi = mid;
+                }
+                level = lo;
+                before = at_least(lo + 1);
+                upto = at_least(lo);
+            }
+            int rest = (int)r - before;
 #pragma unroll
-                for (int i = 0; i < kSortedBatch / 32; ++i)
-                    if (i == k) nk = n[i], ok = off[i];
-                t0 = first_at(nk, ok, lo);
-                mine = first_at(nk, ok, lo + 1) - t0;
-                if (nk <= 0) mine = 0;
-                int64_t upto = mine;
+            for (int k = 0; k < kEach; ++k) {
+                if (k >= each || x.b >= 0) continue;
+                const int t0 = first_at(n[k], off[k], level), mine = first_at(n[k], off[k], level + 1) - t0;
+                int s = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
+                    const int y = __shfl_up_sync(0xffffffffu, s, o);
+                    if (lane >= o) s += y;
                 }
-                const uint32_t past = __ballot_sync(0xffffffffu, upto > rest);
+                const uint32_t past = __ballot_sync(0xffffffffu, s > rest);
                 if (past) {
                     const int w = __ffs(past) - 1;
                     x.b = k * 32 + w;
-                    const int64_t start = __shfl_sync(0xffffffffu, upto - mine, w);
-                    x.tok0 = (__shfl_sync(0xffffffffu, t0, w) + (int)(rest - start)) * tokens;
+                    x.tok0 = __shfl_sync(0xffffffffu, t0 + rest - (s - mine), w) * (int)tokens;
+                    x.row0 = __shfl_sync(0xffffffffu, row0[k], w);
+                    x.n = __shfl_sync(0xffffffffu, n[k], w);
+                    x.key0 = __shfl_sync(0xffffffffu, key0[k], w);
+                    x.off = __shfl_sync(0xffffffffu, off[k], w);
                 } else {
-                    rest -= __shfl_sync(0xffffffffu, upto, 31);
+                    rest -= __shfl_sync(0xffffffffu, s, 31);
                 }
             }
-        } else {
-            for (;;) {
-                const int mine = b0 + lane < p.B ? pairs_of(load_prompt(p, b0 + lane).n, tokens) : 0;
-                int64_t upto = mine;
+            return x;
+        }
+        for (;;) {
+            Prompt q = {0, 0, 0, 0, false};
+            if (b0 + lane < p.B) q = load_prompt(p, b0 + lane);
+            const int mine = pairs_of(q.n);
+            int64_t s = mine;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
-                }
-                const uint32_t past = __ballot_sync(0xffffffffu, before + upto > r);
-                if (past || b0 >= p.B) {
-                    const int w = past ? __ffs(past) - 1 : 0;
-                    x.b = past ? b0 + w : -1;
-                    const int64_t start = __shfl_sync(0xffffffffu, upto - mine, w);
-                    x.tok0 = (__shfl_sync(0xffffffffu, mine, w) - 1 - (int)(r - before - start)) * tokens;
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, upto, 31);
-                b0 += 32;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
             }
+            const uint32_t past = __ballot_sync(0xffffffffu, passed + s > r);
+            if (past || b0 >= p.B) {
+                const int w = past ? __ffs(past) - 1 : 0;
+                if (past) x.b = b0 + w;
+                const int64_t start = passed + __shfl_sync(0xffffffffu, s - mine, w);
+                x.tok0 = (__shfl_sync(0xffffffffu, mine, w) - 1 - (int)(r - start)) * (int)tokens;
+                x.row0 = __shfl_sync(0xffffffffu, q.row0, w);
+                x.n = __shfl_sync(0xffffffffu, q.n, w);
+                x.key0 = __shfl_sync(0xffffffffu, q.key0, w);
+                x.off = __shfl_sync(0xffffffffu, q.m - q.n, w);
+                return x;
+            }
+            passed += __shfl_sync(0xffffffffu, s, 31);
+            b0 += 32;
         }
-        if (x.b >= 0) {
-            const Prompt q = load_prompt(p, x.b);
-            x.row0 = q.row0;
-            x.n = q.n;
-            x.key0 = q.key0;
-            x.off = q.m - q.n;
-        }
-        return x;
     }
 };
 
@@ -253,9 +263,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// The n lowest bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; }
+
 // A row's output again, over its visible keys alone (one warp; m and l are right as they
 // are: masked scores never enter them).  Stops once every column is NaN.
-__device__ __noinline__ void repair_row(const PromptParams &p, const Item &x, int token, int head, float m, float l, int lane) {
+__device__ __forceinline__ void repair_row(const PromptParams &p, const Item &x, int token, int head, float m, float l, int lane) {
     constexpr int kMost = SPEC_KV_MAX_HEAD_DIM / 32;
     const uint16_t *q = (const uint16_t *)p.q + (int64_t)(x.row0 + token) * p.ld_q + (int64_t)head * p.D;
     float a[kMost], o[kMost];
@@ -294,6 +307,9 @@ __device__ __noinline__ void repair_row(const PromptParams &p, const Item &x, in
     for (int c = 0; c < kMost; ++c)
         if (c * 32 + lane < p.D) dst[c * 32 + lane] = (uint16_t)pack_bf16x2(o[c], 0.f);
 }
+
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
 
 template <int NP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -349,8 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return !dead && x.b >= 0;
     };
 
+    // Softmax rows live in registers: 256 threads x 208 + 128 x 88 is what 384 were launched with.
     if (warp == kFindWarp) {
         // ---------------------------------------------------------------- items
+        fewer_registers();
         Finder f;
         f.start(p, tokens * subs, lane);
         const int64_t total = f.total * p.H;
@@ -361,8 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item x;
             x.b = -1;
             if (!last) {
-                x = f.find(p, i / p.H, lane);
-                x.h = (int)(i % p.H);
+                const int64_t r = i / p.H;
+                x = f.find(p, r, lane);
+                x.h = (int)(i - r * p.H);
+                x.t = tiles_of(p, x, tokens, subs);
             }
             const int at = told % kItems;
             if (told >= kItems) wait(&sm.item_empty[at], (told / kItems - 1) & 1);
@@ -376,10 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kCopyWarp) {
         // ---------------------------------------------------------------- copies
+        fewer_registers();
         int sent = 0, nq = 0;
         Item x;
         while (take(x)) {
-            const Tiles t = tiles_of(p, x, tokens, subs);
+            const Tiles &t = x.t;
             if (t.count == 0) continue;
             if (nq > 0) wait(&sm.q_empty, (nq - 1) & 1);
             if (dead) break;
@@ -414,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nq > 0) mbar_wait(&sm.q_full, (nq - 1) & 1, kWaitNs);
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- products
+        fewer_registers();
         const uint32_t idesc_s = bf16_idesc(kKeys, false), idesc_o = bf16_idesc(p.D, true);
         const uint64_t dq = smem_desc(smem_addr(sm.q), 16, 1024, 2), dk = smem_desc(smem_addr(sm.ring), 16, 1024, 2);
         const uint64_t dv = smem_desc(smem_addr(sm.ring), kPanel, 1024, 2);
@@ -421,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int got = 0, nq = 0, np[2] = {0, 0};  // ring slots, query tiles, tiles of weights used
         Item x;
         while (take(x)) {
-            const Tiles t = tiles_of(p, x, tokens, subs);
+            const Tiles &t = x.t;
             if (t.count == 0) continue;
             int done[2] = {0, 0};
             wait(&sm.q_full, nq & 1);
@@ -481,26 +503,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&sm.drain, 0, kWaitNs);
     } else if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax
+        more_registers();
         const int a = warp >> 2, w4 = warp & 3, r = w4 * 32 + lane;
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16, tS = tm + a * 128 + lanes, tO = tm + 256 + a * 128 + lanes;
         const float scale = p.scale_log2;
         const float2 scale2 = make_float2(scale, scale);
         const int tok_r = r / p.group, head_r = r - tok_r * p.group;
+        const int tok_w0 = __shfl_sync(0xffffffffu, tok_r, 0), tok_w1 = __shfl_sync(0xffffffffu, tok_r, 31);
         const bool wide = ((uintptr_t)p.out & 31) == 0;
         int ns = 0, no = 0;  // tiles of scores, outputs taken
         Item x;
         while (take(x)) {
-            const Tiles t = tiles_of(p, x, tokens, subs);
+            const Tiles &t = x.t;
             const int first = x.tok0 + a * tokens, have = min(tokens, x.n - first);
             if (a >= subs || have <= 0) continue;
-            const auto sub = t.sub[a];
+            const auto sub = a == 0 ? t.sub[0] : t.sub[1];
             const int todo = sub.count(), token = first + tok_r;
             const bool mine = tok_r < have;  // also false for rows past the last whole token
             const int pos = mine ? x.off + token : -1;
             // positions of the warp's first and last row that counts
-            const int wp0 = x.off + first + (w4 * 32) / p.group, wp1 = x.off + first + min(have - 1, (w4 * 32 + 31) / p.group);
+            const int wp0 = x.off + first + tok_w0, wp1 = x.off + first + min(have - 1, tok_w1);
             float m = kNegInf, ref = 0.f;  // the reference (log2) and what is subtracted
-            float2 l = make_float2(0.f, 0.f);
+            float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             int done = 0;
             for (int i = 0; done < todo && !dead; ++i) {
                 if (!sub.active(i)) continue;
@@ -509,25 +533,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ns;
                 if (dead) break;
                 tc_fence_after();
-                uint32_t s[kKeys];
-                tmem_ld<kKeys>(tS, s);
-                tmem_wait_ld();
-                if (j0 + kKeys - 1 > wp0 || (p.window > 0 && j0 <= wp1 - p.window && j0 + kKeys > p.sinks)) {
-                    const int hi = pos - j0, lo = p.window > 0 && pos >= 0 ? pos - p.window - j0 : -1, sinks = p.sinks - j0;
+                // The row's maximum over both halves; the second one is read again for its
+                // weights, so that registers hold half a row besides what is in flight.
+                const bool partly = j0 + kKeys - 1 > wp0 || (p.window > 0 && j0 <= wp1 - p.window && j0 + kKeys > p.sinks);
+                const int hi = pos - j0, lo = p.window > 0 && pos >= 0 ? pos - p.window - j0 : -1, sinks = p.sinks - j0;
+                auto mask = [&](uint32_t (&s)[64], int c0) {  // of columns c0 .., those the row does not see
+                    if (partly) {
 #pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (c > hi || (c <= lo && c >= sinks)) s[c] = 0xff800000u;
+                        for (int c = 0; c < 64; c += 32) {
+                            const int d = c0 + c;
+                            const uint32_t seen = bits_below(hi + 1 - d) & (~bits_below(lo + 1 - d) | bits_below(sinks - d));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1)) s[c + e] = 0xff800000u;
+                        }
+                    }
+                };
+                // four chains: two warps a scheduler hide little of an instruction's latency
+                float tops[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+                auto maxima = [&](const uint32_t (&s)[64]) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+                };
+                uint32_t s[64];
+                {
+                    uint32_t s2[64];
+                    tmem_ld<64>(tS + 64, s2);
+                    tmem_wait_ld();
+                    tmem_ld<64>(tS, s);
+                    mask(s2, 64);
+                    maxima(s2);
                 }
-                float top = kNegInf;
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 2) top = max3(top, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                top *= scale;
+                tmem_wait_ld();
+                mask(s, 0);
+                maxima(s);
+                const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
                 const bool moves = top > m + kRefStep;  // also from -inf
                 if (__any_sync(0xffffffffu, moves)) {
                     const float alpha = moves && m > kNegInf ? ex2_approx(m - top) : 1.f;
                     if (moves) m = ref = top;
-                    l.x *= alpha;
-                    l.y *= alpha;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) l[e] = make_float2(l[e].x * alpha, l[e].y * alpha);
                     if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         for (int c = 0; c < p.D; c += 16) {
                             uint32_t o[16];
@@ -540,19 +588,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float2 nref = make_float2(-ref, -ref);
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 32) {
+                auto weights = [&](const uint32_t (&s)[64], int c, uint32_t at) {  // of 32 columns, into tensor memory
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float2 y = ffma2(make_float2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), scale2, nref);
                         y.x = ex2_approx(y.x);
                         y.y = ex2_approx(y.y);
-                        l = fadd2(l, y);
+                        l[e / 2 & 1] = fadd2(l[e / 2 & 1], y);
                         w[e / 2] = pack_bf16x2(y.x, y.y);
                     }
-                    tmem_st16(tS + c / 2, w);
-                }
+                    tmem_st16(at, w);
+                };
+                uint32_t s2[64];
+                weights(s, 0, tS);
+                tmem_ld<64>(tS + 64, s2);
+                weights(s, 32, tS + 16);
+                tmem_wait_ld();
+                mask(s2, 64);
+                weights(s2, 0, tS + 32);
+                weights(s2, 32, tS + 48);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -565,36 +620,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             if (dead) break;
-            const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float sum = (l[0].x + l[0].y) + (l[1].x + l[1].y), inv = sum == 0.f ? 0.f : 1.f / sum;
             const int64_t row = (int64_t)(x.row0 + token) * p.Hq + x.h * p.group + head_r;
             uint16_t *dst = (uint16_t *)p.out + row * p.D;
-            bool odd = false;
-            for (int c = 0; c < p.D; c += 16) {
-                uint32_t o[16], w[8];
+            float odd = 0.f;  // stays 0 while everything is finite
+#pragma unroll
+            for (int c0 = 0; c0 < NP * 64; c0 += 64) {
+                uint32_t o[64];
                 if (todo > 0) {
-                    tmem_ld16(tO + c, o);
+                    tmem_ld<64>(tO + c0, o);  // columns past D are not used
                     tmem_wait_ld();
                 }
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float f = todo > 0 ? __uint_as_float(o[e]) * inv : 0.f, g = todo > 0 ? __uint_as_float(o[e + 1]) * inv : 0.f;
-                    odd |= !isfinite(f) || !isfinite(g);
-                    w[e / 2] = pack_bf16x2(f, g);
-                }
-                if (mine) {
+                for (int c = 0; c < 64; c += 16) {
+                    if (c0 + c >= p.D) break;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float f = todo > 0 ? __uint_as_float(o[c + e]) * inv : 0.f, g = todo > 0 ? __uint_as_float(o[c + e + 1]) * inv : 0.f;
+                        odd = fmaf(f, 0.f, odd);
+                        odd = fmaf(g, 0.f, odd);
+                        w[e / 2] = pack_bf16x2(f, g);
+                    }
+                    if (!mine) continue;
                     if (wide) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c), "r"(w[0]), "r"(w[1]),
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c0 + c), "r"(w[0]), "r"(w[1]),
                                      "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                                      : "memory");
                     } else {
-                        *(uint4 *)(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *(uint4 *)(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        *(uint4 *)(dst + c0 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *(uint4 *)(dst + c0 + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
                 }
             }
             if (mine && p.lse) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
             tc_fence_before();
-            uint32_t again = __ballot_sync(0xffffffffu, odd && mine && todo > 0);
+            uint32_t again = __ballot_sync(0xffffffffu, odd != 0.f && mine && todo > 0);
             while (again) {
                 const int w = __ffs(again) - 1;
                 again &= again - 1;
@@ -604,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    if (warp == kThreads / 32 - 1) fewer_registers();  // idle: the fourth of its warpgroup
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_free(tm, 512);

@@ -1,4 +1,4 @@
-// prompt_tc.cu -- prompt attention on the tensor cores (bf16, heads of up to 128 columns).
+// prompt_tc.cu -- prompt attention on the tensor cores (bf16).
 //
 // An item is a key head's two row tiles of up to 128 rows (queries of consecutive tokens,
 // the group's heads of each) and the tiles of 128 keys that one of them sees.  For each key
@@ -245,11 +245,19 @@ struct Finder {
 };
 
 // ------------------------------------------------------------------ shared memory
+// Heads of up to 128 columns (NP panels of 64): two row tiles, whose S and O fill tensor
+// memory; a ring of tiles K0 V0 K1 V1 ..  Wider heads: O takes half of tensor memory, so one
+// row tile with two buffers of S, and the next tile's S is computed during the exponentials;
+// the ring holds halves of tiles (64 keys) in the order K0 K1 V0 K2 V1 ..
 template <int NP>
 struct PromptShared {
-    static constexpr int kStages = NP == 1 ? 10 : 5;
-    uint8_t q[2][NP * kPanel];
-    uint8_t ring[kStages][NP * kPanel];
+    static constexpr bool kWide = NP > 2;
+    static constexpr int kSubs = kWide ? 1 : 2;
+    static constexpr int kRingKeys = kWide ? 64 : 128, kPieces = kKeys / kRingKeys;
+    static constexpr int kRingPanel = kRingKeys * 128, kRingBytes = NP * kRingPanel;
+    static constexpr int kStages = NP == 1 ? 10 : NP == 3 ? 7 : 5;
+    uint8_t q[kSubs][NP * kPanel];
+    uint8_t ring[kStages][kRingBytes];
     uint64_t full[kStages], empty[kStages], q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
     uint64_t item_full[kItems], item_empty[kItems];
     Item items[kItems];
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap vmap, int tokens, int subs) {
     using SM = PromptShared<NP>;
     constexpr int NS = SM::kStages;
-    constexpr uint32_t kTileBytes = NP * kPanel;
+    constexpr bool kWide = SM::kWide;
     extern __shared__ __align__(1024) uint8_t raw[];
     SM &sm = *reinterpret_cast<SM *>(raw);
     const int tid = threadIdx.x, lane = tid & 31;
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     write_prompt_statuses(p, blockIdx.x * kThreads + tid, gridDim.x * kThreads);
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = sm.tmem;  // S of the two row tiles at 0 and 128, O at 256 and 384
+    const uint32_t tm = sm.tmem;  // S of the two row tiles (or its two buffers) at 0 and 128, O from 256
     bool dead = false;            // a wait ran out: end
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!dead && !try_barrier(smem_addr(bar), parity)) dead = !poll_barrier(smem_addr(bar), parity, &sm.failed);
@@ -406,28 +414,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (dead) break;
             if (elect_one()) {
                 const uint32_t bytes = (uint32_t)tokens * p.group * 128 * NP;
-                mbar_arrive_expect_tx(&sm.q_full, (t.sub[0].count() > 0 ? bytes : 0) + (t.sub[1].count() > 0 ? bytes : 0));
-                for (int a = 0; a < 2; ++a)
+                mbar_arrive_expect_tx(&sm.q_full, (t.sub[0].count() > 0 ? bytes : 0) + (t.sub[1].count() > 0 ? bytes : 0));  // wide: no second one
+#pragma unroll
+                for (int a = 0; a < SM::kSubs; ++a)
                     if (t.sub[a].count() > 0)
                         for (int c = 0; c < NP; ++c)
                             tma_load_4d(sm.q[a] + c * kPanel, &qmap, 64 * c, 0, x.h, x.row0 + x.tok0 + a * tokens, &sm.q_full);
             }
             __syncwarp();
             ++nq;
-            for (int i = 0; i < t.count && !dead; ++i) {
+            auto copy_tile = [&](bool values, int i) {
                 const int key = x.key0 + t.tile(i) * kKeys;
-                for (int kv = 0; kv < 2; ++kv) {
+                for (int part = 0; part < SM::kPieces; ++part) {
                     const int slot = sent % NS;
                     if (sent >= NS) wait(&sm.empty[slot], (sent / NS - 1) & 1);
-                    if (dead) break;
+                    if (dead) return;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(&sm.full[slot], kTileBytes);
+                        mbar_arrive_expect_tx(&sm.full[slot], SM::kRingBytes);
                         for (int c = 0; c < NP; ++c)
-                            tma_load_3d(sm.ring[slot] + c * kPanel, kv ? &vmap : &kmap, 64 * c, x.h, key, &sm.full[slot]);
+                            tma_load_3d(sm.ring[slot] + c * SM::kRingPanel, values ? &vmap : &kmap, 64 * c, x.h,
+                                        key + part * SM::kRingKeys, &sm.full[slot]);
                     }
                     __syncwarp();
                     ++sent;
                 }
+            };
+            if (kWide) copy_tile(false, 0);
+            for (int i = 0; i < t.count && !dead; ++i) {
+                if (!kWide) copy_tile(false, i);
+                else if (i + 1 < t.count) copy_tile(false, i + 1);
+                if (!dead) copy_tile(true, i);
             }
         }
         // none of the copies may be in flight when the CTA ends
@@ -436,9 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- products
         fewer_registers();
-        const uint32_t idesc_s = bf16_idesc(kKeys, false), idesc_o = bf16_idesc(p.D, true);
+        const uint32_t idesc_s = bf16_idesc(SM::kRingKeys, false), idesc_o = bf16_idesc(p.D, true);
         const uint64_t dq = smem_desc(smem_addr(sm.q), 16, 1024, 2), dk = smem_desc(smem_addr(sm.ring), 16, 1024, 2);
-        const uint64_t dv = smem_desc(smem_addr(sm.ring), kPanel, 1024, 2);
+        const uint64_t dv = smem_desc(smem_addr(sm.ring), SM::kRingPanel, 1024, 2);
         const int steps = p.D / 16;
         int got = 0, nq = 0, np[2] = {0, 0};  // ring slots, query tiles, tiles of weights used
         Item x;
@@ -448,54 +464,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             int done[2] = {0, 0};
             wait(&sm.q_full, nq & 1);
             ++nq;
-            for (int i = -1; i < t.count && !dead; ++i) {
-                // the ring holds K0 V0 K1 V1 ..: tile i's values, then tile i + 1's keys
-                const int sv = got + 2 * i + 1, sk = got + 2 * i + 2;
-                if (i >= 0) wait(&sm.full[sv % NS], (sv / NS) & 1);
-                tc_fence_after();
+            if constexpr (kWide) {
+                for (int i = -1; i < t.count && !dead; ++i) {
+                    if (i + 1 < t.count) {  // S of tile i + 1, in the buffer that the tile's number says
+                        const int buf = (np[0] + (i < 0 ? 0 : 1)) & 1;
+                        for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
+                            const int slot = got % NS;
+                            wait(&sm.full[slot], (got / NS) & 1);
+                            if (dead) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                const uint64_t k = dk + (uint64_t)(slot * (SM::kRingBytes >> 4));
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    const uint32_t tS = tm + a * 128, tO = tm + 256 + a * 128;
-                    if (i >= 0 && t.sub[a].active(i)) {
-                        wait(&sm.p_full[a], np[a] & 1);
+                                for (int s = 0; s < NP * 4; ++s)
+                                    if (s < steps)
+                                        mma_bf16(tm + buf * 128 + part * SM::kRingKeys, dq + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
+                                                 k + (s >> 2) * (SM::kRingPanel >> 4) + (s & 3) * 2, idesc_s, s > 0);
+                                mma_commit(&sm.empty[slot]);
+                                if (part + 1 == SM::kPieces) mma_commit(&sm.s_full[buf]);
+                                if (part + 1 == SM::kPieces && i + 2 == t.count) mma_commit(&sm.q_empty);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (i < 0) continue;
+                    wait(&sm.p_full[np[0] & 1], (np[0] >> 1) & 1);
+                    for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
+                        const int slot = got % NS;
+                        wait(&sm.full[slot], (got / NS) & 1);
                         if (dead) break;
-                        ++np[a];
                         tc_fence_after();
                         if (elect_one()) {
-                            const uint64_t v = dv + (uint64_t)((sv % NS) * (kTileBytes >> 4));
+                            const uint64_t v = dv + (uint64_t)(slot * (SM::kRingBytes >> 4));
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k) mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
-                        }
-                        __syncwarp();
-                        if (++done[a] == t.sub[a].count() && elect_one()) mma_commit(&sm.o_full[a]);
-                        __syncwarp();
-                    }
-                    if (i + 1 < t.count && t.sub[a].active(i + 1)) {
-                        wait(&sm.full[sk % NS], (sk / NS) & 1);
-                        if (dead) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint64_t q = dq + (uint64_t)(a * (kTileBytes >> 4)), k = dk + (uint64_t)((sk % NS) * (kTileBytes >> 4));
-#pragma unroll
-                            for (int s = 0; s < NP * 4; ++s)
-                                if (s < steps) {
-                                    const uint64_t at = (s >> 2) * (kPanel >> 4) + (s & 3) * 2;
-                                    mma_bf16(tS, q + at, k + at, idesc_s, s > 0);
-                                }
-                            mma_commit(&sm.s_full[a]);
+                            for (int k = 0; k < SM::kRingKeys / 16; ++k)
+                                mma_bf16_ta(tm + 256, tm + (np[0] & 1) * 128 + part * (SM::kRingKeys / 2) + k * 8, v + k * 128, idesc_o,
+                                            i > 0 || part > 0 || k > 0);
+                            mma_commit(&sm.empty[slot]);
+                            if (part + 1 == SM::kPieces) mma_commit(&sm.o_full[0]);
                         }
                         __syncwarp();
                     }
+                    ++np[0];
                 }
-                if (dead) break;
-                if (elect_one()) {
-                    if (i >= 0) mma_commit(&sm.empty[sv % NS]);
-                    if (i + 1 < t.count) mma_commit(&sm.empty[sk % NS]);
-                    if (i + 2 == t.count) mma_commit(&sm.q_empty);
+            } else {
+                for (int i = -1; i < t.count && !dead; ++i) {
+                    // the ring holds K0 V0 K1 V1 ..: tile i's values, then tile i + 1's keys
+                    const int sv = got + 2 * i + 1, sk = got + 2 * i + 2;
+                    if (i >= 0) wait(&sm.full[sv % NS], (sv / NS) & 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        const uint32_t tS = tm + a * 128, tO = tm + 256 + a * 128;
+                        if (i >= 0 && t.sub[a].active(i)) {
+                            wait(&sm.p_full[a], np[a] & 1);
+                            if (dead) break;
+                            ++np[a];
+                            tc_fence_after();
+                            if (elect_one()) {
+                                const uint64_t v = dv + (uint64_t)((sv % NS) * (SM::kRingBytes >> 4));
+#pragma unroll
+                                for (int k = 0; k < kKeys / 16; ++k) mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
+                            }
+                            __syncwarp();
+                            if (++done[a] == t.sub[a].count() && elect_one()) mma_commit(&sm.o_full[a]);
+                            __syncwarp();
+                        }
+                        if (i + 1 < t.count && t.sub[a].active(i + 1)) {
+                            wait(&sm.full[sk % NS], (sk / NS) & 1);
+                            if (dead) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                const uint64_t q = dq + (uint64_t)(a * (NP * kPanel >> 4)), k = dk + (uint64_t)((sk % NS) * (SM::kRingBytes >> 4));
+#pragma unroll
+                                for (int s = 0; s < NP * 4; ++s)
+                                    if (s < steps) {
+                                        const uint64_t at = (s >> 2) * (kPanel >> 4) + (s & 3) * 2;
+                                        mma_bf16(tS, q + at, k + at, idesc_s, s > 0);
+                                    }
+                                mma_commit(&sm.s_full[a]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (dead) break;
+                    if (elect_one()) {
+                        if (i >= 0) mma_commit(&sm.empty[sv % NS]);
+                        if (i + 1 < t.count) mma_commit(&sm.empty[sk % NS]);
+                        if (i + 2 == t.count) mma_commit(&sm.q_empty);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                got += 2 * t.count;
             }
-            got += 2 * t.count;
         }
         // no product may be under way when the tensor memory is freed
         if (elect_one()) mma_commit(&sm.drain);
@@ -505,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------------- softmax
         more_registers();
         const int a = warp >> 2, w4 = warp & 3, r = w4 * 32 + lane;
-        const uint32_t lanes = (uint32_t)(w4 * 32) << 16, tS = tm + a * 128 + lanes, tO = tm + 256 + a * 128 + lanes;
+        const uint32_t lanes = (uint32_t)(w4 * 32) << 16, tO = tm + 256 + a * 128 + lanes;
         const float scale = p.scale_log2;
         const float2 scale2 = make_float2(scale, scale);
         const int tok_r = r / p.group, head_r = r - tok_r * p.group;
@@ -529,7 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; done < todo && !dead; ++i) {
                 if (!sub.active(i)) continue;
                 const int j0 = t.tile(i) * kKeys;
-                wait(&sm.s_full[a], ns & 1);
+                const uint32_t tS = tm + (kWide ? ns & 1 : a) * 128 + lanes;
+                if (kWide) wait(&sm.s_full[ns & 1], (ns >> 1) & 1);
+                else wait(&sm.s_full[a], ns & 1);
                 ++ns;
                 if (dead) break;
                 tc_fence_after();
@@ -577,6 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) l[e] = make_float2(l[e].x * alpha, l[e].y * alpha);
                     if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        if (kWide) {  // S was ready before the last product with V
+                            wait(&sm.o_full[0], ns & 1);
+                            tc_fence_after();
+                        }
                         for (int c = 0; c < p.D; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(tO + c, o);
@@ -611,11 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[a]);
+                if (lane == 0) mbar_arrive(&sm.p_full[kWide ? (ns - 1) & 1 : a]);
                 ++done;
             }
             if (todo > 0) {
-                wait(&sm.o_full[a], no & 1);
+                wait(&sm.o_full[a], kWide ? (ns - 1) & 1 : no & 1);
                 ++no;
                 tc_fence_after();
             }
@@ -717,9 +784,10 @@ int launch(const PromptParams &p, const CUtensorMap &qmap, const CUtensorMap &km
 }  // namespace
 
 int launch_prompt_tc(const PromptParams &p, int dev, int sms, cudaStream_t st) {
-    if (p.D > 128 || p.group > kRows || p.n_q == 0 || p.n_k == 0) return SPEC_EUNSUPPORTED;
+    if (p.D > 256 || p.group > kRows || p.n_q == 0 || p.n_k == 0) return SPEC_EUNSUPPORTED;
     const int tokens = kRows / p.group;
     const cuuint64_t head = (cuuint64_t)p.D * 2;
+    const bool wide = p.D > 128;
     alignas(64) CUtensorMap qmap, kmap, vmap;
     {
         const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.group, (cuuint64_t)p.H, (cuuint64_t)p.n_q};
@@ -730,16 +798,18 @@ int launch_prompt_tc(const PromptParams &p, int dev, int sms, cudaStream_t st) {
     for (int v = 0; v < 2; ++v) {
         const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.n_k};
         const cuuint64_t strides[2] = {head, (cuuint64_t)(v ? p.ld_v : p.ld_k) * 2};
-        const cuuint32_t box[3] = {64, 1, kKeys};
+        const cuuint32_t box[3] = {64, 1, (cuuint32_t)(wide ? PromptShared<4>::kRingKeys : PromptShared<2>::kRingKeys)};
         if (!encode(v ? &vmap : &kmap, v ? p.v : p.k, 3, dims, strides, box)) return SPEC_EUNSUPPORTED;
     }
     // pairs of row tiles, at most; where they are too few for the SMs, single row tiles
     const int64_t pairs = (((int64_t)p.n_q + 2 * tokens - 1) / (2 * tokens) + p.B) * p.H;
-    const int subs = pairs < sms ? 1 : 2;
+    const int subs = wide || pairs < sms ? 1 : 2;
     const int64_t items = (((int64_t)p.n_q + subs * tokens - 1) / (subs * tokens) + p.B) * p.H;
     const int ctas = (int)(items < sms ? items : sms);
     if (p.D <= 64) return launch<1>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
-    return launch<2>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
+    if (p.D <= 128) return launch<2>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
+    if (p.D <= 192) return launch<3>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
+    return launch<4>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
 }
 
 }  // namespace specv

@@ -258,7 +258,7 @@ struct PromptShared {
     static constexpr int kStages = NP == 1 ? 10 : NP == 3 ? 7 : 5;
     uint8_t q[kSubs][NP * kPanel];
     uint8_t ring[kStages][kRingBytes];
-    uint64_t full[kStages], empty[kStages], q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+    uint64_t full[kStages], empty[kStages], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain;
     uint64_t item_full[kItems], item_empty[kItems];
     Item items[kItems];
     uint32_t tmem;
@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.q_empty, 1);
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sm.s_full[a], 1);
-            mbar_init(&sm.p_full[a], 4);
+            mbar_init(&sm.p_full[a][0], 4);
+            mbar_init(&sm.p_full[a][1], 4);
             mbar_init(&sm.o_full[a], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -488,10 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (i < 0) continue;
-                    wait(&sm.p_full[np[0] & 1], (np[0] >> 1) & 1);
                     for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
                         const int slot = got % NS;
                         wait(&sm.full[slot], (got / NS) & 1);
+                        wait(&sm.p_full[np[0] & 1][part], (np[0] >> 1) & 1);
                         if (dead) break;
                         tc_fence_after();
                         if (elect_one()) {
@@ -517,18 +518,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int a = 0; a < 2; ++a) {
                         const uint32_t tS = tm + a * 128, tO = tm + 256 + a * 128;
                         if (i >= 0 && t.sub[a].active(i)) {
-                            wait(&sm.p_full[a], np[a] & 1);
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                wait(&sm.p_full[a][part], np[a] & 1);
+                                if (dead) break;
+                                tc_fence_after();
+                                if (elect_one()) {
+                                    const uint64_t v = dv + (uint64_t)((sv % NS) * (SM::kRingBytes >> 4));
+#pragma unroll
+                                    for (int k = part * 4; k < part * 4 + 4; ++k)
+                                        mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
+                                    if (part > 0) mma_commit(&sm.o_full[a]);
+                                }
+                                __syncwarp();
+                            }
                             if (dead) break;
                             ++np[a];
-                            tc_fence_after();
-                            if (elect_one()) {
-                                const uint64_t v = dv + (uint64_t)((sv % NS) * (SM::kRingBytes >> 4));
-#pragma unroll
-                                for (int k = 0; k < kKeys / 16; ++k) mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
-                            }
-                            __syncwarp();
-                            if (++done[a] == t.sub[a].count() && elect_one()) mma_commit(&sm.o_full[a]);
-                            __syncwarp();
+                            ++done[a];
                         }
                         if (i + 1 < t.count && t.sub[a].active(i + 1)) {
                             wait(&sm.full[sk % NS], (sk / NS) & 1);
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok_r = r / p.group, head_r = r - tok_r * p.group;
         const int tok_w0 = __shfl_sync(0xffffffffu, tok_r, 0), tok_w1 = __shfl_sync(0xffffffffu, tok_r, 31);
         const bool wide = ((uintptr_t)p.out & 31) == 0;
-        int ns = 0, no = 0;  // tiles of scores, outputs taken
+        int ns = 0;  // tiles of scores
         Item x;
         while (take(x)) {
             const Tiles &t = x.t;
@@ -640,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) l[e] = make_float2(l[e].x * alpha, l[e].y * alpha);
                     if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        if (kWide) {  // S was ready before the last product with V
+                        if (kWide) {  // S was ready before the last tile's products
                             wait(&sm.o_full[0], ns & 1);
                             tc_fence_after();
                         }
@@ -667,23 +673,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_st16(at, w);
                 };
+                auto let_go = [&](int part) {  // of a half's weights, to the products
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_full[kWide ? (ns - 1) & 1 : a][part]);
+                };
                 uint32_t s2[64];
                 weights(s, 0, tS);
                 tmem_ld<64>(tS + 64, s2);
                 weights(s, 32, tS + 16);
+                let_go(0);
                 tmem_wait_ld();
                 mask(s2, 64);
                 weights(s2, 0, tS + 32);
                 weights(s2, 32, tS + 48);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[kWide ? (ns - 1) & 1 : a]);
+                // wide: the next S may be there before this tile's products are, and a barrier's
+                // parity tells a phase only where the one before is known to be over
+                if (kWide && ns > 1) wait(&sm.o_full[0], ns & 1);
+                let_go(1);
                 ++done;
             }
             if (todo > 0) {
-                wait(&sm.o_full[a], kWide ? (ns - 1) & 1 : no & 1);
-                ++no;
+                wait(&sm.o_full[a], (ns - 1) & 1);
                 tc_fence_after();
             }
             if (dead) break;

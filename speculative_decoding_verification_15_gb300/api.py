@@ -361,13 +361,15 @@ def kv_plan(pool: PagePool, page_table, held, keep_len, new_len, page_size: int,
     held [B] (int32, contiguous) are updated in place.  Returns cu_new [B + 1], seq_len [B],
     slot [n_out] (int64: page * page_size + place in it), position [n_out] and status [B];
     n_out bounds the new tokens, and rows behind the last one hold -1."""
-    dev = page_table.device
-    B = page_table.shape[0]
+    dev, B = page_table.device, page_table.shape[0]
+    if n_out < 0:
+        raise ValueError(f"n_out must not be negative, got {n_out}")
     ints = torch.empty(3 * B + 1 + n_out, dtype=_I32, device=dev)  # one allocation for what is int32
-    cu, seq_len, status, position = ints.split((B + 1, B, B, n_out))
     slot = torch.empty(n_out, dtype=torch.int64, device=dev)
-    binding.spec_kv_plan(pool, page_table, held, _i32(keep_len, dev), _i32(new_len, dev), page_size, cu, seq_len, slot,
-                         position, status, stream)
+    at = ints.data_ptr()
+    binding._plan(pool, page_table, held, _i32(keep_len, dev), _i32(new_len, dev), page_size, at, at + 4 * B + 4,
+                  slot.data_ptr(), at + 12 * B + 4, at + 8 * B + 4, n_out, stream)
+    cu, seq_len, status, position = ints.split_with_sizes((B + 1, B, B, n_out))
     return {"cu_new": cu, "seq_len": seq_len, "slot": slot, "position": position, "status": status}
 
 
@@ -433,6 +435,6 @@ def prompt_attention(q, k, v, cu_query, max_query: int, cu_key=None, scale: floa
     lse = torch.empty((n, heads), dtype=_F32, device=dev) if want_lse else None
     cu_query = _i32(cu_query, dev)
     status = torch.empty(max(0, cu_query.numel() - 1), dtype=_I32, device=dev)
-    binding.spec_prompt_attention(q, k, v, cu_query, max_query, _i32(cu_key, dev), dim ** -0.5 if scale is None else scale,
-                                  window, sinks, out, lse, status, stream)
+    binding._prompt(q, k, v, cu_query, max_query, _i32(cu_key, dev), dim ** -0.5 if scale is None else scale, window, sinks,
+                    out.data_ptr(), None if lse is None else lse.data_ptr(), status.data_ptr(), stream)
     return {"out": out, "lse": lse, "status": status}

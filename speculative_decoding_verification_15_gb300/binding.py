@@ -646,32 +646,47 @@ def spec_cache_attention(q, cache, page_table, seq_len, cu_query, max_query: int
             nbytes)
 
 
+def _plan(pool, page_table, held, keep_len, new_len, page_size, cu, seq_len, slot, position, status, n, stream) -> None:
+    """spec_kv_plan with the addresses of its outputs."""
+    free, count = pool
+    at = free.get_device()
+    if at < 0:
+        raise ValueError("the pool and the call's tensors must be on one CUDA device")
+    pages, (B, width) = free.numel(), page_table.shape
+    one = (B,)
+    _launch("spec_kv_plan", at, stream, _flat(free, "free", _I32, (pages,), at), _flat(count, "count", _I32, (1,), at), pages,
+            _count(page_size, "page_size"), _flat(page_table, "page_table", _I32, (B, width), at), width,
+            _flat(held, "held", _I32, one, at), B, _flat(keep_len, "keep_len", _I32, one, at),
+            _flat(new_len, "new_len", _I32, one, at), _count(n, "n_out"), cu, seq_len, slot, position, status)
+
+
 def spec_kv_plan(pool, page_table, held, keep_len, new_len, page_size: int, out_cu, out_seq_len, out_slot, out_position,
                  out_status, stream=None) -> None:
     """page_table [B, pages] and held [B], updated in place as is the pool; keep_len,
     new_len [B]; out_cu [B + 1], out_seq_len [B], out_slot [rows] int64, out_position
     [rows], out_status [B]."""
-    free, count = pool
-    at = free.get_device()
-    if at < 0:
-        raise ValueError("the pool and the call's tensors must be on one CUDA device")
-    (B, width), n = page_table.shape, out_slot.shape[0]
-    one = (B,)
-    _launch("spec_kv_plan", at, stream, _flat(free, "free", _I32, (free.numel(),), at), _flat(count, "count", _I32, (1,), at),
-            free.numel(), _count(page_size, "page_size"), _flat(page_table, "page_table", _I32, (B, width), at), width,
-            _flat(held, "held", _I32, one, at), B, _flat(keep_len, "keep_len", _I32, one, at),
-            _flat(new_len, "new_len", _I32, one, at), n, _flat(out_cu, "out_cu", _I32, (B + 1,), at),
-            _flat(out_seq_len, "out_seq_len", _I32, one, at), _flat(out_slot, "out_slot", torch.int64, (n,), at),
-            _flat(out_position, "out_position", _I32, (n,), at), _flat(out_status, "out_status", _I32, one, at))
+    at, B, n = pool[0].get_device(), page_table.shape[0], out_slot.shape[0]
+    _plan(pool, page_table, held, keep_len, new_len, page_size, _flat(out_cu, "out_cu", _I32, (B + 1,), at),
+          _flat(out_seq_len, "out_seq_len", _I32, (B,), at), _flat(out_slot, "out_slot", torch.int64, (n,), at),
+          _flat(out_position, "out_position", _I32, (n,), at), _flat(out_status, "out_status", _I32, (B,), at), n, stream)
 
 
 def _head_rows(t, name, index: int):
     """Tokens, heads, head_dim and row stride of [tokens, heads, head_dim] rows."""
-    shape = t.shape
+    shape, strides = t.shape, t.stride()
     if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(shape)}")
     n, heads, dim = shape
-    return n, heads, dim, _token_rows(t, name, heads, dim, index) if n else heads * dim
+    if t.get_device() != index:
+        raise ValueError(f"{name} is not on the device of the call's other tensors")
+    if n == 0:
+        return 0, heads, dim, heads * dim
+    if strides[2] != 1 or (strides[1] != dim and heads > 1):
+        raise ValueError(f"{name} must have heads and head_dim contiguous within a token")
+    ld = strides[0] if n > 1 else heads * dim
+    if ld < heads * dim:
+        raise ValueError(f"{name}: token rows overlap")
+    return n, heads, dim, ld
 
 
 def spec_rotary(q, k, position, freq, axis, adjacent: bool, scale: float, out_q, out_k, stream=None) -> None:
@@ -682,38 +697,36 @@ def spec_rotary(q, k, position, freq, axis, adjacent: bool, scale: float, out_q,
     if at < 0:
         raise ValueError("the call's tensors must be on one CUDA device")
     n, heads, dim, ldq = _head_rows(q, "q", at)
-    dtype, keys, ldk, ldok = q.dtype, 0, 0, 0
+    dtype, keys, ldk, ldok, pk, pok = q.dtype, 0, 0, 0, None, None
     no, ho, do, ldo = _head_rows(out_q, "out_q", at)
-    if out_q.dtype is not dtype or (no, ho, do) != (n, heads, dim):
+    if out_q.dtype is not dtype or no != n or ho != heads or do != dim:
         raise ValueError("out_q must have q's shape and dtype")
     if k is not None:
         nk, keys, dk, ldk = _head_rows(k, "k", at)
         if k.dtype is not dtype or nk != n or dk != dim:
             raise ValueError("q and k must share tokens, head_dim and dtype")
         no, ho, do, ldok = _head_rows(out_k, "out_k", at)
-        if out_k.dtype is not dtype or (no, ho, do) != (n, keys, dim):
+        if out_k.dtype is not dtype or no != n or ho != keys or do != dim:
             raise ValueError("out_k must have k's shape and dtype")
-    if (position.dtype is not _I32 or position.dim() not in (1, 2) or position.shape[-1] != n or position.get_device() != at
-            or (n > 1 and position.stride(-1) != 1)):
+        pk, pok = k.data_ptr(), out_k.data_ptr()
+    shape, strides = position.shape, position.stride()
+    if (position.dtype is not _I32 or not 1 <= len(shape) <= 2 or shape[-1] != n or position.get_device() != at
+            or (n > 1 and strides[-1] != 1)):
         raise ValueError(f"position must be int32 [{n}] or [axes, {n}] with contiguous rows on q's device")
-    axes = 1 if position.dim() == 1 else position.shape[0]
-    ldp = position.stride(0) if axes > 1 else 0
+    axes, ldp = (shape[0], strides[0]) if len(shape) == 2 else (1, 0)
     if axes < 1 or (axes > 1 and ldp < n):
         raise ValueError("position must have one row or more that do not overlap")
     pairs = freq.numel()
     if axes > 1 and axis is None:
         raise ValueError("positions of several axes need the axis of each pair")
-    _launch("spec_rotary", at, stream, q.data_ptr(), None if k is None else k.data_ptr(), _dtype_code(q), ldq, ldk, heads,
-            keys, dim, n, position.data_ptr(), ldp, axes, _flat(freq, "freq", torch.float64, (pairs,), at),
-            None if axis is None else _flat(axis, "axis", _I32, (pairs,), at), pairs, int(bool(adjacent)), scale,
-            out_q.data_ptr(), None if k is None else out_k.data_ptr(), ldo, ldok)
+    _launch("spec_rotary", at, stream, q.data_ptr(), pk, _dtype_code(q), ldq, ldk, heads, keys, dim, _count(n, "tokens"), position.data_ptr(), ldp,
+            axes, _flat(freq, "freq", torch.float64, (pairs,), at),
+            None if axis is None else _flat(axis, "axis", _I32, (pairs,), at), pairs, 1 if adjacent else 0, scale,
+            out_q.data_ptr(), pok, ldo, ldok)
 
 
-def spec_prompt_attention(q, k, v, cu_query, max_query: int, cu_key, scale: float, window: int, sinks: int, out, out_lse,
-                          out_status, stream=None) -> None:
-    """q, out [queries, query heads, head_dim]; k, v [keys, heads, head_dim]; cu_query
-    [B + 1]; cu_key [B + 1], or None where the keys are the queries' tokens; out_lse
-    [queries, query heads] float32 or None; out_status [B]."""
+def _prompt(q, k, v, cu_query, max_query, cu_key, scale, window, sinks, out, lse, status, stream) -> None:
+    """spec_prompt_attention with the addresses of its outputs."""
     at, max_query = q.get_device(), _count(max_query, "max_query")
     window, sinks = _count(window, "window"), _count(sinks, "sinks")
     if at < 0:
@@ -729,13 +742,20 @@ def spec_prompt_attention(q, k, v, cu_query, max_query: int, cu_key, scale: floa
         raise ValueError("cu_query must be [B + 1]")
     if cu_key is None and m != n:
         raise ValueError("without cu_key the keys are the queries' tokens")
-    B = offsets[0] - 1
     _launch("spec_prompt_attention", at, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), ldq, ldk, ldv,
-            heads, keys, dim, n, m, B, _flat(cu_query, "cu_query", _I32, offsets, at), max_query,
-            None if cu_key is None else _flat(cu_key, "cu_key", _I32, offsets, at), scale, window, sinks,
-            _flat(out, "out", dtype, q.shape, at),
-            None if out_lse is None else _flat(out_lse, "out_lse", torch.float32, (n, heads), at),
-            _flat(out_status, "out_status", _I32, (B,), at))
+            heads, keys, dim, _count(n, "queries"), _count(m, "keys"), offsets[0] - 1, _flat(cu_query, "cu_query", _I32, offsets, at), max_query,
+            None if cu_key is None else _flat(cu_key, "cu_key", _I32, offsets, at), scale, window, sinks, out, lse, status)
+
+
+def spec_prompt_attention(q, k, v, cu_query, max_query: int, cu_key, scale: float, window: int, sinks: int, out, out_lse,
+                          out_status, stream=None) -> None:
+    """q, out [queries, query heads, head_dim]; k, v [keys, heads, head_dim]; cu_query
+    [B + 1]; cu_key [B + 1], or None where the keys are the queries' tokens; out_lse
+    [queries, query heads] float32 or None; out_status [B]."""
+    at = q.get_device()
+    _prompt(q, k, v, cu_query, max_query, cu_key, scale, window, sinks, _flat(out, "out", q.dtype, q.shape, at),
+            None if out_lse is None else _flat(out_lse, "out_lse", torch.float32, q.shape[:2], at),
+            _flat(out_status, "out_status", _I32, (cu_query.numel() - 1,), at), stream)
 
 
 def profile_enable(on: bool) -> None:

@@ -40,7 +40,10 @@ def check(got, x, position, freq, axis, adjacent=False, scale=1.0):
 @pytest.mark.parametrize("T,Hq,Hk,D,rot,sections", [
     (1, 32, 8, 128, 128, None), (8, 4, 1, 64, 64, (16, 8, 8)), (301, 3, 3, 80, 80, (20, 20)), (57, 5, 1, 96, 32, (4, 6, 6)),
     (5, 64, 8, 256, 256, (1, 2, 3, 122)), (33, 2, 2, 16, 16, None), (19, 7, 1, 36, 20, (3, 7)), (3, 1, 1, 2, 2, None),
-    (1001, 8, 2, 128, 64, (12, 10, 10)), (4, 2, 1, 24, 0, None)])
+    (1001, 8, 2, 128, 64, (12, 10, 10)), (4, 2, 1, 24, 0, None),
+    # many tokens: whole tokens a warp, lanes that meet one unit of each head or several
+    (3001, 4, 1, 128, 128, (24, 20, 20)), (2600, 3, 1, 80, 48, None), (2500, 5, 2, 96, 96, None), (2700, 1, 1, 256, 0, None),
+    (2433, 12, 4, 256, 256, (100, 28))])
 def test_against_64_bits(pkg, T, Hq, Hk, D, rot, sections, adjacent, dtype):
     axes = 1 if sections is None else len(sections)
     q, k, pos = inputs(T + D, T, Hq, Hk, D, dtype, axes, 100000)

@@ -553,12 +553,22 @@ int spec_rotary(const void *q, const void *k, int dtype, int64_t ld_q, int64_t l
  *  scale        positive and finite; window >= 0; sinks >= 0 (unused when window == 0)
  *  out          [n_query, num_query_heads, head_dim] of type dtype, 16-byte aligned
  *  out_lse      [n_query, num_query_heads] float, or NULL
- *  out_status   [B]: 0 or SPEC_STATUS_BAD_LENGTH (nothing of the request is written)
+ *  out_status   [B]: 0, SPEC_STATUS_BAD_LENGTH (nothing of the request is written) or
+ *               SPEC_STATUS_INTERNAL for every request (rows are unspecified)
+ *  ws           at least spec_prompt_attention_workspace_size bytes, 256-byte aligned (none for
+ *               most calls: few queries over many keys are cut along the keys); nothing in it
+ *               needs initialising or lasts beyond the call
+ * bf16 on the tensor cores: a weight is rounded to bf16 before it meets its value (2^-8 of
+ * itself at most); scores, sums and results are fp32 until the output's own rounding.  fp32
+ * is fp32 throughout.  Results are the same from call to call.
  */
+size_t spec_prompt_attention_workspace_size(int n_query, int n_key, int B, int num_query_heads, int num_heads, int head_dim,
+                                            int dtype, int window, int sinks);
 int spec_prompt_attention(const void *q, const void *k, const void *v, int dtype, int64_t ld_q, int64_t ld_k,
                           int64_t ld_v, int num_query_heads, int num_heads, int head_dim, int n_query, int n_key, int B,
                           const int32_t *cu_query, int max_query, const int32_t *cu_key, float scale, int window,
-                          int sinks, void *out, float *out_lse, int32_t *out_status, void *cuda_stream);
+                          int sinks, void *out, float *out_lse, int32_t *out_status, void *ws, size_t ws_bytes,
+                          void *cuda_stream);
 
 /* Short text for a return code. */
 const char *spec_error_string(int err);

@@ -13,7 +13,8 @@ from .api import (cache_attention, cache_attention_reset, kv_append, kv_cache, k
 from .binding import (KVCache, PagePool, SpecError, spec_cache_attention,  # noqa: F401
                       spec_cache_attention_workspace_size, spec_kv_append, spec_kv_gather, spec_kv_plan,
                       spec_markov_draft, spec_markov_draft_topk, spec_markov_topk_workspace_size,
-                      spec_prompt_attention, spec_rotary, spec_schedule_threshold, spec_schedule_verify_len,
+                      spec_prompt_attention, spec_prompt_attention_workspace_size, spec_rotary,
+                      spec_schedule_threshold, spec_schedule_verify_len,
                       spec_schedule_verify_len_stale, spec_verify_greedy, spec_verify_greedy_early_exit,
                       spec_verify_greedy_flat, spec_verify_sample, spec_verify_sample_early_exit,
                       spec_verify_sample_flat, spec_verify_sample_noalloc,

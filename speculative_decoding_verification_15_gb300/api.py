@@ -421,6 +421,9 @@ def _i32_rows(t, device):
     return _as_i32(t, device)
 
 
+PROMPT_SPLIT_KEYS = 2048  # calls with fewer keys need no workspace
+
+
 @_on_its_stream
 def prompt_attention(q, k, v, cu_query, max_query: int, cu_key=None, scale: float | None = None, window: int = 0,
                      sinks: int = 0, want_lse: bool = False, stream=None) -> dict:
@@ -435,6 +438,13 @@ def prompt_attention(q, k, v, cu_query, max_query: int, cu_key=None, scale: floa
     lse = torch.empty((n, heads), dtype=_F32, device=dev) if want_lse else None
     cu_query = _i32(cu_query, dev)
     status = torch.empty(max(0, cu_query.numel() - 1), dtype=_I32, device=dev)
+    ws, nbytes = None, 0
+    if k.shape[0] >= PROMPT_SPLIT_KEYS and q.dtype is torch.bfloat16 and k.dim() == 3:
+        nbytes = binding.spec_prompt_attention_workspace_size(n, k.shape[0], status.numel(), heads, k.shape[1], dim,
+                                                              binding.SPEC_BF16, window, sinks)
+        if nbytes:  # from the allocator in stream order: calls share none, a graph keeps its own
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     binding._prompt(q, k, v, cu_query, max_query, _i32(cu_key, dev), dim ** -0.5 if scale is None else scale, window, sinks,
-                    out.data_ptr(), None if lse is None else lse.data_ptr(), status.data_ptr(), stream)
+                    out.data_ptr(), None if lse is None else lse.data_ptr(), status.data_ptr(),
+                    None if ws is None else ws.data_ptr(), nbytes, stream)
     return {"out": out, "lse": lse, "status": status}

@@ -129,8 +129,10 @@ def load(path: str | None = None):
                                     P, P, I64, I64, P]
         lib.spec_rotary.restype = I32
         lib.spec_prompt_attention.argtypes = [P, P, P, I32, I64, I64, I64, I32, I32, I32, I32, I32, I32, P, I32, P,
-                                              ctypes.c_float, I32, I32, P, P, P, P]
+                                              ctypes.c_float, I32, I32, P, P, P, P, SZ, P]
         lib.spec_prompt_attention.restype = I32
+        lib.spec_prompt_attention_workspace_size.argtypes = [I32] * 9
+        lib.spec_prompt_attention_workspace_size.restype = SZ
         lib.spec_error_string.argtypes = [I32]
         lib.spec_error_string.restype = ctypes.c_char_p
         lib.spec_last_cuda_error.argtypes = []
@@ -725,8 +727,15 @@ def spec_rotary(q, k, position, freq, axis, adjacent: bool, scale: float, out_q,
             out_q.data_ptr(), pok, ldo, ldok)
 
 
-def _prompt(q, k, v, cu_query, max_query, cu_key, scale, window, sinks, out, lse, status, stream) -> None:
-    """spec_prompt_attention with the addresses of its outputs."""
+def spec_prompt_attention_workspace_size(n_query: int, n_key: int, B: int, num_query_heads: int, num_heads: int,
+                                         head_dim: int, dtype: int, window: int = 0, sinks: int = 0) -> int:
+    return (_lib or load()).spec_prompt_attention_workspace_size(
+        _count(n_query, "n_query"), _count(n_key, "n_key"), _count(B, "B"), _count(num_query_heads, "num_query_heads"),
+        _count(num_heads, "num_heads"), _count(head_dim, "head_dim"), dtype, _count(window, "window"), _count(sinks, "sinks"))
+
+
+def _prompt(q, k, v, cu_query, max_query, cu_key, scale, window, sinks, out, lse, status, workspace, nbytes, stream) -> None:
+    """spec_prompt_attention with the addresses of its outputs and workspace."""
     at, max_query = q.get_device(), _count(max_query, "max_query")
     window, sinks = _count(window, "window"), _count(sinks, "sinks")
     if at < 0:
@@ -744,18 +753,21 @@ def _prompt(q, k, v, cu_query, max_query, cu_key, scale, window, sinks, out, lse
         raise ValueError("without cu_key the keys are the queries' tokens")
     _launch("spec_prompt_attention", at, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), ldq, ldk, ldv,
             heads, keys, dim, _count(n, "queries"), _count(m, "keys"), offsets[0] - 1, _flat(cu_query, "cu_query", _I32, offsets, at), max_query,
-            None if cu_key is None else _flat(cu_key, "cu_key", _I32, offsets, at), scale, window, sinks, out, lse, status)
+            None if cu_key is None else _flat(cu_key, "cu_key", _I32, offsets, at), scale, window, sinks, out, lse, status, workspace,
+            nbytes)
 
 
 def spec_prompt_attention(q, k, v, cu_query, max_query: int, cu_key, scale: float, window: int, sinks: int, out, out_lse,
-                          out_status, stream=None) -> None:
+                          out_status, workspace=None, stream=None) -> None:
     """q, out [queries, query heads, head_dim]; k, v [keys, heads, head_dim]; cu_query
     [B + 1]; cu_key [B + 1], or None where the keys are the queries' tokens; out_lse
-    [queries, query heads] float32 or None; out_status [B]."""
-    at = q.get_device()
+    [queries, query heads] float32 or None; out_status [B]; workspace uint8 of
+    spec_prompt_attention_workspace_size bytes (None where that is 0)."""
+    at, nbytes = q.get_device(), 0 if workspace is None else workspace.numel()
     _prompt(q, k, v, cu_query, max_query, cu_key, scale, window, sinks, _flat(out, "out", q.dtype, q.shape, at),
             None if out_lse is None else _flat(out_lse, "out_lse", torch.float32, q.shape[:2], at),
-            _flat(out_status, "out_status", _I32, (cu_query.numel() - 1,), at), stream)
+            _flat(out_status, "out_status", _I32, (cu_query.numel() - 1,), at),
+            None if workspace is None else _flat(workspace, "workspace", torch.uint8, (nbytes,), at), nbytes, stream)
 
 
 def profile_enable(on: bool) -> None:

@@ -268,11 +268,19 @@ int launch_rows_any(const PromptParams &p, int dev, int sms, cudaStream_t st) {
 
 using namespace specv;
 
+extern "C" size_t spec_prompt_attention_workspace_size(int n_query, int n_key, int B, int num_query_heads, int num_heads,
+                                                       int head_dim, int dtype, int window, int sinks) {
+    if (dtype != SPEC_BF16 || n_query <= 0 || n_key <= 0 || B <= 0 || num_query_heads <= 0 || num_heads <= 0 ||
+        num_query_heads % num_heads || num_query_heads / num_heads > 128 || head_dim <= 0 || window < 0 || sinks < 0)
+        return 0;
+    return prompt_plan(n_query, n_key, B, num_query_heads / num_heads, num_heads, head_dim, window, window > 0 ? sinks : 0).bytes;
+}
+
 extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v, int dtype, int64_t ld_q, int64_t ld_k,
                                      int64_t ld_v, int num_query_heads, int num_heads, int head_dim, int n_query,
                                      int n_key, int B, const int32_t *cu_query, int max_query, const int32_t *cu_key,
-                                     float scale, int window, int sinks, void *out, float *out_lse, int32_t *out_status,
-                                     void *cuda_stream) {
+                                     float scale, int window, int sinks, void *out, float *out_lse, int32_t *out_status, void *ws,
+                                     size_t ws_bytes, void *cuda_stream) {
     if (dtype != SPEC_BF16 && dtype != SPEC_F32) return SPEC_EINVAL;
     if (B < 0 || n_query < 0 || n_key < 0 || max_query < 0 || num_query_heads <= 0 || num_heads <= 0 || head_dim <= 0 ||
         window < 0 || sinks < 0 || num_query_heads % num_heads)
@@ -290,6 +298,8 @@ extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v
     if (n_key > 0 && (!k || !v || ld_k < row || ld_v < row)) return SPEC_EINVAL;
     if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v) % esz || ((uintptr_t)out & 15) || ((uintptr_t)out_lse & 3)) return SPEC_EINVAL;
     if (((uintptr_t)cu_query | (uintptr_t)cu_key | (uintptr_t)out_status) & 3) return SPEC_EINVAL;
+    const size_t need = spec_prompt_attention_workspace_size(n_query, n_key, B, num_query_heads, num_heads, head_dim, dtype, window, sinks);
+    if (need > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 255))) return SPEC_EWORKSPACE;
     int dev = 0, sms = 0, rc;
     if ((rc = kv_device_info(&dev, &sms))) return rc;
     if (n_query > 0 && (rc = kv_check_device_pointer(q, dev))) return rc;
@@ -316,6 +326,13 @@ extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v
     p.window = window < (1 << 30) ? window : (1 << 30);  // positions stay below 2^31
     p.sinks = window > 0 ? sinks : 0;
     p.scale_log2 = scale * kLog2e;
+    p.parts = 1;
+    if (need > 0) {
+        const PromptPlan plan = prompt_plan(n_query, n_key, B, group, num_heads, head_dim, p.window, p.sinks);
+        p.parts = plan.parts;
+        p.part_o = (float *)ws;
+        p.part_ml = (float2 *)((char *)ws + (size_t)plan.parts * n_query * num_query_heads * head_dim * sizeof(float));
+    }
     const cudaStream_t st = (cudaStream_t)cuda_stream;
     if (esz == 2) {
         rc = launch_prompt_tc(p, dev, sms, st);

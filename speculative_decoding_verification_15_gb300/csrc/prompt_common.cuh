@@ -15,7 +15,45 @@ struct PromptParams {
     int64_t ld_q, ld_k, ld_v;
     int B, n_q, n_k, max_query, Hq, H, group, D, window, sinks;
     float scale_log2;
+    int parts;        // tensor cores: of an item's tiles at most, joined afterwards if more than one
+    float *part_o;    // [parts][n_q * Hq][D]
+    float2 *part_ml;  // [parts][n_q * Hq]: reference and sum
 };
+
+// How the tensor-core kernel cuts a call, from what the host knows of it.
+struct PromptPlan {
+    int tokens, subs;  // of a row tile; row tiles an item
+    int64_t items;     // at most
+    int parts;
+    size_t bytes;      // of the parts' results
+};
+inline PromptPlan prompt_plan(int n_q, int n_k, int B, int group, int H, int D, int window, int sinks) {
+    constexpr int kSms = 152, kMostParts = 32, kLeastTiles = 8;
+    PromptPlan x = {};
+    x.tokens = 128 / group;
+    x.parts = 1;
+    // pairs of row tiles (heads of up to 128 columns), which keep the tensor cores busier;
+    // single ones where there is an SM for each (203 tokens of 32 heads: 11.1 us, in pairs 11.9)
+    const int64_t pairs = (((int64_t)n_q + 2 * x.tokens - 1) / (2 * x.tokens) + B) * H;
+    x.subs = D > 128 || 2 * pairs <= kSms ? 1 : 2;
+    x.items = (((int64_t)n_q + x.subs * x.tokens - 1) / (x.subs * x.tokens) + B) * H;
+    // Fewer items than SMs, over many keys: each one's tiles in parts, eight tiles or more on
+    // average (a part costs its rows' sums in fp32, written and read).  The kernel, which knows
+    // the lengths, cuts each request into as many parts as its length asks for, up to x.parts.
+    int64_t keys = (int64_t)n_k / B - n_q / B / 2;
+    window = window < (1 << 30) ? window : (1 << 30);  // as the kernels see it
+    if (window > 0 && keys > (int64_t)window + sinks) keys = (int64_t)window + sinks;
+    const int64_t most = keys / 128 / kLeastTiles;
+    if (x.items < kSms && B <= 128 && most > 1) {
+        x.parts = (int)(most < kMostParts ? most : kMostParts);
+        if (D <= 128) x.subs = 2;
+        x.items = (((int64_t)n_q + x.subs * x.tokens - 1) / (x.subs * x.tokens) + B) * H;
+        const int64_t want = (6 * kSms + x.items - 1) / x.items;
+        if (x.parts > want) x.parts = (int)want;
+    }
+    if (x.parts > 1) x.bytes = (size_t)x.parts * n_q * group * H * (D + 2) * sizeof(float);
+    return x;
+}
 
 struct Prompt {
     int row0, n, key0, m;  // first query row, queries, first key row, keys; n = 0 where unusable

@@ -74,7 +74,9 @@ struct Tiles {
     struct Sub {
         int s1, w, e;
         __device__ __forceinline__ bool active(int i) const { return i < s1 || (i >= w && i < e); }
-        __device__ __forceinline__ int count() const { return s1 + e - w; }
+        __device__ __forceinline__ int count(int i0, int i1) const {  // of indexes i0 .. i1 - 1
+            return max(0, min(s1, i1) - i0) + max(0, min(e, i1) - max(w, i0));
+        }
     } sub[2];
     __device__ __forceinline__ int tile(int i) const { return i < s1 ? i : w0 + (i - s1); }
 };
@@ -82,6 +84,7 @@ struct Tiles {
 struct Item {
     int b;                            // -1: no more
     int row0, n, key0, off, tok0, h;  // off: position of query 0; tok0: first token of the first row tile
+    int part, parts, i0, i1;          // its part of the tiles: indexes i0 .. i1 - 1
     Tiles t;
 };
 
@@ -122,6 +125,7 @@ struct Finder {
     int64_t passed;                // not sorted: pairs of the requests below b0
     int64_t total;                 // pairs in all
     int each, b0, level;           // each: requests a lane really has, at most
+    int parts[kEach];              // cut: of a lane's requests
     bool sorted;
 
     __device__ __forceinline__ int pairs_of(int n) const { return (int)(((uint32_t)n + tokens - 1) / tokens); }
@@ -169,6 +173,81 @@ struct Finder {
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         sorted = sorted && total < 1 << 30;  // more only where offsets overlap
         level = __reduce_max_sync(0xffffffffu, longest) + 1;
+    }
+    // Items in parts (few requests, p.parts > 1): request after request; in each, head by head
+    // and part by part all pairs, which read the same keys at the same time.  Every part is of
+    // about `unit` tiles, so that all cost alike: the unit is the one of six whose rounds over
+    // the CTAs take least.  Returns the number of items.
+    __device__ __forceinline__ int64_t cut(const PromptParams &p, int ctas) {
+        constexpr int kFixed = 3;  // tiles that an item's start and end cost
+        int tiles[kEach];
+        int64_t all = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int first = (pairs_of(n[k]) - 1) * (int)tokens;  // of the last pair
+            tiles[k] = n[k] > 0 ? max(1, span_of<kKeys>(p, off[k] + first, off[k] + n[k] - 1).count) : 0;
+            all += (int64_t)pairs_of(n[k]) * tiles[k];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        const int longest = __reduce_max_sync(0xffffffffu, max(max(tiles[0], tiles[1]), max(tiles[2], tiles[3])));
+        int64_t least = 0, count = 0;
+        int unit = 0;
+        for (int rounds = 1; rounds <= 6; ++rounds) {
+            const int64_t fair = (all * p.H + (int64_t)rounds * ctas - 1) / ((int64_t)rounds * ctas);
+            const int u = (int)max(max(fair, (int64_t)4), (int64_t)(longest + p.parts - 1) / p.parts);
+            int64_t items = 0;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) items += (int64_t)pairs_of(n[k]) * ((tiles[k] + u - 1) / u);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
+            items *= p.H;
+            const int64_t time = (items + ctas - 1) / ctas * (u + kFixed);
+            if (unit == 0 || time < least) {
+                least = time;
+                unit = u;
+                count = items;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) parts[k] = (tiles[k] + unit - 1) / unit;
+        return count;
+    }
+    // Item i of these (i below their number).
+    __device__ __forceinline__ Item find_part(const PromptParams &p, int64_t i, int lane) {
+        Item x;
+        x.b = -1;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            if (k >= each || x.b >= 0) continue;
+            const int pairs = pairs_of(n[k]);
+            const int64_t mine = (int64_t)pairs * parts[k] * p.H;
+            int64_t s = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, s > i);
+            if (past) {
+                const int w = __ffs(past) - 1;
+                const int64_t rest = i - __shfl_sync(0xffffffffu, s - mine, w);
+                const int np = __shfl_sync(0xffffffffu, pairs, w), nparts = __shfl_sync(0xffffffffu, parts[k], w);
+                const int which = (int)(rest / np);
+                x.b = k * 32 + w;
+                x.tok0 = (np - 1 - (int)(rest - (int64_t)which * np)) * (int)tokens;
+                x.h = which / nparts;
+                x.part = which - x.h * nparts;
+                x.parts = nparts;
+                x.row0 = __shfl_sync(0xffffffffu, row0[k], w);
+                x.n = __shfl_sync(0xffffffffu, n[k], w);
+                x.key0 = __shfl_sync(0xffffffffu, key0[k], w);
+                x.off = __shfl_sync(0xffffffffu, off[k], w);
+            } else {
+                i -= __shfl_sync(0xffffffffu, s, 31);
+            }
+        }
+        return x;
     }
     // Pair number r of the order (r < total, rising from call to call).
     __device__ __forceinline__ Item find(const PromptParams &p, int64_t r, int lane) {
@@ -274,9 +353,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The n lowest bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; }
 
-// A row's output again, over its visible keys alone (one warp; m and l are right as they
-// are: masked scores never enter them).  Stops once every column is NaN.
-__device__ __forceinline__ void repair_row(const PromptParams &p, const Item &x, int token, int head, float m, float l, int lane) {
+__device__ __forceinline__ void store_v8(void *dst, const uint32_t *w) {  // 32-byte aligned
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// A row's output again, over its visible keys of the item's tiles alone (one warp; its
+// reference and sum are right as they are: masked scores never enter them).  Stops once
+// every column is NaN.
+__device__ __forceinline__ void repair_row(const PromptParams &p, const Item &x, const Tiles::Sub &sub, int token, int head, float ref,
+                                           float inv, int lane) {
     constexpr int kMost = SPEC_KV_MAX_HEAD_DIM / 32;
     const uint16_t *q = (const uint16_t *)p.q + (int64_t)(x.row0 + token) * p.ld_q + (int64_t)head * p.D;
     float a[kMost], o[kMost];
@@ -286,34 +373,38 @@ __device__ __forceinline__ void repair_row(const PromptParams &p, const Item &x,
         o[c] = 0.f;
     }
     const int pos = x.off + token;
-    const float ref = m == kNegInf ? 0.f : m, inv = l == 0.f ? 0.f : 1.f / l;
-    for (int j = 0; j <= pos; ++j) {
-        if (!visible(p, pos, j)) {
-            j = max(j, pos - p.window);  // on to the window
-            continue;
+    bool some = true;  // a column is not NaN yet
+    for (int i = x.i0; i < x.i1 && some; ++i) {
+        if (!sub.active(i)) continue;
+        const int j0 = x.t.tile(i) * kKeys, end = min(j0 + kKeys, pos + 1);
+        for (int j = j0; j < end && some; ++j) {
+            if (!visible(p, pos, j)) continue;
+            const int64_t row = (int64_t)(x.key0 + j);
+            const uint16_t *k = (const uint16_t *)p.k + row * p.ld_k + (int64_t)x.h * p.D;
+            const uint16_t *v = (const uint16_t *)p.v + row * p.ld_v + (int64_t)x.h * p.D;
+            float s = 0.f;
+#pragma unroll
+            for (int c = 0; c < kMost; ++c)
+                if (c * 32 + lane < p.D) s += a[c] * ld_elem<2>(k, c * 32 + lane);
+            s = warp_sum(s);
+            const float w = ex2_approx(fmaf(s, p.scale_log2, -ref)) * inv;
+            bool finite = false;
+#pragma unroll
+            for (int c = 0; c < kMost; ++c)
+                if (c * 32 + lane < p.D) {
+                    o[c] = fmaf(w, ld_elem<2>(v, c * 32 + lane), o[c]);
+                    finite |= !isnan(o[c]);
+                }
+            some = __any_sync(0xffffffffu, finite);
         }
-        const int64_t row = (int64_t)(x.key0 + j);
-        const uint16_t *k = (const uint16_t *)p.k + row * p.ld_k + (int64_t)x.h * p.D;
-        const uint16_t *v = (const uint16_t *)p.v + row * p.ld_v + (int64_t)x.h * p.D;
-        float s = 0.f;
-#pragma unroll
-        for (int c = 0; c < kMost; ++c)
-            if (c * 32 + lane < p.D) s += a[c] * ld_elem<2>(k, c * 32 + lane);
-        s = warp_sum(s);
-        const float w = ex2_approx(fmaf(s, p.scale_log2, -ref)) * inv;
-        bool finite = false;
-#pragma unroll
-        for (int c = 0; c < kMost; ++c)
-            if (c * 32 + lane < p.D) {
-                o[c] = fmaf(w, ld_elem<2>(v, c * 32 + lane), o[c]);
-                finite |= !isnan(o[c]);
-            }
-        if (!__any_sync(0xffffffffu, finite)) break;
     }
-    uint16_t *dst = (uint16_t *)p.out + ((int64_t)(x.row0 + token) * p.Hq + head) * p.D;
+    const int64_t row = (int64_t)(x.row0 + token) * p.Hq + head;
 #pragma unroll
     for (int c = 0; c < kMost; ++c)
-        if (c * 32 + lane < p.D) dst[c * 32 + lane] = (uint16_t)pack_bf16x2(o[c], 0.f);
+        if (c * 32 + lane < p.D) {
+            if (p.parts > 1) p.part_o[((int64_t)x.part * p.n_q * p.Hq + row) * p.D + c * 32 + lane] = o[c];
+            else ((uint16_t *)p.out)[row * p.D + c * 32 + lane] = (uint16_t)pack_bf16x2(o[c], 0.f);
+        }
 }
 
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
@@ -380,7 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fewer_registers();
         Finder f;
         f.start(p, tokens * subs, lane);
-        const int64_t total = f.total * p.H;
+        const bool cut = p.parts > 1;
+        const int64_t total = cut ? f.cut(p, gridDim.x) : f.total * p.H;
         for (int64_t round = 0;; ++round) {
             const int64_t i = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             const bool last = round * gridDim.x >= total;
@@ -388,10 +480,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item x;
             x.b = -1;
             if (!last) {
-                const int64_t r = i / p.H;
-                x = f.find(p, r, lane);
-                x.h = (int)(i - r * p.H);
+                if (cut) {
+                    x = f.find_part(p, i, lane);
+                } else {
+                    const int64_t r = i / p.H;
+                    x = f.find(p, r, lane);
+                    x.h = (int)(i - r * p.H);
+                    x.part = 0;
+                    x.parts = 1;
+                }
                 x.t = tiles_of(p, x, tokens, subs);
+                x.i0 = (int)((int64_t)x.t.count * x.part / x.parts);
+                x.i1 = (int)((int64_t)x.t.count * (x.part + 1) / x.parts);
             }
             const int at = told % kItems;
             if (told >= kItems) wait(&sm.item_empty[at], (told / kItems - 1) & 1);
@@ -410,20 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item x;
         while (take(x)) {
             const Tiles &t = x.t;
-            if (t.count == 0) continue;
-            if (nq > 0) wait(&sm.q_empty, (nq - 1) & 1);
-            if (dead) break;
-            if (elect_one()) {
-                const uint32_t bytes = (uint32_t)tokens * p.group * 128 * NP;
-                mbar_arrive_expect_tx(&sm.q_full, (t.sub[0].count() > 0 ? bytes : 0) + (t.sub[1].count() > 0 ? bytes : 0));  // wide: no second one
-#pragma unroll
-                for (int a = 0; a < SM::kSubs; ++a)
-                    if (t.sub[a].count() > 0)
-                        for (int c = 0; c < NP; ++c)
-                            tma_load_4d(sm.q[a] + c * kPanel, &qmap, 64 * c, 0, x.h, x.row0 + x.tok0 + a * tokens, &sm.q_full);
-            }
-            __syncwarp();
-            ++nq;
+            if (x.i0 >= x.i1) continue;
             auto copy_tile = [&](bool values, int i) {
                 const int key = x.key0 + t.tile(i) * kKeys;
                 for (int part = 0; part < SM::kPieces; ++part) {
@@ -440,10 +527,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++sent;
                 }
             };
-            if (kWide) copy_tile(false, 0);
-            for (int i = 0; i < t.count && !dead; ++i) {
-                if (!kWide) copy_tile(false, i);
-                else if (i + 1 < t.count) copy_tile(false, i + 1);
+            copy_tile(false, x.i0);  // the ring is free before the last item's queries are
+            if (dead) break;
+            if (nq > 0) wait(&sm.q_empty, (nq - 1) & 1);
+            if (dead) break;
+            if (elect_one()) {
+                const uint32_t bytes = (uint32_t)tokens * p.group * 128 * NP;
+                const bool one = t.sub[0].count(x.i0, x.i1) > 0, two = t.sub[1].count(x.i0, x.i1) > 0;  // wide: no second one
+                mbar_arrive_expect_tx(&sm.q_full, (one ? bytes : 0) + (two ? bytes : 0));
+#pragma unroll
+                for (int a = 0; a < SM::kSubs; ++a)
+                    if (a == 0 ? one : two)
+                        for (int c = 0; c < NP; ++c)
+                            tma_load_4d(sm.q[a] + c * kPanel, &qmap, 64 * c, 0, x.h, x.row0 + x.tok0 + a * tokens, &sm.q_full);
+            }
+            __syncwarp();
+            ++nq;
+            for (int i = x.i0; i < x.i1 && !dead; ++i) {
+                if (!kWide && i > x.i0) copy_tile(false, i);
+                if (kWide && i + 1 < x.i1) copy_tile(false, i + 1);
                 if (!dead) copy_tile(true, i);
             }
         }
@@ -461,14 +563,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item x;
         while (take(x)) {
             const Tiles &t = x.t;
-            if (t.count == 0) continue;
+            const int i0 = x.i0, i1 = x.i1;
+            if (i0 >= i1) continue;
             int done[2] = {0, 0};
             wait(&sm.q_full, nq & 1);
             ++nq;
             if constexpr (kWide) {
-                for (int i = -1; i < t.count && !dead; ++i) {
-                    if (i + 1 < t.count) {  // S of tile i + 1, in the buffer that the tile's number says
-                        const int buf = (np[0] + (i < 0 ? 0 : 1)) & 1;
+                for (int i = i0 - 1; i < i1 && !dead; ++i) {
+                    if (i + 1 < i1) {  // S of tile i + 1, in the buffer that the tile's number says
+                        const int buf = (np[0] + (i < i0 ? 0 : 1)) & 1;
                         for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
                             const int slot = got % NS;
                             wait(&sm.full[slot], (got / NS) & 1);
@@ -483,12 +586,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  k + (s >> 2) * (SM::kRingPanel >> 4) + (s & 3) * 2, idesc_s, s > 0);
                                 mma_commit(&sm.empty[slot]);
                                 if (part + 1 == SM::kPieces) mma_commit(&sm.s_full[buf]);
-                                if (part + 1 == SM::kPieces && i + 2 == t.count) mma_commit(&sm.q_empty);
+                                if (part + 1 == SM::kPieces && i + 2 == i1) mma_commit(&sm.q_empty);
                             }
                             __syncwarp();
                         }
                     }
-                    if (i < 0) continue;
+                    if (i < i0) continue;
                     for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
                         const int slot = got % NS;
                         wait(&sm.full[slot], (got / NS) & 1);
@@ -500,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < SM::kRingKeys / 16; ++k)
                                 mma_bf16_ta(tm + 256, tm + (np[0] & 1) * 128 + part * (SM::kRingKeys / 2) + k * 8, v + k * 128, idesc_o,
-                                            i > 0 || part > 0 || k > 0);
+                                            i > i0 || part > 0 || k > 0);
                             mma_commit(&sm.empty[slot]);
                             if (part + 1 == SM::kPieces) mma_commit(&sm.o_full[0]);
                         }
@@ -509,15 +612,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++np[0];
                 }
             } else {
-                for (int i = -1; i < t.count && !dead; ++i) {
+                for (int i = i0 - 1; i < i1 && !dead; ++i) {
                     // the ring holds K0 V0 K1 V1 ..: tile i's values, then tile i + 1's keys
-                    const int sv = got + 2 * i + 1, sk = got + 2 * i + 2;
-                    if (i >= 0) wait(&sm.full[sv % NS], (sv / NS) & 1);
+                    const int sv = got + 2 * (i - i0) + 1, sk = got + 2 * (i - i0) + 2;
+                    if (i >= i0) wait(&sm.full[sv % NS], (sv / NS) & 1);
                     tc_fence_after();
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         const uint32_t tS = tm + a * 128, tO = tm + 256 + a * 128;
-                        if (i >= 0 && t.sub[a].active(i)) {
+                        if (i >= i0 && t.sub[a].active(i)) {
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
                                 wait(&sm.p_full[a][part], np[a] & 1);
@@ -536,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ++np[a];
                             ++done[a];
                         }
-                        if (i + 1 < t.count && t.sub[a].active(i + 1)) {
+                        if (i + 1 < i1 && t.sub[a].active(i + 1)) {
                             wait(&sm.full[sk % NS], (sk / NS) & 1);
                             if (dead) break;
                             tc_fence_after();
@@ -555,13 +658,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (dead) break;
                     if (elect_one()) {
-                        if (i >= 0) mma_commit(&sm.empty[sv % NS]);
-                        if (i + 1 < t.count) mma_commit(&sm.empty[sk % NS]);
-                        if (i + 2 == t.count) mma_commit(&sm.q_empty);
+                        if (i >= i0) mma_commit(&sm.empty[sv % NS]);
+                        if (i + 1 < i1) mma_commit(&sm.empty[sk % NS]);
+                        if (i + 2 == i1) mma_commit(&sm.q_empty);
                     }
                     __syncwarp();
                 }
-                got += 2 * t.count;
+                got += 2 * (i1 - i0);
             }
         }
         // no product may be under way when the tensor memory is freed
@@ -581,11 +684,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ns = 0;  // tiles of scores
         Item x;
         while (take(x)) {
-            const Tiles &t = x.t;
+            const auto let_item_go = [] {};
             const int first = x.tok0 + a * tokens, have = min(tokens, x.n - first);
-            if (a >= subs || have <= 0) continue;
-            const auto sub = a == 0 ? t.sub[0] : t.sub[1];
-            const int todo = sub.count(), token = first + tok_r;
+            if (a >= subs || have <= 0) {
+                let_item_go();
+                continue;
+            }
+            const int list_s1 = x.t.s1, list_step = x.t.w0 - list_s1;  // of the list of tiles
+            const auto sub = a == 0 ? x.t.sub[0] : x.t.sub[1];
+            const int todo = sub.count(x.i0, x.i1), token = first + tok_r;
             const bool mine = tok_r < have;  // also false for rows past the last whole token
             const int pos = mine ? x.off + token : -1;
             // positions of the warp's first and last row that counts
@@ -593,9 +700,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = kNegInf, ref = 0.f;  // the reference (log2) and what is subtracted
             float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             int done = 0;
-            for (int i = 0; done < todo && !dead; ++i) {
+            for (int i = x.i0; done < todo && !dead; ++i) {
                 if (!sub.active(i)) continue;
-                const int j0 = t.tile(i) * kKeys;
+                const int j0 = (i < list_s1 ? i : i + list_step) * kKeys;
                 const uint32_t tS = tm + (kWide ? ns & 1 : a) * 128 + lanes;
                 if (kWide) wait(&sm.s_full[ns & 1], (ns >> 1) & 1);
                 else wait(&sm.s_full[a], ns & 1);
@@ -606,10 +713,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // weights, so that registers hold half a row besides what is in flight.
                 const bool partly = j0 + kKeys - 1 > wp0 || (p.window > 0 && j0 <= wp1 - p.window && j0 + kKeys > p.sinks);
                 const int hi = pos - j0, lo = p.window > 0 && pos >= 0 ? pos - p.window - j0 : -1, sinks = p.sinks - j0;
-                auto mask = [&](uint32_t (&s)[64], int c0) {  // of columns c0 .., those the row does not see
+                auto mask = [&](auto &s, int c0) {  // of columns c0 .., those the row does not see
                     if (partly) {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 32) {
+                        for (int c = 0; c < (int)(sizeof(s) / 4); c += 32) {
                             const int d = c0 + c;
                             const uint32_t seen = bits_below(hi + 1 - d) & (~bits_below(lo + 1 - d) | bits_below(sinks - d));
 #pragma unroll
@@ -661,11 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float2 nref = make_float2(-ref, -ref);
-                auto weights = [&](const uint32_t (&s)[64], int c, uint32_t at) {  // of 32 columns, into tensor memory
+                auto weights = [&](const uint32_t *s, uint32_t at) {  // of 32 columns, into tensor memory
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float2 y = ffma2(make_float2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), scale2, nref);
+                        float2 y = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, nref);
                         y.x = ex2_approx(y.x);
                         y.y = ex2_approx(y.y);
                         l[e / 2 & 1] = fadd2(l[e / 2 & 1], y);
@@ -680,14 +787,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&sm.p_full[kWide ? (ns - 1) & 1 : a][part]);
                 };
                 uint32_t s2[64];
-                weights(s, 0, tS);
+                weights(s, tS);
                 tmem_ld<64>(tS + 64, s2);
-                weights(s, 32, tS + 16);
+                weights(s + 32, tS + 16);
                 let_go(0);
                 tmem_wait_ld();
                 mask(s2, 64);
-                weights(s2, 0, tS + 32);
-                weights(s2, 32, tS + 48);
+                weights(s2, tS + 32);
+                weights(s2 + 32, tS + 48);
                 // wide: the next S may be there before this tile's products are, and a barrier's
                 // parity tells a phase only where the one before is known to be over
                 if (kWide && ns > 1) wait(&sm.o_full[0], ns & 1);
@@ -699,12 +806,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             if (dead) break;
-            const float sum = (l[0].x + l[0].y) + (l[1].x + l[1].y), inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float sum = (l[0].x + l[0].y) + (l[1].x + l[1].y);
             const int64_t row = (int64_t)(x.row0 + token) * p.Hq + x.h * p.group + head_r;
+            const bool whole = p.parts == 1;
+            const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t slot = (int64_t)x.part * p.n_q * p.Hq + row;  // of a part's result
             uint16_t *dst = (uint16_t *)p.out + row * p.D;
+            float *part_o = whole ? nullptr : p.part_o + slot * p.D;
             float odd = 0.f;  // stays 0 while everything is finite
 #pragma unroll
             for (int c0 = 0; c0 < NP * 64; c0 += 64) {
+                if (!whole && todo == 0) break;
                 uint32_t o[64];
                 if (todo > 0) {
                     tmem_ld<64>(tO + c0, o);  // columns past D are not used
@@ -713,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) {
                     if (c0 + c >= p.D) break;
-                    uint32_t w[8];
+                    uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         const float f = todo > 0 ? __uint_as_float(o[c + e]) * inv : 0.f, g = todo > 0 ? __uint_as_float(o[c + e + 1]) * inv : 0.f;
@@ -722,26 +834,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                         w[e / 2] = pack_bf16x2(f, g);
                     }
                     if (!mine) continue;
-                    if (wide) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c0 + c), "r"(w[0]), "r"(w[1]),
-                                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                                     : "memory");
+                    if (!whole) {
+                        store_v8(part_o + c0 + c, o + c);
+                        store_v8(part_o + c0 + c + 8, o + c + 8);
+                    } else if (wide) {
+                        store_v8(dst + c0 + c, w);
                     } else {
                         *(uint4 *)(dst + c0 + c) = make_uint4(w[0], w[1], w[2], w[3]);
                         *(uint4 *)(dst + c0 + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
                 }
             }
-            if (mine && p.lse) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
+            if (mine && !whole) {
+                p.part_ml[slot] = make_float2(ref, sum);
+                if (x.part == 0)  // the places that this request has no part for
+                    for (int k = x.parts; k < p.parts; ++k) p.part_ml[(int64_t)k * p.n_q * p.Hq + row] = make_float2(kNegInf, 0.f);
+            }
+            if (mine && whole && p.lse) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
             tc_fence_before();
             uint32_t again = __ballot_sync(0xffffffffu, odd != 0.f && mine && todo > 0);
             while (again) {
                 const int w = __ffs(again) - 1;
                 again &= again - 1;
                 __syncwarp();
-                repair_row(p, x, __shfl_sync(0xffffffffu, token, w), x.h * p.group + __shfl_sync(0xffffffffu, head_r, w),
-                           __shfl_sync(0xffffffffu, m, w), __shfl_sync(0xffffffffu, sum, w), lane);
+                repair_row(p, x, sub, __shfl_sync(0xffffffffu, token, w), x.h * p.group + __shfl_sync(0xffffffffu, head_r, w),
+                           __shfl_sync(0xffffffffu, ref, w), __shfl_sync(0xffffffffu, inv, w), lane);
             }
+            let_item_go();
         }
     }
     if (warp == kThreads / 32 - 1) fewer_registers();  // idle: the fourth of its warpgroup
@@ -750,6 +869,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_free(tm, 512);
     if (sm.failed)
         for (int b = tid; b < p.B; b += kThreads) p.status[b] = SPEC_STATUS_INTERNAL;
+}
+
+// ------------------------------------------------------------------ parts of long items
+// A row's parts joined, in order: a warp a row, 4 columns a lane.  Bound by reading them.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptParams p) {
+    const Prompt r = load_prompt(p, blockIdx.y);
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = (int64_t)r.n * p.Hq, all = (int64_t)p.n_q * p.Hq, step = (int64_t)gridDim.x * (kJoinThreads / 32);
+    for (int64_t i = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); i < rows; i += step) {
+        const int64_t row = (int64_t)r.row0 * p.Hq + i;
+        const float2 ml = lane < p.parts ? p.part_ml[lane * all + row] : make_float2(kNegInf, 0.f);
+        const bool some = ml.y != 0.f;  // also NaN
+        const float top = warp_max_nan(some ? ml.x : kNegInf), ref = top == kNegInf ? 0.f : top;
+        const float weight = some ? ex2_approx(ml.x - ref) : 0.f, sum = warp_sum(some ? weight * ml.y : 0.f);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int c0 = 0; c0 < p.D; c0 += 128) {
+            const int c = c0 + lane * 4;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = 0; k < p.parts; ++k) {
+                const float w = __shfl_sync(0xffffffffu, weight, k);
+                if (w == 0.f || c >= p.D) continue;  // 0: nothing is there, or it does not count
+                const float4 y = __ldcs((const float4 *)(p.part_o + (k * all + row) * p.D + c));
+                o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
+            }
+            if (c < p.D) *(uint2 *)((uint16_t *)p.out + row * p.D + c) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        }
+        if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
+    }
 }
 
 // ------------------------------------------------------------------ host
@@ -790,6 +939,10 @@ int launch(const PromptParams &p, const CUtensorMap &qmap, const CUtensorMap &km
         set[dev].store(true);
     }
     prompt_tc_kernel<NP><<<ctas, kThreads, bytes, st>>>(p, qmap, kmap, vmap, tokens, subs);
+    const int rc = launch_status();
+    if (rc || p.parts == 1) return rc;
+    const int64_t blocks = ((int64_t)p.max_query * p.Hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+    prompt_join_kernel<<<dim3((unsigned)(blocks < 16384 ? blocks : 16384), p.B), kJoinThreads, 0, st>>>(p);
     return launch_status();
 }
 
@@ -813,11 +966,9 @@ int launch_prompt_tc(const PromptParams &p, int dev, int sms, cudaStream_t st) {
         const cuuint32_t box[3] = {64, 1, (cuuint32_t)(wide ? PromptShared<4>::kRingKeys : PromptShared<2>::kRingKeys)};
         if (!encode(v ? &vmap : &kmap, v ? p.v : p.k, 3, dims, strides, box)) return SPEC_EUNSUPPORTED;
     }
-    // pairs of row tiles, at most; where they are too few for the SMs, single row tiles
-    const int64_t pairs = (((int64_t)p.n_q + 2 * tokens - 1) / (2 * tokens) + p.B) * p.H;
-    const int subs = wide || pairs < sms ? 1 : 2;
-    const int64_t items = (((int64_t)p.n_q + subs * tokens - 1) / (subs * tokens) + p.B) * p.H;
-    const int ctas = (int)(items < sms ? items : sms);
+    const PromptPlan plan = prompt_plan(p.n_q, p.n_k, p.B, p.group, p.H, p.D, p.window, p.sinks);
+    const int64_t items = plan.items * plan.parts;  // at most
+    const int ctas = (int)(items < sms ? items : sms), subs = plan.subs;
     if (p.D <= 64) return launch<1>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
     if (p.D <= 128) return launch<2>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);
     if (p.D <= 192) return launch<3>(p, qmap, kmap, vmap, tokens, subs, ctas, dev, st);

@@ -80,6 +80,30 @@ def test_windows(pkg, new, total, Hq, H, D, window, sinks, dtype):
     close(x.call(pkg, want_lse=True, window=window, sinks=sinks), x.want(window=window, sinks=sinks))
 
 
+@pytest.mark.parametrize("new,total,Hq,H,D", [([33, 5, 0, 100], [5000, 40, 700, 7000], 4, 2, 128), ([70], [4000], 6, 2, 64),
+                                              ([1, 2], [9000, 3000], 8, 1, 256), ([40], [2600], 3, 3, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2500, 300)])
+def test_few_queries_over_many_keys(pkg, new, total, Hq, H, D, window, sinks):
+    """Items whose tiles are cut into parts, some of them without a tile."""
+    x = Inputs(D, new, total, Hq, H, D, BF16)
+    L = int(x.cu_k[-1])
+    assert pkg.spec_prompt_attention_workspace_size(int(x.cu_q[-1]), L, len(new), Hq, H, D, 0, window, sinks) > 0
+    close(x.call(pkg, want_lse=True, window=window, sinks=sinks), x.want(window=window, sinks=sinks))
+
+
+def test_parts_with_spoilt_keys(pkg):
+    """A NaN value behind a row, in the tile that it shares with the row's own last key."""
+    x = Inputs(31, [60], [5000], 4, 2, 64, BF16)
+    want = x.want()
+    x.v[4970] = float("nan")
+    x.k[4990] = float("nan")
+    got = x.call(pkg, want_lse=True)
+    out, lse, tol, tol_lse = want
+    g, gl = got["out"].double().cpu().numpy(), got["lse"].double().cpu().numpy()
+    assert (np.abs(g[:30] - out[:30]) <= tol[:30]).all() and (np.abs(gl[:50] - lse[:50]) <= tol_lse[:50]).all()
+    assert np.isnan(g[30:]).all() and np.isnan(gl[50:]).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_queries_that_see_nothing(pkg, D, dtype):

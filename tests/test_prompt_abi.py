@@ -36,7 +36,7 @@ def _rotary(binding, **kw):
 
 def _prompt(binding, **kw):
     a = dict(q=P, k=P, v=P, dtype=0, ldq=512, ldk=128, ldv=128, Hq=8, H=2, D=64, n=4, m=4, B=2, cu=P, max_query=4, cuk=None,
-             scale=0.1, window=0, sinks=0, out=P, lse=None, status=P)
+             scale=0.1, window=0, sinks=0, out=P, lse=None, status=P, ws=None, ws_bytes=0)
     a.update(kw)
     return binding.load().spec_prompt_attention(*a.values(), None)
 
@@ -70,6 +70,19 @@ def test_prompt_arguments(binding):
         assert _prompt(binding, **bad) == EINVAL, bad
     for bad in (dict(D=72), dict(D=272), dict(B=8193), dict(max_query=0x7fffffff), dict(H=65536, Hq=65536)):
         assert _prompt(binding, **bad) == EUNSUP, bad
+
+
+def test_prompt_workspace(binding):
+    size = binding.spec_prompt_attention_workspace_size
+    assert size(500, 500, 1, 32, 8, 128, 0) == 0 and size(64, 60000, 1, 32, 8, 128, 1) == 0  # short; fp32
+    need = size(64, 60000, 1, 32, 8, 128, 0)
+    assert need > 0 and need % (64 * 32 * 130 * 4) == 0
+    assert size(64, 60000, 1, 32, 8, 128, 0, 500, 4) == 0  # the window leaves little to cut
+    assert size(-1, 60000, 1, 32, 8, 128, 0) == size(64, 60000, 1, 32, 7, 128, 0) == size(64, 60000, 0, 32, 8, 128, 0) == 0
+    many = dict(n=64, m=60000, Hq=32, H=8, D=128, ldq=4096, ldk=1024, ldv=1024, B=1, cuk=P, max_query=64)
+    assert _prompt(binding, **many) == 4
+    assert _prompt(binding, **many, ws=P, ws_bytes=need - 1) == 4
+    assert _prompt(binding, **many, ws=ctypes.c_void_p(264), ws_bytes=need) == 4
 
 
 def test_refusals_of_the_package():

@@ -34,14 +34,14 @@ __device__ __forceinline__ float to_float(uint16_t x) { return __uint_as_float((
 // ND: columns of the output in 32s.
 template <typename T, int ND>
 struct RowsShape {
-    static constexpr int kEach = ND <= 4 ? 8 : 4;  // rows a thread
+    static constexpr int kEach = ND == 4 ? 8 : 4;  // rows a thread: two CTAs an SM up to 96 columns
     static constexpr int kRows = 16 * kEach;
     static constexpr int kStride = 32 * ND + 4;    // floats of a row: 16 bytes of skew
     static constexpr int kBytes = 4 * (kRows * kStride + 2 * kKeys * kStride + kRows * (kKeys + 4));
 };
 
-template <typename T, int ND>
-__global__ void __launch_bounds__(kRowsThreads) attention_rows_kernel(PromptParams p) {
+template <typename T, int ND, bool VEC>
+__global__ void __launch_bounds__(kRowsThreads, ND <= 3 ? 2 : 1) attention_rows_kernel(PromptParams p) {
     using S = RowsShape<T, ND>;
     constexpr int E = S::kEach, R = S::kRows, LD = S::kStride, LP = kKeys + 4;
     extern __shared__ __align__(16) float rows_smem[];
@@ -112,24 +112,33 @@ __global__ void __launch_bounds__(kRowsThreads) attention_rows_kernel(PromptPara
         int pos[E];  // a thread's rows: ty + 16 e
 #pragma unroll
         for (int e = 0; e < E; ++e) pos[e] = ty + 16 * e < nrows ? off + (first + ty + 16 * e) / p.group : -1;
+        // A tile of keys or values on its way to shared memory; rows past the request's are 0.
+        const int d4 = D / 4;
+        auto load_tile = [&](float *dst, const void *src, int64_t ld, int j0) {
+            const T *rows = (const T *)src + (int64_t)(r.key0 + j0) * ld + (int64_t)h * D;
+            const int have = r.m - j0;
+            for (int x = tid; x < kKeys * d4; x += kRowsThreads) {
+                const int row = (int)((uint32_t)x / (uint32_t)d4), c = (x - row * d4) * 4;
+                const T *from = rows + (row < have ? row * ld + c : 0);  // in bounds: j0 < r.m
+                float *to = dst + row * LD + c;
+                if (sizeof(T) == 4 && VEC) {
+                    const int bytes = row < have ? 16 : 0;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(bytes) : "memory");
+                } else {
+                    const float4 y = make_float4(to_float(from[0]), to_float(from[1]), to_float(from[2]), to_float(from[3]));
+                    *(float4 *)to = row < have ? y : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        auto arrived = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };  // all but the last one sent
+        if (span.count > 0) load_tile(sk, p.k, p.ld_k, span.tile(0) * kKeys);
         for (int i = 0; i < span.count; ++i) {
             const int j0 = span.tile(i) * kKeys;
             const bool masked = j0 + kKeys - 1 > pos0 || (p.window > 0 && j0 <= pos1 - p.window && j0 + kKeys > p.sinks) || nrows < R;
-            int strange = 0;  // values that are not finite
-            for (int x = tid; x < kKeys * (LD / 4); x += kRowsThreads) {
-                const int row = x / (LD / 4), c = (x - row * (LD / 4)) * 4;
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
-                if (j0 + row < r.m && c < D) {
-                    const T *ks = (const T *)p.k + (r.key0 + j0 + row) * p.ld_k + (int64_t)h * D + c;
-                    const T *vs = (const T *)p.v + (r.key0 + j0 + row) * p.ld_v + (int64_t)h * D + c;
-                    a = make_float4(to_float(ks[0]), to_float(ks[1]), to_float(ks[2]), to_float(ks[3]));
-                    d = make_float4(to_float(vs[0]), to_float(vs[1]), to_float(vs[2]), to_float(vs[3]));
-                    strange |= !isfinite(d.x) || !isfinite(d.y) || !isfinite(d.z) || !isfinite(d.w);
-                }
-                *(float4 *)(sk + row * LD + c) = a;
-                *(float4 *)(sv + row * LD + c) = d;
-            }
-            strange = __syncthreads_or(strange);
+            load_tile(sv, p.v, p.ld_v, j0);  // under way during the scores
+            arrived();
+            __syncthreads();
             // scores: pairs of columns summed side by side
             float2 s[E][4];
 #pragma unroll
@@ -150,6 +159,9 @@ __global__ void __launch_bounds__(kRowsThreads) attention_rows_kernel(PromptPara
                         s[e][k] = ffma2(make_float2(a[e].z, a[e].w), make_float2(d[k].z, d[k].w), s[e][k]);
                     }
             }
+            __syncthreads();  // the keys have been read: the next ones' copy runs until the next scores
+            if (i + 1 < span.count) load_tile(sk, p.k, p.ld_k, span.tile(i + 1) * kKeys);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 float x[4], top = kNegInf;
@@ -178,8 +190,18 @@ __global__ void __launch_bounds__(kRowsThreads) attention_rows_kernel(PromptPara
                     o[e][c].y *= alpha;
                 }
             }
-            __syncwarp();  // a row's 16 threads are of one warp
-            if (masked && strange) {  // a value that a row does not see must not meet its zero
+            arrived();
+            int strange = 0;  // values that are not finite
+            if (masked) {
+                __syncthreads();
+                for (int x = tid; x < kKeys * d4; x += kRowsThreads) {
+                    const int row = (int)((uint32_t)x / (uint32_t)d4);
+                    const float4 d = *(const float4 *)(sv + row * LD + (x - row * d4) * 4);
+                    strange |= !isfinite(d.x) || !isfinite(d.y) || !isfinite(d.z) || !isfinite(d.w);
+                }
+            }
+            strange = __syncthreads_or(strange);
+            if (strange) {  // a value that a row does not see must not meet its zero
                 for (int k = 0; k < kKeys; ++k)
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
@@ -235,12 +257,12 @@ __global__ void __launch_bounds__(kRowsThreads) attention_rows_kernel(PromptPara
     }
 }
 
-template <typename T, int ND>
-int launch_rows(const PromptParams &p, int dev, int sms, cudaStream_t st) {
+template <typename T, int ND, bool VEC>
+int launch_rows(const PromptParams &p, int dev, cudaStream_t st) {
     using S = RowsShape<T, ND>;
     static std::atomic<bool> set[64];
     if (!set[dev].load()) {
-        const cudaError_t e = cudaFuncSetAttribute(attention_rows_kernel<T, ND>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+        const cudaError_t e = cudaFuncSetAttribute(attention_rows_kernel<T, ND, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
         if (e != cudaSuccess) {
             note_cuda_error((int)e);
             return SPEC_ECUDA;
@@ -250,17 +272,17 @@ int launch_rows(const PromptParams &p, int dev, int sms, cudaStream_t st) {
     // row tiles at most: every request's last one may be partial
     const int64_t tiles = ((int64_t)p.n_q * p.group + S::kRows - 1) / S::kRows + p.B;
     const dim3 grid((unsigned)(tiles < 1 << 20 ? tiles : 1 << 20), p.H);
-    attention_rows_kernel<T, ND><<<grid, kRowsThreads, S::kBytes, st>>>(p);
+    attention_rows_kernel<T, ND, VEC><<<grid, kRowsThreads, S::kBytes, st>>>(p);
     return launch_status();
 }
 
-template <typename T>
-int launch_rows_any(const PromptParams &p, int dev, int sms, cudaStream_t st) {
-    if (p.D <= 64) return launch_rows<T, 2>(p, dev, sms, st);
-    if (p.D <= 96) return launch_rows<T, 3>(p, dev, sms, st);
-    if (p.D <= 128) return launch_rows<T, 4>(p, dev, sms, st);
-    if (p.D <= 192) return launch_rows<T, 6>(p, dev, sms, st);
-    return launch_rows<T, 8>(p, dev, sms, st);
+template <typename T, bool VEC>
+int launch_rows_any(const PromptParams &p, int dev, cudaStream_t st) {
+    if (p.D <= 64) return launch_rows<T, 2, VEC>(p, dev, st);
+    if (p.D <= 96) return launch_rows<T, 3, VEC>(p, dev, st);
+    if (p.D <= 128) return launch_rows<T, 4, VEC>(p, dev, st);
+    if (p.D <= 192) return launch_rows<T, 6, VEC>(p, dev, st);
+    return launch_rows<T, 8, VEC>(p, dev, st);
 }
 
 }  // namespace
@@ -336,7 +358,8 @@ extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v
     const cudaStream_t st = (cudaStream_t)cuda_stream;
     if (esz == 2) {
         rc = launch_prompt_tc(p, dev, sms, st);
-        return rc == SPEC_EUNSUPPORTED ? launch_rows_any<uint16_t>(p, dev, sms, st) : rc;
+        return rc == SPEC_EUNSUPPORTED ? launch_rows_any<uint16_t, false>(p, dev, st) : rc;
     }
-    return launch_rows_any<float>(p, dev, sms, st);
+    const bool vec = !(((uintptr_t)k | (uintptr_t)v) & 15) && !((ld_k | ld_v) & 3);  // copies of 16 bytes
+    return vec ? launch_rows_any<float, true>(p, dev, st) : launch_rows_any<float, false>(p, dev, st);
 }

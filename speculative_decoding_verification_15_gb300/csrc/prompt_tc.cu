@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t slot = (int64_t)x.part * p.n_q * p.Hq + row;  // of a part's result
             uint16_t *dst = (uint16_t *)p.out + row * p.D;
             float *part_o = whole ? nullptr : p.part_o + slot * p.D;
-            float odd = 0.f;  // stays 0 while everything is finite
+            float odd4[4] = {0.f, 0.f, 0.f, 0.f};  // stay 0 while everything is finite
 #pragma unroll
             for (int c0 = 0; c0 < NP * 64; c0 += 64) {
                 if (!whole && todo == 0) break;
@@ -829,8 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         const float f = todo > 0 ? __uint_as_float(o[c + e]) * inv : 0.f, g = todo > 0 ? __uint_as_float(o[c + e + 1]) * inv : 0.f;
-                        odd = fmaf(f, 0.f, odd);
-                        odd = fmaf(g, 0.f, odd);
+                        odd4[e & 2] = fmaf(f, 0.f, odd4[e & 2]);
+                        odd4[(e & 2) + 1] = fmaf(g, 0.f, odd4[(e & 2) + 1]);
                         w[e / 2] = pack_bf16x2(f, g);
                     }
                     if (!mine) continue;
@@ -845,6 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            const float odd = (odd4[0] + odd4[1]) + (odd4[2] + odd4[3]);
             if (mine && !whole) {
                 p.part_ml[slot] = make_float2(ref, sum);
                 if (x.part == 0)  // the places that this request has no part for

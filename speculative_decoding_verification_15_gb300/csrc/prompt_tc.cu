@@ -713,16 +713,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // weights, so that registers hold half a row besides what is in flight.
                 const bool partly = j0 + kKeys - 1 > wp0 || (p.window > 0 && j0 <= wp1 - p.window && j0 + kKeys > p.sinks);
                 const int hi = pos - j0, lo = p.window > 0 && pos >= 0 ? pos - p.window - j0 : -1, sinks = p.sinks - j0;
-                auto mask = [&](auto &s, int c0) {  // of columns c0 .., those the row does not see
-                    if (partly) {
+                auto mask = [&](uint32_t (&s)[64], int c0) {  // of columns c0 .., those the row does not see
 #pragma unroll
-                        for (int c = 0; c < (int)(sizeof(s) / 4); c += 32) {
-                            const int d = c0 + c;
-                            const uint32_t seen = bits_below(hi + 1 - d) & (~bits_below(lo + 1 - d) | bits_below(sinks - d));
+                    for (int c = 0; c < 64; c += 32) {
+                        const int d = c0 + c;
+                        const uint32_t seen = bits_below(hi + 1 - d) & (~bits_below(lo + 1 - d) | bits_below(sinks - d));
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(seen >> e & 1)) s[c + e] = 0xff800000u;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen >> e & 1)) s[c + e] = 0xff800000u;
                     }
                 };
                 // four chains: two warps a scheduler hide little of an instruction's latency
@@ -739,11 +737,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld<64>(tS + 64, s2);
                     tmem_wait_ld();
                     tmem_ld<64>(tS, s);
-                    mask(s2, 64);
+                    if (partly) {
+                        mask(s2, 64);
+#pragma unroll
+                        for (int c = 0; c < 64; c += 16) tmem_st16(tS + 64 + c, s2 + c);  // for the second reading
+                    }
                     maxima(s2);
                 }
                 tmem_wait_ld();
-                mask(s, 0);
+                if (partly) {
+                    mask(s, 0);
+                    tmem_wait_st();
+                }
                 maxima(s);
                 const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
                 const bool moves = top > m + kRefStep;  // also from -inf
@@ -792,7 +797,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 weights(s + 32, tS + 16);
                 let_go(0);
                 tmem_wait_ld();
-                mask(s2, 64);
                 weights(s2, tS + 32);
                 weights(s2 + 32, tS + 48);
                 // wide: the next S may be there before this tile's products are, and a barrier's
@@ -814,8 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint16_t *dst = (uint16_t *)p.out + row * p.D;
             float *part_o = whole ? nullptr : p.part_o + slot * p.D;
             float odd4[4] = {0.f, 0.f, 0.f, 0.f};  // stay 0 while everything is finite
-#pragma unroll
-            for (int c0 = 0; c0 < NP * 64; c0 += 64) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < p.D; c0 += 64) {
                 if (!whole && todo == 0) break;
                 uint32_t o[64];
                 if (todo > 0) {

@@ -229,8 +229,7 @@ template <int NT>
 int launch(const PlanParams &p, int ctas, size_t smem, int dev, cudaStream_t st) {
     static std::atomic<bool> set[64];
     if (!set[dev].load()) {
-        cudaError_t e = cudaFuncSetAttribute(page_plan_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 13 * SPEC_MAX_BATCH + 64);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(page_plan_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 13 * SPEC_MAX_BATCH + 64);
         if (e != cudaSuccess) {
             note_cuda_error((int)e);
             return SPEC_ECUDA;
@@ -303,7 +302,7 @@ extern "C" int spec_kv_plan(int32_t *free_pages, int32_t *free_count, int num_pa
     // two calls for 4096 requests, 110000 and 750000 tokens: 60 us with the rows in the cluster's own
     // CTAs, 44 apart
     p.rows_apart = n_out > 16384;
-    rc = launch<1024>(p, B <= 1024 ? 4 : 16, smem, dev, st);
+    rc = launch<1024>(p, B <= 1024 ? 4 : 8, smem, dev, st);
     if (rc || !p.rows_apart) return rc;
     constexpr int each = kRowsThreads * kRowsEach;
     page_rows_kernel<<<(n_out + each - 1) / each, kRowsThreads, 0, st>>>(p);

@@ -23,7 +23,8 @@
 // without a counter.
 //
 // What a row does not see has weight 0, but 0 times a NaN or an infinity is NaN: a row whose
-// output is not finite is computed again over its visible keys alone.
+// output is not finite, where a hidden value is not either, is computed again over its visible
+// keys alone.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -359,40 +360,64 @@ __device__ __forceinline__ void store_v8(void *dst, const uint32_t *w) {  // 32-
                  : "memory");
 }
 
-// A row's output again, over its visible keys of the item's tiles alone (one warp; its
-// reference and sum are right as they are: masked scores never enter them).  Stops once
-// every column is NaN.
+// Whether a value that the row does not see, in the item's tiles, is not finite (one warp).
+__device__ __forceinline__ bool hidden_strange(const PromptParams &p, const Item &x, const Tiles::Sub &sub, int pos, int lane) {
+    bool found = false;
+    for (int i = x.i0; i < x.i1; ++i) {
+        if (!sub.active(i)) continue;
+        const int j0 = x.t.tile(i) * kKeys, j1 = j0 + kKeys - 1;
+        if (j1 <= pos && (p.window == 0 || j0 > pos - p.window || j1 < p.sinks)) continue;  // it sees them all
+        for (int j = j0 + lane; j <= j1 && x.key0 + j < p.n_k; j += 32) {
+            if (visible(p, pos, j)) continue;
+            const uint4 *v = (const uint4 *)((const uint16_t *)p.v + (int64_t)(x.key0 + j) * p.ld_v + (int64_t)x.h * p.D);
+            for (int c = 0; c < p.D / 8; ++c) {
+                const uint4 y = v[c];
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) found |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+            }
+        }
+    }
+    return __any_sync(0xffffffffu, found);
+}
+
+// A row's output again, over its visible keys of the item's tiles alone, four at a time (one
+// warp; its reference and sum are right as they are: masked scores never enter them).  Stops
+// once every column is NaN.
 __device__ __forceinline__ void repair_row(const PromptParams &p, const Item &x, const Tiles::Sub &sub, int token, int head, float ref,
                                            float inv, int lane) {
-    constexpr int kMost = SPEC_KV_MAX_HEAD_DIM / 32;
-    const uint16_t *q = (const uint16_t *)p.q + (int64_t)(x.row0 + token) * p.ld_q + (int64_t)head * p.D;
-    float a[kMost], o[kMost];
-#pragma unroll
-    for (int c = 0; c < kMost; ++c) {
-        a[c] = c * 32 + lane < p.D ? ld_elem<2>(q, c * 32 + lane) : 0.f;
-        o[c] = 0.f;
-    }
+    constexpr int kMost = SPEC_KV_MAX_HEAD_DIM / 32, kAtOnce = 4;
     const int pos = x.off + token;
+    if (!hidden_strange(p, x, sub, pos, lane)) return;
+    const uint16_t *q = (const uint16_t *)p.q + (int64_t)(x.row0 + token) * p.ld_q + (int64_t)head * p.D;
+    float o[kMost];
+#pragma unroll
+    for (int c = 0; c < kMost; ++c) o[c] = 0.f;
     bool some = true;  // a column is not NaN yet
     for (int i = x.i0; i < x.i1 && some; ++i) {
         if (!sub.active(i)) continue;
         const int j0 = x.t.tile(i) * kKeys, end = min(j0 + kKeys, pos + 1);
-        for (int j = j0; j < end && some; ++j) {
-            if (!visible(p, pos, j)) continue;
-            const int64_t row = (int64_t)(x.key0 + j);
-            const uint16_t *k = (const uint16_t *)p.k + row * p.ld_k + (int64_t)x.h * p.D;
-            const uint16_t *v = (const uint16_t *)p.v + row * p.ld_v + (int64_t)x.h * p.D;
-            float s = 0.f;
+        for (int j = j0; j < end && some; j += kAtOnce) {
+            float w[kAtOnce];
 #pragma unroll
-            for (int c = 0; c < kMost; ++c)
-                if (c * 32 + lane < p.D) s += a[c] * ld_elem<2>(k, c * 32 + lane);
-            s = warp_sum(s);
-            const float w = ex2_approx(fmaf(s, p.scale_log2, -ref)) * inv;
+            for (int k = 0; k < kAtOnce; ++k) {
+                float s = 0.f;
+                if (j + k < end) {
+                    const uint16_t *key = (const uint16_t *)p.k + (int64_t)(x.key0 + j + k) * p.ld_k + (int64_t)x.h * p.D;
+                    for (int c = lane; c < p.D; c += 32) s += ld_elem<2>(q, c) * ld_elem<2>(key, c);
+                }
+                w[k] = s;
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) w[k] = ex2_approx(fmaf(warp_sum(w[k]), p.scale_log2, -ref)) * inv;
             bool finite = false;
 #pragma unroll
             for (int c = 0; c < kMost; ++c)
                 if (c * 32 + lane < p.D) {
-                    o[c] = fmaf(w, ld_elem<2>(v, c * 32 + lane), o[c]);
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k)
+                        if (j + k < end && visible(p, pos, j + k))
+                            o[c] = fmaf(w[k], ld_elem<2>((const uint16_t *)p.v + (int64_t)(x.key0 + j + k) * p.ld_v + (int64_t)x.h * p.D, c * 32 + lane), o[c]);
                     finite |= !isnan(o[c]);
                 }
             some = __any_sync(0xffffffffu, finite);

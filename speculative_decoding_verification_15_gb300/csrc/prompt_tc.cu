@@ -180,7 +180,7 @@ struct Finder {
     // about `unit` tiles, so that all cost alike: the unit is the one of six whose rounds over
     // the CTAs take least.  Returns the number of items.
     __device__ __forceinline__ int64_t cut(const PromptParams &p, int ctas) {
-        constexpr int kFixed = 3;  // tiles that an item's start and end cost
+        constexpr int kFixed = 6;  // tiles that an item's start and end cost
         int tiles[kEach];
         int64_t all = 0;
 #pragma unroll
@@ -918,12 +918,20 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptP
         for (int c0 = 0; c0 < p.D; c0 += 128) {
             const int c = c0 + lane * 4;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = 0; k < p.parts; ++k) {
-                const float w = __shfl_sync(0xffffffffu, weight, k);
-                if (w == 0.f || c >= p.D) continue;  // 0: nothing is there, or it does not count
-                const float4 y = __ldcs((const float4 *)(p.part_o + (k * all + row) * p.D + c));
-                o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
+            const float *src = p.part_o + row * p.D + c;
+            for (int k0 = 0; k0 < p.parts; k0 += 4) {  // four loads at a time
+                float4 y[4];
+                float w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, weight, (k0 + k) & 31);
+                    w[k] = k0 + k < p.parts && c < p.D ? wk : 0.f;  // 0: nothing is there, or it does not count
+                    if (w[k] != 0.f) y[k] = __ldcs((const float4 *)(src + (k0 + k) * all * p.D));
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (w[k] != 0.f)
+                        o = make_float4(fmaf(w[k], y[k].x, o.x), fmaf(w[k], y[k].y, o.y), fmaf(w[k], y[k].z, o.z), fmaf(w[k], y[k].w, o.w));
             }
             if (c < p.D) *(uint2 *)((uint16_t *)p.out + row * p.D + c) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         }

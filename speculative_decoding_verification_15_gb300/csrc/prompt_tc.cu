@@ -326,7 +326,9 @@ struct Finder {
 
 // ------------------------------------------------------------------ shared memory
 // Heads of up to 128 columns (NP panels of 64): two row tiles, whose S and O fill tensor
-// memory; a ring of tiles K0 V0 K1 V1 ..  Wider heads: O takes half of tensor memory, so one
+// memory; a ring of tiles K0 V0 K1 V1 ..  (Up to 64 columns P
+// would have room beside S and the next S could be computed while the last weights are: 378 us
+// instead of 363 on 8 prompts of 4500 tokens, 16 heads.)  Wider heads: O takes half of tensor memory, so one
 // row tile with two buffers of S, and the next tile's S is computed during the exponentials;
 // the ring holds halves of tiles (64 keys) in the order K0 K1 V0 K2 V1 ..
 template <int NP>
@@ -645,28 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         const uint32_t tS = tm + a * 128, tO = tm + 256 + a * 128;
-                        if (i >= i0 && t.sub[a].active(i)) {
-#pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-                                wait(&sm.p_full[a][part], np[a] & 1);
-                                if (dead) break;
-                                tc_fence_after();
-                                if (elect_one()) {
-                                    const uint64_t v = dv + (uint64_t)((sv % NS) * (SM::kRingBytes >> 4));
-#pragma unroll
-                                    for (int k = part * 4; k < part * 4 + 4; ++k)
-                                        mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
-                                    if (part > 0) mma_commit(&sm.o_full[a]);
-                                }
-                                __syncwarp();
-                            }
-                            if (dead) break;
-                            ++np[a];
-                            ++done[a];
-                        }
-                        if (i + 1 < i1 && t.sub[a].active(i + 1)) {
+                        const bool now = i >= i0 && t.sub[a].active(i), next = i + 1 < i1 && t.sub[a].active(i + 1);
+                        auto scores = [&] {  // of tile i + 1
                             wait(&sm.full[sk % NS], (sk / NS) & 1);
-                            if (dead) break;
+                            if (dead) return;
                             tc_fence_after();
                             if (elect_one()) {
                                 const uint64_t q = dq + (uint64_t)(a * (NP * kPanel >> 4)), k = dk + (uint64_t)((sk % NS) * (SM::kRingBytes >> 4));
@@ -679,6 +663,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mma_commit(&sm.s_full[a]);
                             }
                             __syncwarp();
+                        };
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            if (now) {
+                                wait(&sm.p_full[a][part], np[a] & 1);
+                                if (dead) break;
+                                tc_fence_after();
+                                if (elect_one()) {
+                                    const uint64_t v = dv + (uint64_t)((sv % NS) * (SM::kRingBytes >> 4));
+#pragma unroll
+                                    for (int k = part * 4; k < part * 4 + 4; ++k)
+                                        mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
+                                    if (part > 0) mma_commit(&sm.o_full[a]);
+                                }
+                                __syncwarp();
+                            }
+                            if (next && part == 1) scores();
+                            if (dead) break;
+                        }
+                        if (dead) break;
+                        if (now) {
+                            ++np[a];
+                            ++done[a];
                         }
                     }
                     if (dead) break;

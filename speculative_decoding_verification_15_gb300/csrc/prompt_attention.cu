@@ -41,45 +41,60 @@ struct RowsShape {
 };
 
 template <typename T, int ND, bool VEC>
-__global__ void __launch_bounds__(kRowsThreads, ND <= 3 ? 2 : 1) attention_rows_kernel(PromptParams p) {
+__global__ void __launch_bounds__(kRowsThreads, ND <= 3 ? 2 : 1) attention_rows_kernel(PromptParams p, int levels) {
     using S = RowsShape<T, ND>;
     constexpr int E = S::kEach, R = S::kRows, LD = S::kStride, LP = kKeys + 4;
     extern __shared__ __align__(16) float rows_smem[];
     float *sq = rows_smem, *sk = sq + R * LD, *sv = sk + kKeys * LD, *sp = sv + kKeys * LD;
-    __shared__ int found[3];
+    __shared__ int found[2];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, D = p.D;
-    if (blockIdx.y == 0) write_prompt_statuses(p, blockIdx.x * kRowsThreads + tid, gridDim.x * kRowsThreads);
-    const int h = blockIdx.y;
+    write_prompt_statuses(p, blockIdx.x * kRowsThreads + tid, gridDim.x * kRowsThreads);
+    // Items, the heads of a row tile side by side.  Where that asks for few that do not exist,
+    // the last row tiles of all requests come first, then the last but one (levels: row tiles
+    // of the longest request): the longest items are not left to the end.  5 prompts of 60 to
+    // 1700 tokens, 10 heads of 80: 487 us so, 570 request after request.
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
-        // the request that holds row tile `item`; its last tiles, the longest, come first
-        if (tid < 32) {
-            int64_t before = 0;
-            int b = -1, tile = 0, tiles_of_b = 0;
-            for (int b0 = 0; b0 < p.B && b < 0; b0 += 32) {
-                const int mine = b0 + lane < p.B ? (int)(((int64_t)load_prompt(p, b0 + lane).n * p.group + R - 1) / R) : 0;
-                int64_t upto = mine;
+        const int64_t which = item / p.H;
+        const int h = (int)(item - which * p.H);
+        int b, tile;
+        if (levels > 0) {
+            const int level = (int)(which / p.B);
+            if (level >= levels) return;
+            b = (int)(which - (int64_t)level * p.B);
+            tile = levels - 1 - level;
+            if (tile >= ((int64_t)load_prompt(p, b).n * p.group + R - 1) / R) continue;
+        } else {
+            // the request that holds row tile `which`; its last tiles, the longest, come first
+            if (tid < 32) {
+                int64_t before = 0;
+                int at = -1, nth = 0;
+                for (int b0 = 0; b0 < p.B && at < 0; b0 += 32) {
+                    const int mine = b0 + lane < p.B ? (int)(((int64_t)load_prompt(p, b0 + lane).n * p.group + R - 1) / R) : 0;
+                    int64_t upto = mine;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += x;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += x;
+                    }
+                    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > which);
+                    if (past) {
+                        const int w = __ffs(past) - 1;
+                        at = b0 + w;
+                        const int tiles = __shfl_sync(0xffffffffu, mine, w);
+                        nth = tiles - 1 - (int)(which - before - (__shfl_sync(0xffffffffu, upto, w) - tiles));
+                    }
+                    before += __shfl_sync(0xffffffffu, upto, 31);
                 }
-                const uint32_t past = __ballot_sync(0xffffffffu, before + upto > item);
-                if (past) {
-                    const int w = __ffs(past) - 1;
-                    b = b0 + w;
-                    tiles_of_b = __shfl_sync(0xffffffffu, mine, w);
-                    tile = (int)(item - before - (__shfl_sync(0xffffffffu, upto, w) - tiles_of_b));
+                if (lane == 0) {
+                    found[0] = at;
+                    found[1] = nth;
                 }
-                before += __shfl_sync(0xffffffffu, upto, 31);
             }
-            if (lane == 0) {
-                found[0] = b;
-                found[1] = tiles_of_b - 1 - tile;
-            }
+            __syncthreads();
+            b = found[0];
+            tile = found[1];
+            if (b < 0) return;
         }
-        __syncthreads();
-        const int b = found[0], tile = found[1];
-        if (b < 0) return;
         const Prompt r = load_prompt(p, b);
         const int first = tile * R, nrows = min(R, r.n * p.group - first);  // the host keeps n * group below 2^31
         const int off = r.m - r.n;  // position of query 0
@@ -271,8 +286,11 @@ int launch_rows(const PromptParams &p, int dev, cudaStream_t st) {
     }
     // row tiles at most: every request's last one may be partial
     const int64_t tiles = ((int64_t)p.n_q * p.group + S::kRows - 1) / S::kRows + p.B;
-    const dim3 grid((unsigned)(tiles < 1 << 20 ? tiles : 1 << 20), p.H);
-    attention_rows_kernel<T, ND, VEC><<<grid, kRowsThreads, S::kBytes, st>>>(p);
+    const int64_t levels = ((int64_t)p.max_query * p.group + S::kRows - 1) / S::kRows;
+    const bool by_level = levels * p.B <= 4 * tiles;
+    const int64_t items = (by_level ? levels * p.B : tiles) * p.H;
+    const unsigned grid = (unsigned)(items < 1 ? 1 : items < 1 << 20 ? items : 1 << 20);
+    attention_rows_kernel<T, ND, VEC><<<grid, kRowsThreads, S::kBytes, st>>>(p, by_level ? (int)levels : 0);
     return launch_status();
 }
 

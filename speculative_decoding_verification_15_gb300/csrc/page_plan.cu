@@ -298,7 +298,8 @@ extern "C" int spec_kv_plan(int32_t *free_pages, int32_t *free_count, int num_pa
     p.n_out = n_out;
     const size_t smem = (size_t)3 * 4 * (B + 1) + B;
     const cudaStream_t st = (cudaStream_t)cuda_stream;
-    if (B <= 256 && n_out <= 2048) return launch<256>(p, 1, smem, dev, st);
+    // one CTA while few tokens are to be placed and few pages can move
+    if (B <= 256 && n_out <= 2048 && (int64_t)B * ld_table <= 32768) return launch<256>(p, 1, smem, dev, st);
     // two calls for 4096 requests, 110000 and 750000 tokens: 60 us with the rows in the cluster's own
     // CTAs, 44 apart
     p.rows_apart = n_out > 16384;

@@ -28,7 +28,7 @@ struct PromptPlan {
     size_t bytes;      // of the parts' results
 };
 inline PromptPlan prompt_plan(int n_q, int n_k, int B, int group, int H, int D, int window, int sinks) {
-    constexpr int kSms = 152, kMostParts = 32, kLeastTiles = 8;
+    constexpr int kSms = 152, kMostParts = 32, kLeastTiles = 8;  // parts: a lane each in the join
     PromptPlan x = {};
     x.tokens = 128 / group;
     x.parts = 1;

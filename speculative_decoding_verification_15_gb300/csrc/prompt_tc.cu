@@ -7,9 +7,9 @@
 //   P = 2^(S - m) rounded to bf16, by 128 threads, a row each, back into S's columns,
 //   O += P V      P from tensor memory, V from shared memory, fp32 in tensor memory.
 // The two row tiles take turns: while one's exponentials are computed the tensor cores work
-// for the other.  The reference m of a row moves only when a score exceeds it by more than
-// 2^8 (its weights then stay below 2^8 and keep their relative precision, sums included), so
-// O is rarely rescaled.
+// for the other.  The reference m of a row moves only when a log2 score exceeds it by more
+// than 8 (weights stay below 2^8 and keep their relative precision, sums included), so O is
+// rarely rescaled.
 //
 // P's rounding to bf16 (2^-8 of each weight at most) is of the size of the output's own; it
 // lets both products run at the bf16 rate.  Everything else is fp32.
@@ -20,7 +20,12 @@
 //
 // Order.  CTAs stay, and items go to them longest first, forth and back (CTA c takes numbers
 // c, 2 n - 1 - c, 2 n + c, ..): costs fall along the order, so the sums are nearly equal
-// without a counter.
+// without a counter.  Where the host sees fewer items than SMs over many keys, items are cut
+// along the keys into parts of equal length, whose sums prompt_join_kernel joins in order.
+//
+// Bound by the chain scores, maximum, exponentials, weights of two warps a scheduler (1710
+// TFLOP/s on one prompt of 16384 tokens with 16 heads of 128 columns, 1.0 PFLOP/s with heads
+// of 64), and with short items by their starts and ends (some 3 us a pair of row tiles).
 //
 // What a row does not see has weight 0, but 0 times a NaN or an infinity is NaN: a row whose
 // output is not finite, where a hidden value is not either, is computed again over its visible
@@ -191,6 +196,7 @@ struct Finder {
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        static_assert(kEach == 4, "tiles of a lane's requests");
         const int longest = __reduce_max_sync(0xffffffffu, max(max(tiles[0], tiles[1]), max(tiles[2], tiles[3])));
         int64_t least = 0, count = 0;
         int unit = 0;
@@ -716,12 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ns = 0;  // tiles of scores
         Item x;
         while (take(x)) {
-            const auto let_item_go = [] {};
             const int first = x.tok0 + a * tokens, have = min(tokens, x.n - first);
-            if (a >= subs || have <= 0) {
-                let_item_go();
-                continue;
-            }
+            if (a >= subs || have <= 0) continue;
             const int list_s1 = x.t.s1, list_step = x.t.w0 - list_s1;  // of the list of tiles
             const auto sub = a == 0 ? x.t.sub[0] : x.t.sub[1];
             const int todo = sub.count(x.i0, x.i1), token = first + tok_r;
@@ -897,7 +899,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 repair_row(p, x, sub, __shfl_sync(0xffffffffu, token, w), x.h * p.group + __shfl_sync(0xffffffffu, head_r, w),
                            __shfl_sync(0xffffffffu, ref, w), __shfl_sync(0xffffffffu, inv, w), lane);
             }
-            let_item_go();
         }
     }
     if (warp == kThreads / 32 - 1) fewer_registers();  // idle: the fourth of its warpgroup
@@ -918,7 +919,8 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptP
     for (int64_t i = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); i < rows; i += step) {
         const int64_t row = (int64_t)r.row0 * p.Hq + i;
         const float2 ml = lane < p.parts ? p.part_ml[lane * all + row] : make_float2(kNegInf, 0.f);
-        const bool some = ml.y != 0.f;  // also NaN
+        const bool some = ml.y != 0.f;  // the part saw something (also NaN); without, it wrote no sums
+        const uint32_t parts = __ballot_sync(0xffffffffu, some);
         const float top = warp_max_nan(some ? ml.x : kNegInf), ref = top == kNegInf ? 0.f : top;
         const float weight = some ? ex2_approx(ml.x - ref) : 0.f, sum = warp_sum(some ? weight * ml.y : 0.f);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -928,17 +930,16 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptP
             const float *src = p.part_o + row * p.D + c;
             for (int k0 = 0; k0 < p.parts; k0 += 4) {  // four loads at a time
                 float4 y[4];
-                float w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float wk = __shfl_sync(0xffffffffu, weight, (k0 + k) & 31);
-                    w[k] = k0 + k < p.parts && c < p.D ? wk : 0.f;  // 0: nothing is there, or it does not count
-                    if (w[k] != 0.f) y[k] = __ldcs((const float4 *)(src + (k0 + k) * all * p.D));
-                }
+                const bool in = c < p.D;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (w[k] != 0.f)
-                        o = make_float4(fmaf(w[k], y[k].x, o.x), fmaf(w[k], y[k].y, o.y), fmaf(w[k], y[k].z, o.z), fmaf(w[k], y[k].w, o.w));
+                    if (in && (parts >> (k0 + k) & 1)) y[k] = __ldcs((const float4 *)(src + (k0 + k) * all * p.D));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float w = __shfl_sync(0xffffffffu, weight, k0 + k);
+                    if (in && (parts >> (k0 + k) & 1))
+                        o = make_float4(fmaf(w, y[k].x, o.x), fmaf(w, y[k].y, o.y), fmaf(w, y[k].z, o.z), fmaf(w, y[k].w, o.w));
+                }
             }
             if (c < p.D) *(uint2 *)((uint16_t *)p.out + row * p.D + c) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         }

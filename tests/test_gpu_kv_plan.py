@@ -159,6 +159,17 @@ def test_captured_rounds():
         keep, new = s.lengths(20)
 
 
+def test_many_pages_of_few_requests():
+    """A few requests with long tables end and start: their pages move without new tokens."""
+    s = State(23, 40, 16, 1200, 100)
+    zero = np.zeros(40, np.int32)
+    s.check(s.call(zero, zero, 3), zero, zero, 3)
+    new = s.g.integers(0, 1200 * 16 + 1, 40).astype(np.int32)
+    new[np.cumsum(-(-new // 16)) > s.count] = 1
+    s.check(s.call(zero, new, 2000), zero, new, 2000)  # most tokens' rows do not fit: those requests fail
+    s.check(s.call(zero, new, int(new.sum())), zero, new, int(new.sum()))
+
+
 def test_another_stream():
     s = State(22, 300, 32, 9, 3000)
     keep, new = s.lengths(20)

@@ -104,6 +104,20 @@ def test_parts_with_spoilt_keys(pkg):
     assert np.isnan(g[30:]).all() and np.isnan(gl[50:]).all()
 
 
+@pytest.mark.parametrize("total", [300, 6000])
+def test_a_visible_nan_of_no_weight(pkg, total):
+    """Its weight underflows, in its tile or as a whole part's: NaN all the same."""
+    x = Inputs(32, [40], [total], 4, 2, 64, BF16)
+    x.q[:] = 8.0
+    x.k[:total // 2] = -100.0
+    x.k[total // 2:] = 0.0
+    x.v[10, 0, 5] = float("nan")
+    got = x.call(pkg)["out"]
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[:, :2, 5] = True
+    assert torch.equal(torch.isnan(got), bad)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_queries_that_see_nothing(pkg, D, dtype):

@@ -424,8 +424,10 @@ __device__ __forceinline__ void repair_row(const PromptParams &p, const Item &x,
                 if (c * 32 + lane < p.D) {
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k)
-                        if (j + k < end && visible(p, pos, j + k))
-                            o[c] = fmaf(w[k], ld_elem<2>((const uint16_t *)p.v + (int64_t)(x.key0 + j + k) * p.ld_v + (int64_t)x.h * p.D, c * 32 + lane), o[c]);
+                        if (j + k < end && visible(p, pos, j + k)) {
+                            const uint16_t *v = (const uint16_t *)p.v + (int64_t)(x.key0 + j + k) * p.ld_v + (int64_t)x.h * p.D;
+                            o[c] = fmaf(w[k], ld_elem<2>(v, c * 32 + lane), o[c]);
+                        }
                     finite |= !isnan(o[c]);
                 }
             some = __any_sync(0xffffffffu, finite);
@@ -941,7 +943,9 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptP
                         o = make_float4(fmaf(w, y[k].x, o.x), fmaf(w, y[k].y, o.y), fmaf(w, y[k].z, o.z), fmaf(w, y[k].w, o.w));
                 }
             }
-            if (c < p.D) *(uint2 *)((uint16_t *)p.out + row * p.D + c) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (c < p.D)
+                *(uint2 *)((uint16_t *)p.out + row * p.D + c) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         }
         if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
     }

@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryParams p, int he
     }
 }
 
-// Many tokens: warps that stay, each taking every W-th token whole.  A lane copies its units
-// of the next token (the last but one, with two ahead) into its own places of shared memory
+// Many tokens: warps that stay, each taking every W-th share of a token.  A lane copies its
+// units of the next share (and the one after, with two ahead) into its own places of shared memory
 // asynchronously while it turns this one's, so a warp's loads never wait for its stores, and
 // needs no barrier but its own copies' completion.  The frequencies of a lane's pairs stay in
 // registers.
@@ -214,24 +214,31 @@ __device__ __forceinline__ void read8(const uint4 *s, float (&x)[8]) {  // place
 }
 
 constexpr int kStreamSmem = 200 * 1024;
-// Bytes of a warp's place for one token: a lane's units, two groups of 8 columns each.
-__host__ __device__ inline int stream_slot(int heads, int units, int esz) { return (heads * units + 31) / 32 * 2 * 32 * 8 * esz; }
+// Units of a share of a token (all are full warps but the last), and the bytes of a warp's
+// place for one: a lane's units, two groups of 8 columns each.
+__host__ __device__ inline int share_units(int heads, int units, int shares) {
+    return ((heads * units + shares - 1) / shares + 31) / 32 * 32;
+}
+__host__ __device__ inline int stream_slot(int heads, int units, int shares, int esz) {
+    return share_units(heads, units, shares) * 2 * 8 * esz;
+}
 
 template <typename T, bool ADJ>
-__global__ void __launch_bounds__(512) rotary_stream_kernel(RotaryParams p, int stages) {
+__global__ void __launch_bounds__(512) rotary_stream_kernel(RotaryParams p, int stages, int shares) {
     extern __shared__ __align__(16) uint8_t stream_smem[];
     __shared__ float4 turns[16][4][kMaxPairs / 8];
     constexpr int V = sizeof(T) / 2;  // 16-byte words of 8 columns
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int turning = p.pairs / 8, units = turning + (p.D - 2 * p.pairs) / 8;
-    const int heads = p.heads[0] + p.heads[1], mine = (heads * units - lane + 31) / 32;
-    const int slot = stream_slot(heads, units, sizeof(T));
+    const int heads = p.heads[0] + p.heads[1], per = share_units(heads, units, shares);
+    const int slot = stream_slot(heads, units, shares, sizeof(T));
     uint4 *place = (uint4 *)(stream_smem + (size_t)warp * stages * slot) + lane;
     const int step_h = 32 / units, step_u = 32 - step_h * units;
-    auto each_unit = [&](auto f) {  // of the lane: f(number, head, unit)
-        int h = lane / units, u = lane - h * units;
-        for (int j = 0; j < mine; ++j) {
-            f(j, h, u);
+    auto each_unit = [&](int share, auto f) {  // of the lane: f(whether it is the first, head, unit)
+        int i = share * per + lane, h = i / units, u = i - h * units;
+        const int end = min(heads * units, (share + 1) * per);
+        for (bool start = true; i < end; i += 32, start = false) {
+            f(start, h, u);
             h += step_h;
             u += step_u;
             if (u >= units) {
@@ -240,11 +247,13 @@ __global__ void __launch_bounds__(512) rotary_stream_kernel(RotaryParams p, int 
             }
         }
     };
-    auto fetch = [&](int64_t token, int stage) {
-        if (token < p.T) {
+    const int64_t items = (int64_t)p.T * shares;  // (token, share)
+    auto fetch = [&](int64_t item, int stage) {
+        if (item < items) {
+            const int64_t token = item / shares;
             uint32_t at = smem_addr(place) + stage * slot;
             const T *rq = (const T *)p.src[0] + token * p.ld_src[0], *rk = (const T *)p.src[1] + token * p.ld_src[1] - (int64_t)p.heads[0] * p.D;
-            each_unit([&](int, int h, int u) {
+            each_unit((int)(item - token * shares), [&](bool, int h, int u) {
                 const Unit x = unit_at<T>(p, u, turning, units);
                 const T *src = (h < p.heads[0] ? rq : rk) + (int64_t)h * p.D + x.c0;
 #pragma unroll
@@ -275,9 +284,10 @@ __global__ void __launch_bounds__(512) rotary_stream_kernel(RotaryParams p, int 
     for (int i = 0; i < stages - 1; ++i) fetch(first + i * step, i);
     const bool fixed = step_u == 0;  // a lane's units are one of every head it visits
     int stage = 0;
-    for (int64_t token = first; token < p.T; token += step) {
-        fetch(token + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
-        __syncwarp();  // the last token's turns have been read
+    for (int64_t item = first; item < items; item += step) {
+        const int64_t token = item / shares;
+        fetch(item + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+        __syncwarp();  // the last item's turns have been read
 #pragma unroll
         for (int i = 0; i < kPairsEach; ++i) {
             const int k = lane + 32 * i;
@@ -293,14 +303,14 @@ __global__ void __launch_bounds__(512) rotary_stream_kernel(RotaryParams p, int 
         const uint4 *at = (const uint4 *)((const uint8_t *)place + stage * slot);
         T *wq = (T *)p.dst[0] + token * p.ld_dst[0], *wk = (T *)p.dst[1] + token * p.ld_dst[1] - (int64_t)p.heads[0] * p.D;
         float c[8], d[8];
-        each_unit([&](int j, int h, int u) {
+        each_unit((int)(item - token * shares), [&](bool start, int h, int u) {
             const Unit x = unit_at<T>(p, u, turning, units);
             T *dst = (h < p.heads[0] ? wq : wk) + (int64_t)h * p.D + x.c0;
             float a[8], b[8], y[8], z[8];
             read8<T>(at, a);
             if (x.turns) {
                 read8<T>(at + V * 32, b);
-                if (!fixed || j == 0)
+                if (!fixed || start)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float4 f = turns[warp][i][u];
@@ -356,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) rotary_any_kernel(RotaryParams p) {
 }
 
 template <typename T, bool ADJ>
-int launch_stream(const RotaryParams &p, int sms, int dev, int stages, int warps, int slot, cudaStream_t st) {
+int launch_stream(const RotaryParams &p, int sms, int dev, int stages, int shares, int warps, int slot, cudaStream_t st) {
     static std::atomic<bool> set[64];
     if (!set[dev].load()) {
         const cudaError_t e = cudaFuncSetAttribute(rotary_stream_kernel<T, ADJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
@@ -366,7 +376,7 @@ int launch_stream(const RotaryParams &p, int sms, int dev, int stages, int warps
         }
         set[dev].store(true);
     }
-    rotary_stream_kernel<T, ADJ><<<sms, warps * 32, warps * stages * slot, st>>>(p, stages);
+    rotary_stream_kernel<T, ADJ><<<sms, warps * 32, warps * stages * slot, st>>>(p, stages, shares);
     return launch_status();
 }
 
@@ -426,19 +436,24 @@ extern "C" int spec_rotary(const void *q, const void *k, int dtype, int64_t ld_q
         return launch_status();
     }
     const int units = pairs / 8 + (head_dim - 2 * pairs) / 8;
-    // many tokens, three places for each of 8 to 16 warps in shared memory (two where rows are long)
-    if (stream_slot(heads, units, esz) * 2 * 4 <= kStreamSmem && n_tokens >= 16 * sms) {
-        const int slot = stream_slot(heads, units, esz), stages = slot * 3 * 8 <= kStreamSmem ? 3 : 2;
+    // Many tokens, whole or in shares so small that 16 warps have two places each in shared
+    // memory (9000 tokens of 72 heads: 61 us in halves, 76 whole; 16411 of 40: 57 and 61), three
+    // where that leaves 16 warps.
+    int shares = 1;
+    while (shares < 4 && stream_slot(heads, units, shares, esz) * 2 * 16 > kStreamSmem) shares *= 2;
+    const int slot = stream_slot(heads, units, shares, esz);
+    if (slot * 2 * 4 <= kStreamSmem && n_tokens >= 16 * sms) {
+        const int stages = slot * 3 * 16 <= kStreamSmem ? 3 : 2;
         const int fit = kStreamSmem / (slot * stages), warps = fit < 16 ? fit : 16;
-        if (esz == 2 && adjacent) return launch_stream<uint16_t, true>(p, sms, dev, stages, warps, slot, st);
-        if (esz == 2) return launch_stream<uint16_t, false>(p, sms, dev, stages, warps, slot, st);
-        if (adjacent) return launch_stream<float, true>(p, sms, dev, stages, warps, slot, st);
-        return launch_stream<float, false>(p, sms, dev, stages, warps, slot, st);
+        if (esz == 2 && adjacent) return launch_stream<uint16_t, true>(p, sms, dev, stages, shares, warps, slot, st);
+        if (esz == 2) return launch_stream<uint16_t, false>(p, sms, dev, stages, shares, warps, slot, st);
+        if (adjacent) return launch_stream<float, true>(p, sms, dev, stages, shares, warps, slot, st);
+        return launch_stream<float, false>(p, sms, dev, stages, shares, warps, slot, st);
     }
     // as many heads a CTA as its threads take in one go, in equal shares; with few tokens fewer
     const int groups = kThreads / units / kTokens;
-    const int most = groups * (esz == 2 ? kHeadsEach<uint16_t> : kHeadsEach<float>), shares = (heads + most - 1) / most;
-    int each = (heads + shares - 1) / shares;
+    const int most = groups * (esz == 2 ? kHeadsEach<uint16_t> : kHeadsEach<float>), split = (heads + most - 1) / most;
+    int each = (heads + split - 1) / split;
     while (each > groups && (int64_t)blocks * ((heads + each - 1) / each) < 2 * sms) each = (each + 1) / 2;
     const dim3 grid(blocks, (heads + each - 1) / each);
     if (esz == 2 && adjacent) rotary_kernel<uint16_t, true><<<grid, kThreads, 0, st>>>(p, each);

@@ -300,8 +300,8 @@ extern "C" int spec_kv_plan(int32_t *free_pages, int32_t *free_count, int num_pa
     const cudaStream_t st = (cudaStream_t)cuda_stream;
     // one CTA while few tokens are to be placed and few pages can move
     if (B <= 256 && n_out <= 2048 && (int64_t)B * ld_table <= 32768) return launch<256>(p, 1, smem, dev, st);
-    // two calls for 4096 requests, 110000 and 750000 tokens: 60 us with the rows in the cluster's own
-    // CTAs, 44 apart
+    // Two calls for 4096 requests, 110000 and 750000 tokens: 60 us with the rows in the cluster's
+    // own CTAs (16 of them), 44 apart; 47 with clusters of 8, the portable size.
     p.rows_apart = n_out > 16384;
     rc = launch<1024>(p, B <= 1024 ? 4 : 8, smem, dev, st);
     if (rc || !p.rows_apart) return rc;

@@ -421,7 +421,7 @@ def _i32_rows(t, device):
     return _as_i32(t, device)
 
 
-PROMPT_SPLIT_KEYS = 2048  # calls with fewer keys need no workspace
+PROMPT_SPLIT_KEYS = {torch.bfloat16: 2048, torch.float32: 384}  # calls with fewer keys need no workspace
 
 
 @_on_its_stream
@@ -439,9 +439,9 @@ def prompt_attention(q, k, v, cu_query, max_query: int, cu_key=None, scale: floa
     cu_query = _i32(cu_query, dev)
     status = torch.empty(max(0, cu_query.numel() - 1), dtype=_I32, device=dev)
     ws, nbytes = None, 0
-    if k.shape[0] >= PROMPT_SPLIT_KEYS and q.dtype is torch.bfloat16 and k.dim() == 3:
+    if k.dim() == 3 and k.shape[0] >= PROMPT_SPLIT_KEYS.get(q.dtype, 0):
         nbytes = binding.spec_prompt_attention_workspace_size(n, k.shape[0], status.numel(), heads, k.shape[1], dim,
-                                                              binding.SPEC_BF16, window, sinks)
+                                                              binding._dtype_code(q), window, sinks)
         if nbytes:  # from the allocator in stream order: calls share none, a graph keeps its own
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     binding._prompt(q, k, v, cu_query, max_query, _i32(cu_key, dev), dim ** -0.5 if scale is None else scale, window, sinks,

@@ -54,8 +54,8 @@ __global__ void __launch_bounds__(kRowsThreads, ND <= 3 ? 2 : 1) attention_rows_
     // of the longest request): the longest items are not left to the end.  5 prompts of 60 to
     // 1700 tokens, 10 heads of 80: 487 us so, 570 request after request.
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
-        const int64_t which = item / p.H;
-        const int h = (int)(item - which * p.H);
+        const int64_t whole = item / p.parts, which = whole / p.H;
+        const int part = (int)(item - whole * p.parts), h = (int)(whole - which * p.H);
         int b, tile;
         if (levels > 0) {
             const int level = (int)(which / p.B);
@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kRowsThreads, ND <= 3 ? 2 : 1) attention_rows_
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         auto arrived = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };  // all but the last one sent
-        if (span.count > 0) load_tile(sk, p.k, p.ld_k, span.tile(0) * kKeys);
-        for (int i = 0; i < span.count; ++i) {
+        const int i0 = (int)((int64_t)span.count * part / p.parts), i1 = (int)((int64_t)span.count * (part + 1) / p.parts);
+        if (i0 < i1) load_tile(sk, p.k, p.ld_k, span.tile(i0) * kKeys);
+        for (int i = i0; i < i1; ++i) {
             const int j0 = span.tile(i) * kKeys;
             const bool masked = j0 + kKeys - 1 > pos0 || (p.window > 0 && j0 <= pos1 - p.window && j0 + kKeys > p.sinks) || nrows < R;
             load_tile(sv, p.v, p.ld_v, j0);  // under way during the scores
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kRowsThreads, ND <= 3 ? 2 : 1) attention_rows_
                     }
             }
             __syncthreads();  // the keys have been read: the next ones' copy runs until the next scores
-            if (i + 1 < span.count) load_tile(sk, p.k, p.ld_k, span.tile(i + 1) * kKeys);
+            if (i + 1 < i1) load_tile(sk, p.k, p.ld_k, span.tile(i + 1) * kKeys);
             else asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -257,6 +258,14 @@ __global__ void __launch_bounds__(kRowsThreads, ND <= 3 ? 2 : 1) attention_rows_
             const int row = ty + 16 * e;
             if (row >= nrows) continue;
             const int2 g = global_row(row);
+            if (p.parts > 1) {  // unnormalised, with the reference and the sum
+                const int64_t slot = ((int64_t)part * p.n_q + g.x) * p.Hq + g.y;
+#pragma unroll
+                for (int c = 0; c < ND; ++c)
+                    if (tx * 2 + 32 * c < D) *(float2 *)(p.part_o + slot * D + tx * 2 + 32 * c) = o[e][c];
+                if (tx == 0) p.part_ml[slot] = make_float2(m[e] == kNegInf ? 0.f : m[e], sum);
+                continue;
+            }
             const float f = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: o is 0
             T *dst = (T *)p.out + ((int64_t)g.x * p.Hq + g.y) * D;
 #pragma unroll
@@ -288,10 +297,11 @@ int launch_rows(const PromptParams &p, int dev, cudaStream_t st) {
     const int64_t tiles = ((int64_t)p.n_q * p.group + S::kRows - 1) / S::kRows + p.B;
     const int64_t levels = ((int64_t)p.max_query * p.group + S::kRows - 1) / S::kRows;
     const bool by_level = levels * p.B <= 4 * tiles;
-    const int64_t items = (by_level ? levels * p.B : tiles) * p.H;
+    const int64_t items = (by_level ? levels * p.B : tiles) * p.H * p.parts;
     const unsigned grid = (unsigned)(items < 1 ? 1 : items < 1 << 20 ? items : 1 << 20);
     attention_rows_kernel<T, ND, VEC><<<grid, kRowsThreads, S::kBytes, st>>>(p, by_level ? (int)levels : 0);
-    return launch_status();
+    const int rc = launch_status();
+    return rc || p.parts == 1 ? rc : launch_prompt_join(p, sizeof(T) == 2, st);
 }
 
 template <typename T, bool VEC>
@@ -310,9 +320,14 @@ using namespace specv;
 
 extern "C" size_t spec_prompt_attention_workspace_size(int n_query, int n_key, int B, int num_query_heads, int num_heads,
                                                        int head_dim, int dtype, int window, int sinks) {
-    if (dtype != SPEC_BF16 || n_query <= 0 || n_key <= 0 || B <= 0 || num_query_heads <= 0 || num_heads <= 0 ||
-        num_query_heads % num_heads || num_query_heads / num_heads > 128 || head_dim <= 0 || window < 0 || sinks < 0)
+    if ((dtype != SPEC_BF16 && dtype != SPEC_F32) || n_query <= 0 || n_key <= 0 || B <= 0 || num_query_heads <= 0 ||
+        num_heads <= 0 || num_query_heads % num_heads || head_dim <= 0 || window < 0 || sinks < 0)
         return 0;
+    if (dtype == SPEC_F32) {
+        const int parts = rows_parts(n_query, n_key, B, num_query_heads / num_heads, num_heads, window, window > 0 ? sinks : 0);
+        return parts > 1 ? (size_t)parts * n_query * num_query_heads * (head_dim + 2) * sizeof(float) : 0;
+    }
+    if (num_query_heads / num_heads > 128) return 0;
     return prompt_plan(n_query, n_key, B, num_query_heads / num_heads, num_heads, head_dim, window, window > 0 ? sinks : 0).bytes;
 }
 
@@ -368,10 +383,10 @@ extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v
     p.scale_log2 = scale * kLog2e;
     p.parts = 1;
     if (need > 0) {
-        const PromptPlan plan = prompt_plan(n_query, n_key, B, group, num_heads, head_dim, p.window, p.sinks);
-        p.parts = plan.parts;
+        p.parts = esz == 2 ? prompt_plan(n_query, n_key, B, group, num_heads, head_dim, p.window, p.sinks).parts
+                           : rows_parts(n_query, n_key, B, group, num_heads, p.window, p.sinks);
         p.part_o = (float *)ws;
-        p.part_ml = (float2 *)((char *)ws + (size_t)plan.parts * n_query * num_query_heads * head_dim * sizeof(float));
+        p.part_ml = (float2 *)((char *)ws + (size_t)p.parts * n_query * num_query_heads * head_dim * sizeof(float));
     }
     const cudaStream_t st = (cudaStream_t)cuda_stream;
     if (esz == 2) {

@@ -15,7 +15,7 @@ struct PromptParams {
     int64_t ld_q, ld_k, ld_v;
     int B, n_q, n_k, max_query, Hq, H, group, D, window, sinks;
     float scale_log2;
-    int parts;        // tensor cores: of an item's tiles at most, joined afterwards if more than one
+    int parts;        // of an item's tiles (tensor cores: at most), joined afterwards if more than one
     float *part_o;    // [parts][n_q * Hq][D]
     float2 *part_ml;  // [parts][n_q * Hq]: reference and sum
 };
@@ -96,6 +96,24 @@ __device__ __forceinline__ Span span_of(const PromptParams &p, int pos0, int pos
 __device__ __forceinline__ bool visible(const PromptParams &p, int pos, int j) {
     return j <= pos && (p.window == 0 || j > pos - p.window || j < p.sinks);
 }
+
+// The parts for fp32 arithmetic: row tiles of 64 rows or more, key tiles of 64, which take so
+// long there that three make a part (64 queries after 8000 keys, 8 heads of 128: 1770 us whole,
+// 89 in parts).
+inline int rows_parts(int n_q, int n_k, int B, int group, int H, int window, int sinks) {
+    constexpr int kSms = 152, kMostParts = 32, kLeastTiles = 3;
+    const int64_t items = ((int64_t)n_q * group / 64 + B) * H;
+    int64_t keys = (int64_t)n_k / B - n_q / B / 2;
+    window = window < (1 << 30) ? window : (1 << 30);
+    if (window > 0 && keys > (int64_t)window + sinks) keys = (int64_t)window + sinks;
+    const int64_t most = keys / 64 / kLeastTiles, want = (4 * kSms + items - 1) / items;
+    if (items >= 2 * kSms || most < 2 || want < 2) return 1;
+    const int64_t parts = want < most ? want : most;
+    return (int)(parts < kMostParts ? parts : kMostParts);
+}
+
+// prompt_join_kernel (prompt_tc.cu), for outputs in bf16 or fp32.
+int launch_prompt_join(const PromptParams &p, bool bf16, cudaStream_t st);
 
 // The tensor-core kernel (prompt_tc.cu); SPEC_EUNSUPPORTED where it cannot serve the call.
 int launch_prompt_tc(const PromptParams &p, int dev, int sms, cudaStream_t st);

@@ -915,6 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ parts of long items
 // A row's parts joined, in order: a warp a row, 4 columns a lane.  Bound by reading them.
 constexpr int kJoinThreads = 256;
+template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptParams p) {
     const Prompt r = load_prompt(p, blockIdx.y);
     const int lane = threadIdx.x & 31;
@@ -944,9 +945,10 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptP
                         o = make_float4(fmaf(w, y[k].x, o.x), fmaf(w, y[k].y, o.y), fmaf(w, y[k].z, o.z), fmaf(w, y[k].w, o.w));
                 }
             }
-            if (c < p.D)
-                *(uint2 *)((uint16_t *)p.out + row * p.D + c) =
-                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (c >= p.D) continue;
+            T *dst = (T *)p.out + row * p.D + c;
+            if (sizeof(T) == 2) *(uint2 *)dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            else *(float4 *)dst = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         }
         if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
     }
@@ -991,13 +993,18 @@ int launch(const PromptParams &p, const CUtensorMap &qmap, const CUtensorMap &km
     }
     prompt_tc_kernel<NP><<<ctas, kThreads, bytes, st>>>(p, qmap, kmap, vmap, tokens, subs);
     const int rc = launch_status();
-    if (rc || p.parts == 1) return rc;
-    const int64_t blocks = ((int64_t)p.max_query * p.Hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-    prompt_join_kernel<<<dim3((unsigned)(blocks < 16384 ? blocks : 16384), p.B), kJoinThreads, 0, st>>>(p);
-    return launch_status();
+    return rc || p.parts == 1 ? rc : launch_prompt_join(p, true, st);
 }
 
 }  // namespace
+
+int launch_prompt_join(const PromptParams &p, bool bf16, cudaStream_t st) {
+    const int64_t blocks = ((int64_t)p.max_query * p.Hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+    const dim3 grid((unsigned)(blocks < 1 ? 1 : blocks < 16384 ? blocks : 16384), p.B);
+    if (bf16) prompt_join_kernel<uint16_t><<<grid, kJoinThreads, 0, st>>>(p);
+    else prompt_join_kernel<float><<<grid, kJoinThreads, 0, st>>>(p);
+    return launch_status();
+}
 
 int launch_prompt_tc(const PromptParams &p, int dev, int sms, cudaStream_t st) {
     if (p.D > 256 || p.group > kRows || p.n_q == 0 || p.n_k == 0) return SPEC_EUNSUPPORTED;

@@ -83,17 +83,19 @@ def test_windows(pkg, new, total, Hq, H, D, window, sinks, dtype):
 @pytest.mark.parametrize("new,total,Hq,H,D", [([33, 5, 0, 100], [5000, 40, 700, 7000], 4, 2, 128), ([70], [4000], 6, 2, 64),
                                               ([1, 2], [9000, 3000], 8, 1, 256), ([40], [2600], 3, 3, 16)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (2500, 300)])
-def test_few_queries_over_many_keys(pkg, new, total, Hq, H, D, window, sinks):
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_few_queries_over_many_keys(pkg, new, total, Hq, H, D, window, sinks, dtype):
     """Items whose tiles are cut into parts, some of them without a tile."""
-    x = Inputs(D, new, total, Hq, H, D, BF16)
-    L = int(x.cu_k[-1])
-    assert pkg.spec_prompt_attention_workspace_size(int(x.cu_q[-1]), L, len(new), Hq, H, D, 0, window, sinks) > 0
+    x = Inputs(D, new, total, Hq, H, D, dtype)
+    L, code = int(x.cu_k[-1]), int(dtype == F32)
+    assert pkg.spec_prompt_attention_workspace_size(int(x.cu_q[-1]), L, len(new), Hq, H, D, code, window, sinks) > 0
     close(x.call(pkg, want_lse=True, window=window, sinks=sinks), x.want(window=window, sinks=sinks))
 
 
-def test_parts_with_spoilt_keys(pkg):
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_parts_with_spoilt_keys(pkg, dtype):
     """A NaN value behind a row, in the tile that it shares with the row's own last key."""
-    x = Inputs(31, [60], [5000], 4, 2, 64, BF16)
+    x = Inputs(31, [60], [5000], 4, 2, 64, dtype)
     want = x.want()
     x.v[4970] = float("nan")
     x.k[4990] = float("nan")
@@ -105,9 +107,10 @@ def test_parts_with_spoilt_keys(pkg):
 
 
 @pytest.mark.parametrize("total", [300, 6000])
-def test_a_visible_nan_of_no_weight(pkg, total):
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_visible_nan_of_no_weight(pkg, total, dtype):
     """Its weight underflows, in its tile or as a whole part's: NaN all the same."""
-    x = Inputs(32, [40], [total], 4, 2, 64, BF16)
+    x = Inputs(32, [40], [total], 4, 2, 64, dtype)
     x.q[:] = 8.0
     x.k[:total // 2] = -100.0
     x.k[total // 2:] = 0.0

@@ -74,7 +74,12 @@ def test_prompt_arguments(binding):
 
 def test_prompt_workspace(binding):
     size = binding.spec_prompt_attention_workspace_size
-    assert size(500, 500, 1, 32, 8, 128, 0) == 0 and size(64, 60000, 1, 32, 8, 128, 1) == 0  # short; fp32
+    assert size(500, 500, 1, 32, 8, 128, 0) == size(500, 500, 1, 32, 8, 128, 1) == 0  # short
+    # what the package does not ask about needs none
+    assert not any(size(n, 2047, 1, 4, 1, 64, 0) or size(n, 383, 1, 4, 1, 64, 1) for n in (1, 100, 383))
+    need = size(64, 60000, 1, 32, 8, 128, 1)
+    assert need > 0 and need % (64 * 32 * 130 * 4) == 0 and size(64, 60000, 1, 32, 8, 128, 1, 300, 4) == 0
+    assert size(64, 60000, 1, 32, 8, 128, 2) == 0
     need = size(64, 60000, 1, 32, 8, 128, 0)
     assert need > 0 and need % (64 * 32 * 130 * 4) == 0
     assert size(64, 60000, 1, 32, 8, 128, 0, 500, 4) == 0  # the window leaves little to cut

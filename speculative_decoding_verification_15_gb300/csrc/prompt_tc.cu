@@ -16,7 +16,7 @@
 //
 // Roles: 8 warps of softmax (4 a row tile), one that issues products, one that copies
 // (tensor maps: queries {D, group, heads, tokens}, keys and values {D, heads, tokens}, in
-// panels of 64 columns, zeros past D), one that finds the items.
+// panels of 64 columns, zeros past D), one that finds the items, one that watches the others.
 //
 // Order.  CTAs stay, and items go to them longest first, forth and back (CTA c takes numbers
 // c, 2 n - 1 - c, 2 n + c, ..): costs fall along the order, so the sums are nearly equal
@@ -44,12 +44,19 @@ namespace {
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kKeys = 128, kRows = 128, kPanel = 128 * 128;  // bytes of 64 columns of 128 rows
 constexpr int kThreads = 384, kSoftWarps = 8;
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kFindWarp = 10;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kFindWarp = 10, kWatchWarp = 11;
 constexpr int kItems = 3;         // places for items that have been told and are not done with
 constexpr int kSortedBatch = 128; // requests whose items are put in order of length
 constexpr float kRefStep = 8.f;   // log2: how far a score may exceed the reference
 
-// Polls: these waits are on the path of every tile.  A wait that ran out anywhere ends the others.
+// What a CTA's waits go by: whether it has failed, and the pieces of tiles copied so far.
+struct Watch {
+    int failed, pieces;
+};
+
+// Polls: these waits are on the path of every tile, so they look at no clock.  One warp watches over
+// the others: two seconds without a copy, and all waits end.  (A wait may last a whole item, and
+// an item of 200 million keys takes longer than that.)
 __device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
@@ -58,19 +65,28 @@ __device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
                  : "memory");
     return done != 0;
 }
-__device__ __forceinline__ bool poll_barrier(uint32_t bar, uint32_t parity, volatile int *failed) {
-    uint64_t t0 = 0;
+__device__ __forceinline__ bool poll_barrier(uint32_t bar, uint32_t parity, volatile Watch *watch) {
     for (uint32_t n = 1;; ++n) {
         if (try_barrier(bar, parity)) return true;
-        if ((n & 255) == 0) {
-            const uint64_t now = global_ns();
-            if (t0 == 0) t0 = now;
-            if (*failed || now - t0 > kWaitNs) {
-                *failed = 1;
-                return false;
-            }
+        if ((n & 255) == 0 && watch->failed) return false;
+    }
+}
+// The watching warp's: done() becomes true, or fails the CTA.
+template <typename F>
+__device__ __forceinline__ bool watch_until(volatile Watch *watch, F done) {
+    uint64_t t0 = 0;
+    int pieces = 0;
+    while (!done()) {
+        const uint64_t now = global_ns();
+        const int seen = watch->pieces;
+        if (t0 == 0 || seen != pieces) t0 = now;
+        pieces = seen;
+        if (watch->failed || now - t0 > kWaitNs) {
+            watch->failed = 1;
+            return false;
         }
     }
+    return true;
 }
 
 // Key tiles of an item, as indexes into a list: tiles [0, s1) and [w0, ...).  A row tile's
@@ -347,10 +363,10 @@ struct PromptShared {
     uint8_t q[kSubs][NP * kPanel];
     uint8_t ring[kStages][kRingBytes];
     uint64_t full[kStages], empty[kStages], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain;
-    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t item_full[kItems], item_empty[kItems], finished;
     Item items[kItems];
     uint32_t tmem;
-    int failed;
+    Watch watch;
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -474,7 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.item_full[i], 1);
             mbar_init(&sm.item_empty[i], 2 + kSoftWarps);
         }
-        sm.failed = 0;
+        mbar_init(&sm.finished, kThreads / 32 - 1);
+        sm.watch.failed = 0;
+        sm.watch.pieces = 0;
         mbar_init_fence();
     }
     if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 512);
@@ -486,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = sm.tmem;  // S of the two row tiles (or its two buffers) at 0 and 128, O from 256
     bool dead = false;            // a wait ran out: end
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!dead && !try_barrier(smem_addr(bar), parity)) dead = !poll_barrier(smem_addr(bar), parity, &sm.failed);
+        if (!dead && !try_barrier(smem_addr(bar), parity)) dead = !poll_barrier(smem_addr(bar), parity, &sm.watch);
         dead = __any_sync(0xffffffffu, dead);
     };
     int told = 0;  // items taken
@@ -554,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (sent >= NS) wait(&sm.empty[slot], (sent / NS - 1) & 1);
                     if (dead) return;
                     if (elect_one()) {
+                        ((volatile Watch *)&sm.watch)->pieces = sent + 1;
                         mbar_arrive_expect_tx(&sm.full[slot], SM::kRingBytes);
                         for (int c = 0; c < NP; ++c)
                             tma_load_3d(sm.ring[slot] + c * SM::kRingPanel, values ? &vmap : &kmap, 64 * c, x.h,
@@ -712,6 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) mma_commit(&sm.drain);
         __syncwarp();
         mbar_wait(&sm.drain, 0, kWaitNs);
+    } else if (warp == kWatchWarp) {
+        fewer_registers();
+        watch_until(&sm.watch, [&] { return mbar_try_wait(&sm.finished, 0); });
     } else if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax
         more_registers();
@@ -904,11 +926,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    if (warp == kThreads / 32 - 1) fewer_registers();  // idle: the fourth of its warpgroup
     tc_fence_before();
+    if (warp != kWatchWarp && lane == 0) mbar_arrive(&sm.finished);
     __syncthreads();
     if (warp == kMmaWarp) tmem_free(tm, 512);
-    if (sm.failed)
+    if (sm.watch.failed)
         for (int b = tid; b < p.B; b += kThreads) p.status[b] = SPEC_STATUS_INTERNAL;
 }
 

@@ -1,0 +1,27 @@
+"""A request over hundreds of millions of keys: a CTA works on it for seconds, and its other
+requests wait that long without a failure."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def test_one_long_request_before_hundreds_of_short_ones():
+    import speculative_decoding_verification_15_gb300 as pkg
+
+    B, m, D = 700, 400_000_000, 16  # more requests than are put in order of length: the long one comes first
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 52 GB")
+    k = torch.full((m + B - 1, 1, D), -30.0, dtype=BF16, device="cuda")
+    v = torch.full((m + B - 1, 1, D), 3.0, dtype=BF16, device="cuda")
+    k[m - 1024:] = 0.0  # the last keys have all the weight
+    v[m - 512:m] = 5.0
+    short = torch.randn((B - 1, 1, D), device="cuda").to(BF16)
+    v[m:] = short
+    q = torch.ones((B, 1, D), dtype=BF16, device="cuda")
+    cu_q = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    cu_k = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), m + cu_q[:B]])
+    got = pkg.prompt_attention(q, k, v, cu_q, 1, cu_key=cu_k)
+    assert (got["status"] == 0).all()
+    assert (got["out"][0] == 4.0).all() and torch.equal(got["out"][1:], short)

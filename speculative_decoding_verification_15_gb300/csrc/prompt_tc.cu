@@ -27,13 +27,17 @@
 // TFLOP/s on one prompt of 16384 tokens with 16 heads of 128 columns, 960 on 8 prompts of 4500
 // with 16 heads of 64), and with short items by their starts and ends (some 3 us a pair of row tiles).
 //
-// What a row does not see has weight 0, but 0 times a NaN or an infinity is NaN: a row whose
-// output is not finite, where a hidden value is not either, is computed again over its visible
-// keys alone.
+// What a row does not see has weight 0, but 0 times a NaN or an infinity is NaN.  A CTA marks its
+// items with a row that is not finite, and does them again when all are done, with care: what is
+// not finite in the values of a tile that hides some key from some row is taken out of it in
+// shared memory before the products.  A third round adds that to the rows that see it.  So such
+// values cost their items' time again, however long their rows are (24571 tokens, 16 heads, NaN
+// behind the last one: 1.7 ms; 1.4 without, 658 when rows were repaired key by key).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "prompt_common.cuh"
 #include "tcgen05.cuh"
@@ -46,6 +50,8 @@ constexpr int kKeys = 128, kRows = 128, kPanel = 128 * 128;  // bytes of 64 colu
 constexpr int kThreads = 384, kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kCopyWarp = 9, kFindWarp = 10, kWatchWarp = 11;
 constexpr int kItems = 3;         // places for items that have been told and are not done with
+constexpr int kMarks = 1024;      // of items to be done again, by their number modulo this
+constexpr int kWorking = kThreads - 32;  // all but the watching warp
 constexpr int kSortedBatch = 128; // requests whose items are put in order of length
 constexpr float kRefStep = 8.f;   // log2: how far a score may exceed the reference
 
@@ -130,6 +136,18 @@ __device__ __forceinline__ Tiles tiles_of(const PromptParams &p, const Item &x, 
         t.count = max(t.count, t.sub[a].e);
     }
     return t;
+}
+
+// Whether some row of the row tiles that visit tile i does not see one of its keys.
+__device__ __forceinline__ bool hides(const PromptParams &p, const Item &x, int tokens, int i) {
+    const int j0 = x.t.tile(i) * kKeys;
+    bool some = false;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const int first = x.tok0 + a * tokens, last = min(x.n, first + tokens) - 1;
+        some |= x.t.sub[a].active(i) && (j0 + kKeys - 1 > x.off + first || (p.window > 0 && j0 <= x.off + last - p.window && j0 + kKeys > p.sinks));
+    }
+    return some;
 }
 
 // ------------------------------------------------------------------ the order of the items
@@ -363,8 +381,9 @@ struct PromptShared {
     uint8_t q[kSubs][NP * kPanel];
     uint8_t ring[kStages][kRingBytes];
     uint64_t full[kStages], empty[kStages], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain;
-    uint64_t item_full[kItems], item_empty[kItems], finished;
+    uint64_t item_full[kItems], item_empty[kItems], finished, raw;
     Item items[kItems];
+    uint32_t redo[kMarks / 32], redo_any;  // items to be done again
     uint32_t tmem;
     Watch watch;
 };
@@ -384,78 +403,78 @@ __device__ __forceinline__ void store_v8(void *dst, const uint32_t *w) {  // 32-
                  : "memory");
 }
 
-// Whether a value that the row does not see, in the item's tiles, is not finite (one warp).
-__device__ __forceinline__ bool hidden_strange(const PromptParams &p, const Item &x, const Tiles::Sub &sub, int pos, int lane) {
-    bool found = false;
-    for (int i = x.i0; i < x.i1; ++i) {
-        if (!sub.active(i)) continue;
-        const int j0 = x.t.tile(i) * kKeys, j1 = j0 + kKeys - 1;
-        if (j1 <= pos && (p.window == 0 || j0 > pos - p.window || j1 < p.sinks)) continue;  // it sees them all
-        for (int j = j0 + lane; j <= j1 && x.key0 + j < p.n_k; j += 32) {
-            if (visible(p, pos, j)) continue;
-            const uint4 *v = (const uint4 *)((const uint16_t *)p.v + (int64_t)(x.key0 + j) * p.ld_v + (int64_t)x.h * p.D);
-            for (int c = 0; c < p.D / 8; ++c) {
-                const uint4 y = v[c];
-                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+// Which of keys j0 .. j0 + 31 have values that are not finite, a bit each, and in `all` those that
+// have nothing but NaN (one warp, a key a lane).
+__device__ __forceinline__ uint32_t strange_keys(const PromptParams &p, const Item &x, int j0, int lane, uint32_t *all) {
+    const int key = x.key0 + j0 + lane;
+    bool some = false, only = true;
+    if (key < p.n_k) {
+        const uint4 *v = (const uint4 *)((const uint16_t *)p.v + (int64_t)key * p.ld_v + (int64_t)x.h * p.D);
+#pragma unroll 2
+        for (int c = 0; c < p.D / 8; ++c) {
+            const uint4 y = v[c];
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) found |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+            for (int e = 0; e < 4; ++e) {
+                some |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                only &= (w[e] & 0x7fffu) > 0x7f80u && (w[e] & 0x7fffffffu) >= 0x7f810000u;
             }
         }
     }
-    return __any_sync(0xffffffffu, found);
+    *all = __ballot_sync(0xffffffffu, some && only);
+    return __ballot_sync(0xffffffffu, some);
 }
 
-// A row's output again, over its visible keys of the item's tiles alone, four at a time (one
-// warp; its reference and sum are right as they are: masked scores never enter them).  Stops
-// once every column is NaN.
-__device__ __forceinline__ void repair_row(const PromptParams &p, const Item &x, const Tiles::Sub &sub, int token, int head, float ref,
-                                           float inv, int lane) {
-    constexpr int kMost = SPEC_KV_MAX_HEAD_DIM / 32, kAtOnce = 4;
-    const int pos = x.off + token;
-    if (!hidden_strange(p, x, sub, pos, lane)) return;
-    const uint16_t *q = (const uint16_t *)p.q + (int64_t)(x.row0 + token) * p.ld_q + (int64_t)head * p.D;
-    float o[kMost];
-#pragma unroll
-    for (int c = 0; c < kMost; ++c) o[c] = 0.f;
-    bool some = true;  // a column is not NaN yet
-    for (int i = x.i0; i < x.i1 && some; ++i) {
-        if (!sub.active(i)) continue;
-        const int j0 = x.t.tile(i) * kKeys, end = min(j0 + kKeys, pos + 1);
-        for (int j = j0; j < end && some; j += kAtOnce) {
-            float w[kAtOnce];
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                float s = 0.f;
-                if (j + k < end) {
-                    const uint16_t *key = (const uint16_t *)p.k + (int64_t)(x.key0 + j + k) * p.ld_k + (int64_t)x.h * p.D;
-                    for (int c = lane; c < p.D; c += 32) s += ld_elem<2>(q, c) * ld_elem<2>(key, c);
-                }
-                w[k] = s;
+// Values of KEYS keys in `panels` panels: what is not finite becomes 0 (one warp).
+template <int KEYS>
+__device__ __forceinline__ void take_out(uint8_t *values, int panels, int lane) {
+#pragma unroll 1
+    for (int w = lane; w < panels * KEYS * 32; w += 32) {
+        uint32_t *two = (uint32_t *)values + w;
+        const uint32_t x = *two, lo = (x & 0x7f80u) == 0x7f80u ? 0u : 0xffffu, hi = (x & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u;
+        if ((lo | hi) != 0xffffffffu) *two = x & (lo | hi);
+    }
+    fence_async_shared();  // the products read them next
+}
+
+// What was taken out of an item's tiles, added to the rows that see it, which have been written (a
+// warp's 32 rows, a lane each, at position pos, -1 for rows that do not count; a weight is
+// positive, so an infinity times it is that infinity).
+__device__ __forceinline__ void put_back(const PromptParams &p, const Item &x, int tokens, const Tiles::Sub &sub, int pos, int lane,
+                                         int64_t row) {
+    const int64_t slot = ((int64_t)x.part * p.n_q * p.Hq + row) * p.D;
+    auto add = [&](int c, float z) {
+        if (p.parts > 1) {
+            p.part_o[slot + c] += z;
+        } else {
+            uint16_t *o = (uint16_t *)p.out + row * p.D + c;
+            *o = (uint16_t)pack_bf16x2(__uint_as_float((uint32_t)*o << 16) + z, 0.f);
+        }
+    };
+    bool gone = false;  // the row is NaN throughout
+#pragma unroll 1
+    for (int t = x.i0 * 4; t < x.i1 * 4; ++t) {  // 32 keys at a time
+        if (!hides(p, x, tokens, t >> 2) || !sub.active(t >> 2)) {
+            t |= 3;
+            continue;
+        }
+        const int j0 = x.t.tile(t >> 2) * kKeys + (t & 3) * 32;
+        uint32_t all;
+#pragma unroll 1
+        for (uint32_t left = strange_keys(p, x, j0, lane, &all); left; left &= left - 1) {
+            const int e = __ffs(left) - 1;
+            const bool sees = !gone && visible(p, pos, j0 + e);
+            if (!__any_sync(0xffffffffu, sees)) continue;  // also keys behind the request's last
+            const bool only = all >> e & 1;
+            gone |= sees && only;
+            const uint16_t *v = (const uint16_t *)p.v + (int64_t)(x.key0 + j0 + e) * p.ld_v + (int64_t)x.h * p.D;
+#pragma unroll 1
+            for (int c = 0; c < p.D; ++c) {
+                const float z = ld_elem<2>(v, c);
+                if (sees && !isfinite(z)) add(c, z);
             }
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) w[k] = ex2_approx(fmaf(warp_sum(w[k]), p.scale_log2, -ref)) * inv;
-            bool finite = false;
-#pragma unroll
-            for (int c = 0; c < kMost; ++c)
-                if (c * 32 + lane < p.D) {
-#pragma unroll
-                    for (int k = 0; k < kAtOnce; ++k)
-                        if (j + k < end && visible(p, pos, j + k)) {
-                            const uint16_t *v = (const uint16_t *)p.v + (int64_t)(x.key0 + j + k) * p.ld_v + (int64_t)x.h * p.D;
-                            o[c] = fmaf(w[k], ld_elem<2>(v, c * 32 + lane), o[c]);
-                        }
-                    finite |= !isnan(o[c]);
-                }
-            some = __any_sync(0xffffffffu, finite);
         }
     }
-    const int64_t row = (int64_t)(x.row0 + token) * p.Hq + head;
-#pragma unroll
-    for (int c = 0; c < kMost; ++c)
-        if (c * 32 + lane < p.D) {
-            if (p.parts > 1) p.part_o[((int64_t)x.part * p.n_q * p.Hq + row) * p.D + c * 32 + lane] = o[c];
-            else ((uint16_t *)p.out)[row * p.D + c * 32 + lane] = (uint16_t)pack_bf16x2(o[c], 0.f);
-        }
 }
 
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
@@ -491,10 +510,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.item_empty[i], 2 + kSoftWarps);
         }
         mbar_init(&sm.finished, kThreads / 32 - 1);
+        mbar_init(&sm.raw, 1);
+        sm.redo_any = 0;
         sm.watch.failed = 0;
         sm.watch.pieces = 0;
         mbar_init_fence();
     }
+    if (tid < kMarks / 32) sm.redo[tid] = 0;
     if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 512);
     tc_fence_before();
     // statuses: a CTA that fails corrects them seconds later, when all have written theirs
@@ -517,96 +539,137 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++told;
         return !dead && x.b >= 0;
     };
+    // Every working warp's items are done.  Whether there is a second round, of the marked items with
+    // care, and a third, in which what was taken out of their tiles is put back.  (What one warp
+    // alone knows, that it ended early, all learn at the barrier.)
+    int round = 0;
+    auto another_round = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.finished);
+        uint32_t ended;
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+            : "=r"(ended)
+            : "r"(dead ? 1u : 0u), "n"(kWorking)
+            : "memory");
+        tc_fence_after();
+        if (__builtin_expect(ended || round == 2 || !((volatile uint32_t &)sm.redo_any), 1)) return false;
+        ++round;
+        return true;
+    };
 
     // Softmax rows live in registers: 256 threads x 224 + 128 x 56 is what 384 were launched with
     // (8 prompts of 4500 tokens, 16 heads of 64: 345 us; 350 with 216 and 72, 356 with 208 and 88).
     if (warp == kFindWarp) {
         // ---------------------------------------------------------------- items
         fewer_registers();
-        Finder f;
-        f.start(p, tokens * subs, lane);
-        const bool cut = p.parts > 1;
-        const int64_t total = cut ? f.cut(p, gridDim.x) : f.total * p.H;
-        for (int64_t round = 0;; ++round) {
-            const int64_t i = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            const bool last = round * gridDim.x >= total;
-            if (i >= total && !last) continue;
-            Item x;
-            x.b = -1;
-            if (!last) {
-                if (cut) {
-                    x = f.find_part(p, i, lane);
-                } else {
-                    const int64_t r = i / p.H;
-                    x = f.find(p, r, lane);
-                    x.h = (int)(i - r * p.H);
-                    x.part = 0;
-                    x.parts = 1;
+        do {
+            Finder f;
+            f.start(p, tokens * subs, lane);
+            const bool cut = p.parts > 1;
+            const int64_t total = cut ? f.cut(p, gridDim.x) : f.total * p.H;
+            uint32_t number = 0;
+            for (int64_t turn = 0;; ++turn) {
+                const int64_t i = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                const bool last = turn * gridDim.x >= total;
+                if (i >= total && !last) continue;
+                if (__builtin_expect(round > 0 && !last, 0)) {
+                    const uint32_t at = number++ % kMarks;
+                    if (!(((volatile uint32_t *)sm.redo)[at / 32] >> (at % 32) & 1)) continue;
                 }
-                x.t = tiles_of(p, x, tokens, subs);
-                x.i0 = (int)((int64_t)x.t.count * x.part / x.parts);
-                x.i1 = (int)((int64_t)x.t.count * (x.part + 1) / x.parts);
+                Item x;
+                x.b = -1;
+                if (!last) {
+                    if (cut) {
+                        x = f.find_part(p, i, lane);
+                    } else {
+                        const int64_t r = i / p.H;
+                        x = f.find(p, r, lane);
+                        x.h = (int)(i - r * p.H);
+                        x.part = 0;
+                        x.parts = 1;
+                    }
+                    x.t = tiles_of(p, x, tokens, subs);
+                    x.i0 = (int)((int64_t)x.t.count * x.part / x.parts);
+                    x.i1 = (int)((int64_t)x.t.count * (x.part + 1) / x.parts);
+                }
+                const int at = told % kItems;
+                if (told >= kItems) wait(&sm.item_empty[at], (told / kItems - 1) & 1);
+                if (dead) break;
+                if (lane == 0) {
+                    sm.items[at] = x;
+                    mbar_arrive(&sm.item_full[at]);
+                }
+                ++told;
+                if (last) break;
             }
-            const int at = told % kItems;
-            if (told >= kItems) wait(&sm.item_empty[at], (told / kItems - 1) & 1);
-            if (dead) break;
-            if (lane == 0) {
-                sm.items[at] = x;
-                mbar_arrive(&sm.item_full[at]);
-            }
-            ++told;
-            if (last) break;
-        }
+        } while (another_round());
     } else if (warp == kCopyWarp) {
         // ---------------------------------------------------------------- copies
         fewer_registers();
-        int sent = 0, nq = 0;
-        Item x;
-        while (take(x)) {
-            const Tiles &t = x.t;
-            if (x.i0 >= x.i1) continue;
-            auto copy_tile = [&](bool values, int i) {
-                const int key = x.key0 + t.tile(i) * kKeys;
-                for (int part = 0; part < SM::kPieces; ++part) {
-                    const int slot = sent % NS;
-                    if (sent >= NS) wait(&sm.empty[slot], (sent / NS - 1) & 1);
-                    if (dead) return;
-                    if (elect_one()) {
-                        ((volatile Watch *)&sm.watch)->pieces = sent + 1;
-                        mbar_arrive_expect_tx(&sm.full[slot], SM::kRingBytes);
-                        for (int c = 0; c < NP; ++c)
-                            tma_load_3d(sm.ring[slot] + c * SM::kRingPanel, values ? &vmap : &kmap, 64 * c, x.h,
-                                        key + part * SM::kRingKeys, &sm.full[slot]);
+        int sent = 0, nq = 0, raws = 0;
+        auto copy_items = [&](auto careful) {
+            Item x;
+            while (take(x)) {
+                const Tiles &t = x.t;
+                if (x.i0 >= x.i1 || (careful && round == 2)) continue;
+                auto copy_tile = [&](bool values, int i) {
+                    const int key = x.key0 + t.tile(i) * kKeys;
+                    const bool care = careful && values && hides(p, x, tokens, i);
+                    for (int part = 0; part < SM::kPieces; ++part) {
+                        const int slot = sent % NS;
+                        if (sent >= NS) wait(&sm.empty[slot], (sent / NS - 1) & 1);
+                        if (dead) return;
+                        if (elect_one()) {
+                            ((volatile Watch *)&sm.watch)->pieces = sent + 1;
+                            uint64_t *bar = care ? &sm.raw : &sm.full[slot];
+                            mbar_arrive_expect_tx(bar, SM::kRingBytes);
+                            for (int c = 0; c < NP; ++c)
+                                tma_load_3d(sm.ring[slot] + c * SM::kRingPanel, values ? &vmap : &kmap, 64 * c, x.h,
+                                            key + part * SM::kRingKeys, bar);
+                        }
+                        __syncwarp();
+                        ++sent;
+                        if (care) {
+                            wait(&sm.raw, raws++ & 1);
+                            if (!dead) take_out<SM::kRingKeys>(sm.ring[slot], NP, lane);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.full[slot]);
+                        }
                     }
-                    __syncwarp();
-                    ++sent;
-                }
-            };
-            copy_tile(false, x.i0);  // the ring is free before the last item's queries are
-            if (dead) break;
-            if (nq > 0) wait(&sm.q_empty, (nq - 1) & 1);
-            if (dead) break;
-            if (elect_one()) {
-                const uint32_t bytes = (uint32_t)tokens * p.group * 128 * NP;
-                const bool one = t.sub[0].count(x.i0, x.i1) > 0, two = t.sub[1].count(x.i0, x.i1) > 0;  // wide: no second one
-                mbar_arrive_expect_tx(&sm.q_full, (one ? bytes : 0) + (two ? bytes : 0));
+                };
+                copy_tile(false, x.i0);  // the ring is free before the last item's queries are
+                if (dead) break;
+                if (nq > 0) wait(&sm.q_empty, (nq - 1) & 1);
+                if (dead) break;
+                if (elect_one()) {
+                    const uint32_t bytes = (uint32_t)tokens * p.group * 128 * NP;
+                    const bool one = t.sub[0].count(x.i0, x.i1) > 0, two = t.sub[1].count(x.i0, x.i1) > 0;  // wide: no second one
+                    mbar_arrive_expect_tx(&sm.q_full, (one ? bytes : 0) + (two ? bytes : 0));
 #pragma unroll
-                for (int a = 0; a < SM::kSubs; ++a)
-                    if (a == 0 ? one : two)
-                        for (int c = 0; c < NP; ++c)
-                            tma_load_4d(sm.q[a] + c * kPanel, &qmap, 64 * c, 0, x.h, x.row0 + x.tok0 + a * tokens, &sm.q_full);
+                    for (int a = 0; a < SM::kSubs; ++a)
+                        if (a == 0 ? one : two)
+                            for (int c = 0; c < NP; ++c)
+                                tma_load_4d(sm.q[a] + c * kPanel, &qmap, 64 * c, 0, x.h, x.row0 + x.tok0 + a * tokens, &sm.q_full);
+                }
+                __syncwarp();
+                ++nq;
+                for (int i = x.i0; i < x.i1 && !dead; ++i) {
+                    if (!kWide && i > x.i0) copy_tile(false, i);
+                    if (kWide && i + 1 < x.i1) copy_tile(false, i + 1);
+                    if (!dead) copy_tile(true, i);
+                }
             }
-            __syncwarp();
-            ++nq;
-            for (int i = x.i0; i < x.i1 && !dead; ++i) {
-                if (!kWide && i > x.i0) copy_tile(false, i);
-                if (kWide && i + 1 < x.i1) copy_tile(false, i + 1);
-                if (!dead) copy_tile(true, i);
-            }
-        }
-        // none of the copies may be in flight when the CTA ends
-        for (int i = max(0, sent - NS); i < sent; ++i) mbar_wait(&sm.full[i % NS], (i / NS) & 1, kWaitNs);
-        if (nq > 0) mbar_wait(&sm.q_full, (nq - 1) & 1, kWaitNs);
+        };
+        do {
+            if (round == 0) copy_items(std::false_type());
+            else copy_items(std::true_type());
+            // none of the copies may be in flight when the CTA ends
+            for (int i = max(0, sent - NS); i < sent; ++i) mbar_wait(&sm.full[i % NS], (i / NS) & 1, kWaitNs);
+            if (nq > 0) mbar_wait(&sm.q_full, (nq - 1) & 1, kWaitNs);
+            if (raws > 0) mbar_wait(&sm.raw, (raws - 1) & 1, kWaitNs);
+        } while (another_round());
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- products
         fewer_registers();
@@ -615,125 +678,130 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dv = smem_desc(smem_addr(sm.ring), SM::kRingPanel, 1024, 2);
         const int steps = p.D / 16;
         int got = 0, nq = 0, np[2] = {0, 0};  // ring slots, query tiles, tiles of weights used
-        Item x;
-        while (take(x)) {
-            const Tiles &t = x.t;
-            const int i0 = x.i0, i1 = x.i1;
-            if (i0 >= i1) continue;
-            int done[2] = {0, 0};
-            wait(&sm.q_full, nq & 1);
-            ++nq;
-            if constexpr (kWide) {
-                for (int i = i0 - 1; i < i1 && !dead; ++i) {
-                    if (i + 1 < i1) {  // S of tile i + 1, in the buffer that the tile's number says
-                        const int buf = (np[0] + (i < i0 ? 0 : 1)) & 1;
-                        for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
-                            const int slot = got % NS;
-                            wait(&sm.full[slot], (got / NS) & 1);
-                            if (dead) break;
-                            tc_fence_after();
-                            if (elect_one()) {
-                                const uint64_t k = dk + (uint64_t)(slot * (SM::kRingBytes >> 4));
-#pragma unroll
-                                for (int s = 0; s < NP * 4; ++s)
-                                    if (s < steps)
-                                        mma_bf16(tm + buf * 128 + part * SM::kRingKeys, dq + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
-                                                 k + (s >> 2) * (SM::kRingPanel >> 4) + (s & 3) * 2, idesc_s, s > 0);
-                                mma_commit(&sm.empty[slot]);
-                                if (part + 1 == SM::kPieces) mma_commit(&sm.s_full[buf]);
-                                if (part + 1 == SM::kPieces && i + 2 == i1) mma_commit(&sm.q_empty);
-                            }
-                            __syncwarp();
-                        }
-                    }
-                    if (i < i0) continue;
-                    for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
-                        const int slot = got % NS;
-                        wait(&sm.full[slot], (got / NS) & 1);
-                        wait(&sm.p_full[np[0] & 1][part], (np[0] >> 1) & 1);
-                        if (dead) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint64_t v = dv + (uint64_t)(slot * (SM::kRingBytes >> 4));
-#pragma unroll
-                            for (int k = 0; k < SM::kRingKeys / 16; ++k)
-                                mma_bf16_ta(tm + 256, tm + (np[0] & 1) * 128 + part * (SM::kRingKeys / 2) + k * 8, v + k * 128, idesc_o,
-                                            i > i0 || part > 0 || k > 0);
-                            mma_commit(&sm.empty[slot]);
-                            if (part + 1 == SM::kPieces) mma_commit(&sm.o_full[0]);
-                        }
-                        __syncwarp();
-                    }
-                    ++np[0];
-                }
-            } else {
-                for (int i = i0 - 1; i < i1 && !dead; ++i) {
-                    // the ring holds K0 V0 K1 V1 ..: tile i's values, then tile i + 1's keys
-                    const int sv = got + 2 * (i - i0) + 1, sk = got + 2 * (i - i0) + 2;
-                    if (i >= i0) wait(&sm.full[sv % NS], (sv / NS) & 1);
-                    tc_fence_after();
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        const uint32_t tS = tm + a * 128, tO = tm + 256 + a * 128;
-                        const bool now = i >= i0 && t.sub[a].active(i), next = i + 1 < i1 && t.sub[a].active(i + 1);
-                        auto scores = [&] {  // of tile i + 1
-                            wait(&sm.full[sk % NS], (sk / NS) & 1);
-                            if (dead) return;
-                            tc_fence_after();
-                            if (elect_one()) {
-                                const uint64_t q = dq + (uint64_t)(a * (NP * kPanel >> 4)), k = dk + (uint64_t)((sk % NS) * (SM::kRingBytes >> 4));
-#pragma unroll
-                                for (int s = 0; s < NP * 4; ++s)
-                                    if (s < steps) {
-                                        const uint64_t at = (s >> 2) * (kPanel >> 4) + (s & 3) * 2;
-                                        mma_bf16(tS, q + at, k + at, idesc_s, s > 0);
-                                    }
-                                mma_commit(&sm.s_full[a]);
-                            }
-                            __syncwarp();
-                        };
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            if (now) {
-                                wait(&sm.p_full[a][part], np[a] & 1);
+        do {
+            Item x;
+            while (take(x)) {
+                const Tiles &t = x.t;
+                const int i0 = x.i0, i1 = x.i1;
+                if (i0 >= i1 || round == 2) continue;
+                int done[2] = {0, 0};
+                wait(&sm.q_full, nq & 1);
+                ++nq;
+                if constexpr (kWide) {
+                    for (int i = i0 - 1; i < i1 && !dead; ++i) {
+                        if (i + 1 < i1) {  // S of tile i + 1, in the buffer that the tile's number says
+                            const int buf = (np[0] + (i < i0 ? 0 : 1)) & 1;
+                            for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
+                                const int slot = got % NS;
+                                wait(&sm.full[slot], (got / NS) & 1);
                                 if (dead) break;
                                 tc_fence_after();
                                 if (elect_one()) {
-                                    const uint64_t v = dv + (uint64_t)((sv % NS) * (SM::kRingBytes >> 4));
+                                    const uint64_t k = dk + (uint64_t)(slot * (SM::kRingBytes >> 4));
 #pragma unroll
-                                    for (int k = part * 4; k < part * 4 + 4; ++k)
-                                        mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
-                                    if (part > 0) mma_commit(&sm.o_full[a]);
+                                    for (int s = 0; s < NP * 4; ++s)
+                                        if (s < steps)
+                                            mma_bf16(tm + buf * 128 + part * SM::kRingKeys, dq + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
+                                                     k + (s >> 2) * (SM::kRingPanel >> 4) + (s & 3) * 2, idesc_s, s > 0);
+                                    mma_commit(&sm.empty[slot]);
+                                    if (part + 1 == SM::kPieces) mma_commit(&sm.s_full[buf]);
+                                    if (part + 1 == SM::kPieces && i + 2 == i1) mma_commit(&sm.q_empty);
                                 }
                                 __syncwarp();
                             }
-                            if (next && part == 1) scores();
+                        }
+                        if (i < i0) continue;
+                        for (int part = 0; part < SM::kPieces && !dead; ++part, ++got) {
+                            const int slot = got % NS;
+                            wait(&sm.full[slot], (got / NS) & 1);
+                            wait(&sm.p_full[np[0] & 1][part], (np[0] >> 1) & 1);
                             if (dead) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                const uint64_t v = dv + (uint64_t)(slot * (SM::kRingBytes >> 4));
+#pragma unroll
+                                for (int k = 0; k < SM::kRingKeys / 16; ++k)
+                                    mma_bf16_ta(tm + 256, tm + (np[0] & 1) * 128 + part * (SM::kRingKeys / 2) + k * 8, v + k * 128, idesc_o,
+                                                i > i0 || part > 0 || k > 0);
+                                mma_commit(&sm.empty[slot]);
+                                if (part + 1 == SM::kPieces) mma_commit(&sm.o_full[0]);
+                            }
+                            __syncwarp();
+                        }
+                        ++np[0];
+                    }
+                } else {
+                    for (int i = i0 - 1; i < i1 && !dead; ++i) {
+                        // the ring holds K0 V0 K1 V1 ..: tile i's values, then tile i + 1's keys
+                        const int sv = got + 2 * (i - i0) + 1, sk = got + 2 * (i - i0) + 2;
+                        if (i >= i0) wait(&sm.full[sv % NS], (sv / NS) & 1);
+                        tc_fence_after();
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+                            const uint32_t tS = tm + a * 128, tO = tm + 256 + a * 128;
+                            const bool now = i >= i0 && t.sub[a].active(i), next = i + 1 < i1 && t.sub[a].active(i + 1);
+                            auto scores = [&] {  // of tile i + 1
+                                wait(&sm.full[sk % NS], (sk / NS) & 1);
+                                if (dead) return;
+                                tc_fence_after();
+                                if (elect_one()) {
+                                    const uint64_t q = dq + (uint64_t)(a * (NP * kPanel >> 4)), k = dk + (uint64_t)((sk % NS) * (SM::kRingBytes >> 4));
+#pragma unroll
+                                    for (int s = 0; s < NP * 4; ++s)
+                                        if (s < steps) {
+                                            const uint64_t at = (s >> 2) * (kPanel >> 4) + (s & 3) * 2;
+                                            mma_bf16(tS, q + at, k + at, idesc_s, s > 0);
+                                        }
+                                    mma_commit(&sm.s_full[a]);
+                                }
+                                __syncwarp();
+                            };
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                if (now) {
+                                    wait(&sm.p_full[a][part], np[a] & 1);
+                                    if (dead) break;
+                                    tc_fence_after();
+                                    if (elect_one()) {
+                                        const uint64_t v = dv + (uint64_t)((sv % NS) * (SM::kRingBytes >> 4));
+#pragma unroll
+                                        for (int k = part * 4; k < part * 4 + 4; ++k)
+                                            mma_bf16_ta(tO, tS + k * 8, v + k * 128, idesc_o, done[a] > 0 || k > 0);
+                                        if (part > 0) mma_commit(&sm.o_full[a]);
+                                    }
+                                    __syncwarp();
+                                }
+                                if (next && part == 1) scores();
+                                if (dead) break;
+                            }
+                            if (dead) break;
+                            if (now) {
+                                ++np[a];
+                                ++done[a];
+                            }
                         }
                         if (dead) break;
-                        if (now) {
-                            ++np[a];
-                            ++done[a];
+                        if (elect_one()) {
+                            if (i >= i0) mma_commit(&sm.empty[sv % NS]);
+                            if (i + 1 < i1) mma_commit(&sm.empty[sk % NS]);
+                            if (i + 2 == i1) mma_commit(&sm.q_empty);
                         }
+                        __syncwarp();
                     }
-                    if (dead) break;
-                    if (elect_one()) {
-                        if (i >= i0) mma_commit(&sm.empty[sv % NS]);
-                        if (i + 1 < i1) mma_commit(&sm.empty[sk % NS]);
-                        if (i + 2 == i1) mma_commit(&sm.q_empty);
-                    }
-                    __syncwarp();
+                    got += 2 * (i1 - i0);
                 }
-                got += 2 * (i1 - i0);
             }
-        }
-        // no product may be under way when the tensor memory is freed
-        if (elect_one()) mma_commit(&sm.drain);
-        __syncwarp();
-        mbar_wait(&sm.drain, 0, kWaitNs);
+            // no product may be under way when the tensor memory is freed
+            if (elect_one()) mma_commit(&sm.drain);
+            __syncwarp();
+            mbar_wait(&sm.drain, round & 1, kWaitNs);
+        } while (another_round());
     } else if (warp == kWatchWarp) {
         fewer_registers();
-        watch_until(&sm.watch, [&] { return mbar_try_wait(&sm.finished, 0); });
+        for (int r = 0; r < 3; ++r) {
+            const bool over = watch_until(&sm.watch, [&] { return mbar_try_wait(&sm.finished, r & 1); });
+            if (!over || !(volatile uint32_t &)sm.redo_any) break;
+        }
     } else if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax
         more_registers();
@@ -745,190 +813,202 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok_w0 = __shfl_sync(0xffffffffu, tok_r, 0), tok_w1 = __shfl_sync(0xffffffffu, tok_r, 31);
         const bool wide = ((uintptr_t)p.out & 31) == 0;
         int ns = 0;  // tiles of scores
-        Item x;
-        while (take(x)) {
-            const int first = x.tok0 + a * tokens, have = min(tokens, x.n - first);
-            if (a >= subs || have <= 0) continue;
-            const int list_s1 = x.t.s1, list_step = x.t.w0 - list_s1;  // of the list of tiles
-            const auto sub = a == 0 ? x.t.sub[0] : x.t.sub[1];
-            const int todo = sub.count(x.i0, x.i1), token = first + tok_r;
-            const bool mine = tok_r < have;  // also false for rows past the last whole token
-            const int pos = mine ? x.off + token : -1;
-            // positions of the warp's first and last row that counts
-            const int wp0 = x.off + first + tok_w0, wp1 = x.off + first + min(have - 1, tok_w1);
-            float m = kNegInf, ref = 0.f;  // the reference (log2) and what is subtracted
-            float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            int done = 0;
-            for (int i = x.i0; done < todo && !dead; ++i) {
-                if (!sub.active(i)) continue;
-                const int j0 = (i < list_s1 ? i : i + list_step) * kKeys;
-                const uint32_t tS = tm + (kWide ? ns & 1 : a) * 128 + lanes;
-                if (kWide) wait(&sm.s_full[ns & 1], (ns >> 1) & 1);
-                else wait(&sm.s_full[a], ns & 1);
-                ++ns;
-                if (dead) break;
-                tc_fence_after();
-                // The row's maximum over both halves; the second one is read again for its
-                // weights, so that registers hold half a row besides what is in flight.
-                const bool partly = j0 + kKeys - 1 > wp0 || (p.window > 0 && j0 <= wp1 - p.window && j0 + kKeys > p.sinks);
-                const int hi = pos - j0, lo = p.window > 0 && pos >= 0 ? pos - p.window - j0 : -1, sinks = p.sinks - j0;
-                auto mask = [&](uint32_t (&s)[64], int c0) {  // of columns c0 .., those the row does not see
+        do {
+            Item x;
+            while (take(x)) {
+                const int first = x.tok0 + a * tokens, have = min(tokens, x.n - first);
+                if (a >= subs || have <= 0) continue;
+                const int list_s1 = x.t.s1, list_step = x.t.w0 - list_s1;  // of the list of tiles
+                const auto sub = a == 0 ? x.t.sub[0] : x.t.sub[1];
+                const int todo = sub.count(x.i0, x.i1), token = first + tok_r;
+                const bool mine = tok_r < have;  // also false for rows past the last whole token
+                const int pos = mine ? x.off + token : -1;
+                // positions of the warp's first and last row that counts
+                const int wp0 = x.off + first + tok_w0, wp1 = x.off + first + min(have - 1, tok_w1);
+                float m = kNegInf, ref = 0.f;  // the reference (log2) and what is subtracted
+                float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                int done = 0;
+                for (int i = x.i0; done < todo && !dead; ++i) {
+                    if (!sub.active(i)) continue;
+                    const int j0 = (i < list_s1 ? i : i + list_step) * kKeys;
+                    const uint32_t tS = tm + (kWide ? ns & 1 : a) * 128 + lanes;
+                    if (kWide) wait(&sm.s_full[ns & 1], (ns >> 1) & 1);
+                    else wait(&sm.s_full[a], ns & 1);
+                    ++ns;
+                    if (dead) break;
+                    tc_fence_after();
+                    // The row's maximum over both halves; the second one is read again for its
+                    // weights, so that registers hold half a row besides what is in flight.
+                    const bool partly = j0 + kKeys - 1 > wp0 || (p.window > 0 && j0 <= wp1 - p.window && j0 + kKeys > p.sinks);
+                    const int hi = pos - j0, lo = p.window > 0 && pos >= 0 ? pos - p.window - j0 : -1, sinks = p.sinks - j0;
+                    auto mask = [&](uint32_t (&s)[64], int c0) {  // of columns c0 .., those the row does not see
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        const int d = c0 + c;
-                        const uint32_t seen = bits_below(hi + 1 - d) & (~bits_below(lo + 1 - d) | bits_below(sinks - d));
+                        for (int c = 0; c < 64; c += 32) {
+                            const int d = c0 + c;
+                            const uint32_t seen = bits_below(hi + 1 - d) & (~bits_below(lo + 1 - d) | bits_below(sinks - d));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(seen >> e & 1)) s[c + e] = 0xff800000u;
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1)) s[c + e] = 0xff800000u;
+                        }
+                    };
+                    // four chains: two warps a scheduler hide little of an instruction's latency
+                    float tops[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+                    auto maxima = [&](const uint32_t (&s)[64]) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+                    };
+                    uint32_t s[64];
+                    {
+                        uint32_t s2[64];
+                        tmem_ld<64>(tS + 64, s2);
+                        tmem_wait_ld();
+                        tmem_ld<64>(tS, s);
+                        if (partly) {
+                            mask(s2, 64);
+#pragma unroll
+                            for (int c = 0; c < 64; c += 16) tmem_st16(tS + 64 + c, s2 + c);  // for the second reading
+                        }
+                        maxima(s2);
                     }
-                };
-                // four chains: two warps a scheduler hide little of an instruction's latency
-                float tops[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-                auto maxima = [&](const uint32_t (&s)[64]) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
-                };
-                uint32_t s[64];
-                {
-                    uint32_t s2[64];
-                    tmem_ld<64>(tS + 64, s2);
                     tmem_wait_ld();
-                    tmem_ld<64>(tS, s);
                     if (partly) {
-                        mask(s2, 64);
-#pragma unroll
-                        for (int c = 0; c < 64; c += 16) tmem_st16(tS + 64 + c, s2 + c);  // for the second reading
+                        mask(s, 0);
+                        tmem_wait_st();
                     }
-                    maxima(s2);
-                }
-                tmem_wait_ld();
-                if (partly) {
-                    mask(s, 0);
-                    tmem_wait_st();
-                }
-                maxima(s);
-                const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
-                const bool moves = top > m + kRefStep;  // also from -inf
-                if (__any_sync(0xffffffffu, moves)) {
-                    const float alpha = moves && m > kNegInf ? ex2_approx(m - top) : 1.f;
-                    if (moves) m = ref = top;
+                    maxima(s);
+                    const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
+                    const bool moves = top > m + kRefStep;  // also from -inf
+                    if (__any_sync(0xffffffffu, moves)) {
+                        const float alpha = moves && m > kNegInf ? ex2_approx(m - top) : 1.f;
+                        if (moves) m = ref = top;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) l[e] = make_float2(l[e].x * alpha, l[e].y * alpha);
-                    if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        if (kWide) {  // S was ready before the last tile's products
-                            wait(&sm.o_full[0], ns & 1);
-                            tc_fence_after();
-                        }
-                        for (int c = 0; c < p.D; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + c, o);
-                            tmem_wait_ld();
+                        for (int e = 0; e < 2; ++e) l[e] = make_float2(l[e].x * alpha, l[e].y * alpha);
+                        if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                            if (kWide) {  // S was ready before the last tile's products
+                                wait(&sm.o_full[0], ns & 1);
+                                tc_fence_after();
+                            }
+                            for (int c = 0; c < p.D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + c, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st16(tO + c, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(tO + c, o);
+                            }
                         }
                     }
-                }
-                const float2 nref = make_float2(-ref, -ref);
-                auto weights = [&](const uint32_t *s, uint32_t at) {  // of 32 columns, into tensor memory
-                    uint32_t w[16];
+                    const float2 nref = make_float2(-ref, -ref);
+                    auto weights = [&](const uint32_t *s, uint32_t at) {  // of 32 columns, into tensor memory
+                        uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float2 y = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, nref);
-                        y.x = ex2_approx(y.x);
-                        y.y = ex2_approx(y.y);
-                        l[e / 2 & 1] = fadd2(l[e / 2 & 1], y);
-                        w[e / 2] = pack_bf16x2(y.x, y.y);
-                    }
-                    tmem_st16(at, w);
-                };
-                auto let_go = [&](int part) {  // of a half's weights, to the products
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_full[kWide ? (ns - 1) & 1 : a][part]);
-                };
-                uint32_t s2[64];
-                weights(s, tS);
-                tmem_ld<64>(tS + 64, s2);
-                weights(s + 32, tS + 16);
-                let_go(0);
-                tmem_wait_ld();
-                weights(s2, tS + 32);
-                weights(s2 + 32, tS + 48);
-                // wide: the next S may be there before this tile's products are, and a barrier's
-                // parity tells a phase only where the one before is known to be over
-                if (kWide && ns > 1) wait(&sm.o_full[0], ns & 1);
-                let_go(1);
-                ++done;
-            }
-            if (todo > 0) {
-                wait(&sm.o_full[a], (ns - 1) & 1);
-                tc_fence_after();
-            }
-            if (dead) break;
-            const float sum = (l[0].x + l[0].y) + (l[1].x + l[1].y);
-            const int64_t row = (int64_t)(x.row0 + token) * p.Hq + x.h * p.group + head_r;
-            const bool whole = p.parts == 1;
-            const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-            const int64_t slot = (int64_t)x.part * p.n_q * p.Hq + row;  // of a part's result
-            uint16_t *dst = (uint16_t *)p.out + row * p.D;
-            float *part_o = whole ? nullptr : p.part_o + slot * p.D;
-            float odd4[4] = {0.f, 0.f, 0.f, 0.f};  // stay 0 while everything is finite
-#pragma unroll 1
-            for (int c0 = 0; c0 < p.D; c0 += 64) {
-                if (!whole && todo == 0) break;
-                uint32_t o[64];
-                if (todo > 0) {
-                    tmem_ld<64>(tO + c0, o);  // columns past D are not used
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 y = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, nref);
+                            y.x = ex2_approx(y.x);
+                            y.y = ex2_approx(y.y);
+                            l[e / 2 & 1] = fadd2(l[e / 2 & 1], y);
+                            w[e / 2] = pack_bf16x2(y.x, y.y);
+                        }
+                        tmem_st16(at, w);
+                    };
+                    auto let_go = [&](int part) {  // of a half's weights, to the products
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.p_full[kWide ? (ns - 1) & 1 : a][part]);
+                    };
+                    uint32_t s2[64];
+                    weights(s, tS);
+                    tmem_ld<64>(tS + 64, s2);
+                    weights(s + 32, tS + 16);
+                    let_go(0);
                     tmem_wait_ld();
+                    weights(s2, tS + 32);
+                    weights(s2 + 32, tS + 48);
+                    // wide: the next S may be there before this tile's products are, and a barrier's
+                    // parity tells a phase only where the one before is known to be over
+                    if (kWide && ns > 1) wait(&sm.o_full[0], ns & 1);
+                    let_go(1);
+                    ++done;
                 }
-#pragma unroll
-                for (int c = 0; c < 64; c += 16) {
-                    if (c0 + c >= p.D) break;
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float f = todo > 0 ? __uint_as_float(o[c + e]) * inv : 0.f, g = todo > 0 ? __uint_as_float(o[c + e + 1]) * inv : 0.f;
-                        odd4[e & 2] = fmaf(f, 0.f, odd4[e & 2]);
-                        odd4[(e & 2) + 1] = fmaf(g, 0.f, odd4[(e & 2) + 1]);
-                        w[e / 2] = pack_bf16x2(f, g);
+                if (todo > 0) {
+                    wait(&sm.o_full[a], (ns - 1) & 1);
+                    tc_fence_after();
+                }
+                if (dead) break;
+                const float sum = (l[0].x + l[0].y) + (l[1].x + l[1].y);
+                const int64_t row = (int64_t)(x.row0 + token) * p.Hq + x.h * p.group + head_r;
+                const bool whole = p.parts == 1;
+                const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                const int64_t slot = (int64_t)x.part * p.n_q * p.Hq + row;  // of a part's result
+                uint16_t *dst = (uint16_t *)p.out + row * p.D;
+                float *part_o = whole ? nullptr : p.part_o + slot * p.D;
+                float odd4[4] = {0.f, 0.f, 0.f, 0.f};  // stay 0 while everything is finite
+#pragma unroll 1
+                for (int c0 = 0; c0 < p.D; c0 += 64) {
+                    if (!whole && todo == 0) break;
+                    uint32_t o[64];
+                    if (todo > 0) {
+                        tmem_ld<64>(tO + c0, o);  // columns past D are not used
+                        tmem_wait_ld();
                     }
-                    if (!mine) continue;
-                    if (!whole) {
-                        store_v8(part_o + c0 + c, o + c);
-                        store_v8(part_o + c0 + c + 8, o + c + 8);
-                    } else if (wide) {
-                        store_v8(dst + c0 + c, w);
-                    } else {
-                        *(uint4 *)(dst + c0 + c) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *(uint4 *)(dst + c0 + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 16) {
+                        if (c0 + c >= p.D) break;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float f = todo > 0 ? __uint_as_float(o[c + e]) * inv : 0.f, g = todo > 0 ? __uint_as_float(o[c + e + 1]) * inv : 0.f;
+                            odd4[e & 2] = fmaf(f, 0.f, odd4[e & 2]);
+                            odd4[(e & 2) + 1] = fmaf(g, 0.f, odd4[(e & 2) + 1]);
+                            w[e / 2] = pack_bf16x2(f, g);
+                        }
+                        if (!mine) continue;
+                        if (!whole) {
+                            store_v8(part_o + c0 + c, o + c);
+                            store_v8(part_o + c0 + c + 8, o + c + 8);
+                        } else if (wide) {
+                            store_v8(dst + c0 + c, w);
+                        } else {
+                            *(uint4 *)(dst + c0 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *(uint4 *)(dst + c0 + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 }
+                const float odd = (odd4[0] + odd4[1]) + (odd4[2] + odd4[3]);
+                if (mine && !whole) {
+                    p.part_ml[slot] = make_float2(ref, sum);
+                    if (x.part == 0)  // the places that this request has no part for
+                        for (int k = x.parts; k < p.parts; ++k) p.part_ml[(int64_t)k * p.n_q * p.Hq + row] = make_float2(kNegInf, 0.f);
+                }
+                if (mine && whole && p.lse) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
+                tc_fence_before();
+                if (__builtin_expect(__any_sync(0xffffffffu, odd != 0.f && mine && todo > 0), 0)) {
+                    if (lane == 0 && round == 0) {
+                        const uint32_t at = (uint32_t)(told - 1) % kMarks;
+                        atomicOr(&sm.redo[at / 32], 1u << (at % 32));
+                        (volatile uint32_t &)sm.redo_any = 1;
+                    }
+                    __syncwarp();
+                }
             }
-            const float odd = (odd4[0] + odd4[1]) + (odd4[2] + odd4[3]);
-            if (mine && !whole) {
-                p.part_ml[slot] = make_float2(ref, sum);
-                if (x.part == 0)  // the places that this request has no part for
-                    for (int k = x.parts; k < p.parts; ++k) p.part_ml[(int64_t)k * p.n_q * p.Hq + row] = make_float2(kNegInf, 0.f);
+        } while (another_round() && round < 2);
+        if (round == 2) {
+            Item x;
+            while (take(x)) {
+                if (a >= subs) continue;
+                const int first = x.tok0 + a * tokens, token = first + tok_r;
+                const int pos = tok_r < min(tokens, x.n - first) ? x.off + token : -1;
+                const int64_t row = (int64_t)(x.row0 + token) * p.Hq + x.h * p.group + head_r;
+                const Tiles::Sub sub = a == 0 ? x.t.sub[0] : x.t.sub[1];
+                put_back(p, x, tokens, sub, pos, lane, row);
+                if (lane == 0) ((volatile Watch *)&sm.watch)->pieces = -told;  // for the watching warp
             }
-            if (mine && whole && p.lse) p.lse[row] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.6931471805599453f;
-            tc_fence_before();
-            uint32_t again = __ballot_sync(0xffffffffu, odd != 0.f && mine && todo > 0);
-            while (again) {
-                const int w = __ffs(again) - 1;
-                again &= again - 1;
-                __syncwarp();
-                repair_row(p, x, sub, __shfl_sync(0xffffffffu, token, w), x.h * p.group + __shfl_sync(0xffffffffu, head_r, w),
-                           __shfl_sync(0xffffffffu, ref, w), __shfl_sync(0xffffffffu, inv, w), lane);
-            }
+            another_round();
         }
     }
-    tc_fence_before();
-    if (warp != kWatchWarp && lane == 0) mbar_arrive(&sm.finished);
-    __syncthreads();
     if (warp == kMmaWarp) tmem_free(tm, 512);
     if (sm.watch.failed)
         for (int b = tid; b < p.B; b += kThreads) p.status[b] = SPEC_STATUS_INTERNAL;

@@ -519,8 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid < kMarks / 32) sm.redo[tid] = 0;
     if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 512);
     tc_fence_before();
-    // statuses: a CTA that fails corrects them seconds later, when all have written theirs
-    write_prompt_statuses(p, blockIdx.x * kThreads + tid, gridDim.x * kThreads);
+    // Statuses: the first CTA's alone, at its start.  One that fails overwrites them seconds after its
+    // own start, which is not before the first one's; a late one of the others writes none.
+    if (blockIdx.x == 0) write_prompt_statuses(p, tid, kThreads);
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sm.tmem;  // S of the two row tiles (or its two buffers) at 0 and 128, O from 256

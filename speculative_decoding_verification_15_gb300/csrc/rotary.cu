@@ -48,6 +48,11 @@ __device__ __forceinline__ uint64_t turns_a_position(double freq) {
     else if (shift >= 0) f = shift == 0 ? m * lo : m * lo >> shift | w1 << (64 - shift);
     return bits >> 63 ? 0 - f : f;
 }
+// The scale of a pair's turn: NaN where the frequency is not a number, infinite, or 2^64 and more
+// (there those 128 bits no longer hold the angle at every position).
+__device__ __forceinline__ float scale_at(double freq, float scale) {
+    return fabs(freq) < 18446744073709551616.0 ? scale : __int_as_float(0x7fffffff);
+}
 
 // cos and sin of pair i at the token's positions, times the scale.
 __device__ __forceinline__ float2 turn_of(const RotaryParams &p, int64_t token, int i) {
@@ -56,7 +61,8 @@ __device__ __forceinline__ float2 turn_of(const RotaryParams &p, int64_t token, 
     const int phase = (int)(((uint64_t)(int64_t)pos * turns_a_position(p.freq[i])) >> 32);
     float s, c;
     sincospif((float)phase * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
-    return make_float2(c * p.scale, s * p.scale);
+    const float scale = scale_at(p.freq[i], p.scale);
+    return make_float2(c * scale, s * scale);
 }
 
 // 8 columns of a unit: one 16-byte word of bf16, or two of fp32 that lie `words` columns apart,
@@ -271,12 +277,14 @@ __global__ void __launch_bounds__(512) rotary_stream_kernel(RotaryParams p, int 
     // the lane's pairs, 32 apart
     constexpr int kPairsEach = kMaxPairs / 32;
     uint64_t F[kPairsEach];
+    float scale[kPairsEach];
     int place_k[kPairsEach];
     const int32_t *row[kPairsEach];
 #pragma unroll
     for (int i = 0; i < kPairsEach; ++i) {
         const int k = lane + 32 * i;
         F[i] = k < p.pairs ? turns_a_position(p.freq[k]) : 0;
+        scale[i] = k < p.pairs ? scale_at(p.freq[k], p.scale) : 0.f;
         place_k[i] = k < p.pairs ? place_of<T, ADJ>(k, p.pairs, turning) : 0;
         row[i] = p.position + (k < p.pairs && p.axis ? min(max(p.axis[k], 0), p.axes - 1) : 0) * p.ld_pos;
     }
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(512) rotary_stream_kernel(RotaryParams p, int 
             const int phase = (int)(((uint64_t)(int64_t)row[i][token] * F[i]) >> 32);
             float s, c;
             sincospif((float)phase * 4.656612873077393e-10f, &s, &c);
-            ((float2 *)turns[warp])[place_k[i]] = make_float2(c * p.scale, s * p.scale);
+            ((float2 *)turns[warp])[place_k[i]] = make_float2(c * scale[i], s * scale[i]);
         }
         __syncwarp();
         if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");

@@ -523,7 +523,8 @@ int spec_kv_plan(int32_t *free_pages, int32_t *free_count, int num_pages, int pa
  *  q, k         rows of num_query_heads (num_heads) * head_dim elements of type dtype, ld
  *               elements apart; num_heads 0: no keys.  out_q, out_k likewise; each may be its
  *               input (in place), but must not overlap it otherwise.
- *  position     [num_axes] rows of n_tokens, ld_position apart (unused for one axis)
+ *  position     [num_axes] rows of n_tokens, ld_position apart (unused for one axis; 0: the same
+ *               row for every axis)
  *  freq         [pairs] double, of a magnitude below 2^64 (a pair whose frequency is larger,
  *               infinite or NaN becomes NaN); axis [pairs] int32 in [0, num_axes) (others
  *               count as the nearest), NULL for one axis

@@ -401,10 +401,11 @@ def rotary(q, k, position, freq, axis=None, adjacent: bool = False, scale: float
            stream=None) -> dict:
     """Rotate queries q and keys k (or None) [tokens, heads, head_dim] by their positions:
     position int32 [tokens], or [axes, tokens] with the axis of each pair (see
-    rotary_frequencies).  A pair is columns (i, i + pairs), or (2 i, 2 i + 1) if adjacent;
-    columns past the pairs are copied; scale multiplies what is rotated.  out_q and out_k may
-    be q and k themselves (slices of a fused projection's output, for instance).  Returns q
-    and k."""
+    rotary_frequencies); a prompt of text, with one position for every axis, may expand it.
+    A pair is columns (i, i + pairs), or (2 i, 2 i + 1) if adjacent; columns past the pairs
+    are copied; scale multiplies what is rotated.  A pair whose frequency is infinite or NaN
+    becomes NaN.  out_q and out_k may be q and k themselves (slices of a fused projection's
+    output, for instance).  Returns q and k."""
     dev = q.device
     if out_q is None:
         out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
@@ -415,8 +416,11 @@ def rotary(q, k, position, freq, axis=None, adjacent: bool = False, scale: float
 
 
 def _i32_rows(t, device):
-    """int32 with contiguous rows on the device; as it is where it already is that."""
-    if t.dtype is _I32 and t.device == device and (t.stride(-1) == 1 or t.shape[-1] <= 1):
+    """int32 on the device, with contiguous rows that are one and the same or do not overlap;
+    as it is where it already is that."""
+    n, strides = t.shape[-1], t.stride()
+    apart = len(strides) != 2 or strides[0] == 0 or strides[0] >= n
+    if t.dtype is _I32 and t.device == device and (strides[-1] == 1 or n <= 1) and apart:
         return t
     return _as_i32(t, device)
 

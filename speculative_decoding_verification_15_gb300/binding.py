@@ -716,8 +716,8 @@ def spec_rotary(q, k, position, freq, axis, adjacent: bool, scale: float, out_q,
             or (n > 1 and strides[-1] != 1)):
         raise ValueError(f"position must be int32 [{n}] or [axes, {n}] with contiguous rows on q's device")
     axes, ldp = (shape[0], strides[0]) if len(shape) == 2 else (1, 0)
-    if axes < 1 or (axes > 1 and ldp < n):
-        raise ValueError("position must have one row or more that do not overlap")
+    if axes < 1 or (axes > 1 and ldp != 0 and ldp < n):
+        raise ValueError("position must have one row or more, the same one or rows that do not overlap")
     pairs = freq.numel()
     if axes > 1 and axis is None:
         raise ValueError("positions of several axes need the axis of each pair")

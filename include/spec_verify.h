@@ -516,7 +516,7 @@ int spec_kv_plan(int32_t *free_pages, int32_t *free_count, int num_pages, int pa
  *   a = position[axis[i], token] * freq[i]   radians,
  *   (x, y) -> scale * (x cos a - y sin a, y cos a + x sin a),
  * (x, y) being columns (i, i + pairs), or (2 i, 2 i + 1) if adjacent; columns 2 * pairs ..
- * are copied.  Angles keep their bits at every position that an int32 holds (off by 2^-25
+ * are copied.  Angles keep their bits at every position that an int32 holds (off by 2^-27
  * turns at most, for the value of freq that its 53 bits hold); sines and cosines are in 32
  * bits.
  *

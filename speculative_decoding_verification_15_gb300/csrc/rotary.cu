@@ -5,7 +5,7 @@
 // The angle matters modulo a turn only, so it is kept in turns as a 64-bit fixed-point
 // fraction: F_i = (freq_i / 2 pi) 2^64 modulo 2^64, and position * F_i in wrapping integer
 // arithmetic is the phase, off by |position| 2^-64 turns (2^-33 at the farthest position).
-// Its highest 32 bits, a signed number of half turns, go through sincospi in 32 bits.  A
+// Its highest 32 bits, less the nearest quarter turn, go through sincospi in 32 bits.  A
 // product in fp32 would be off by 2^-24 of an angle of up to 2^31 radians.
 //
 // Bound by memory: queries and keys are read and written once.  A CTA takes kTokens tokens;
@@ -54,15 +54,25 @@ __device__ __forceinline__ float scale_at(double freq, float scale) {
     return fabs(freq) < 18446744073709551616.0 ? scale : __int_as_float(0x7fffffff);
 }
 
+// cos and sin, times the scale, of a phase of 2^-32 turns.  The nearest quarter turn is taken off
+// as an integer: what becomes a float is an eighth of a turn at most and loses 2^-28 turns (half a
+// turn would lose 2^-26).
+__device__ __forceinline__ float2 turn(uint32_t phase, float scale) {
+    const uint32_t quarter = phase + 0x20000000u;  // its number in the two highest bits
+    const int rest = (int)(phase - (quarter & 0xc0000000u));
+    float s, c;
+    sincospif((float)rest * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
+    const bool odd = quarter & 0x40000000u;
+    const uint32_t x = __float_as_uint(odd ? s : c) ^ ((quarter ^ quarter << 1) & 0x80000000u);
+    const uint32_t y = __float_as_uint(odd ? c : s) ^ (quarter & 0x80000000u);
+    return make_float2(__uint_as_float(x) * scale, __uint_as_float(y) * scale);
+}
+
 // cos and sin of pair i at the token's positions, times the scale.
 __device__ __forceinline__ float2 turn_of(const RotaryParams &p, int64_t token, int i) {
     const int a = p.axis ? min(max(p.axis[i], 0), p.axes - 1) : 0;
     const int pos = p.position[a * p.ld_pos + token];
-    const int phase = (int)(((uint64_t)(int64_t)pos * turns_a_position(p.freq[i])) >> 32);
-    float s, c;
-    sincospif((float)phase * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
-    const float scale = scale_at(p.freq[i], p.scale);
-    return make_float2(c * scale, s * scale);
+    return turn((uint32_t)(((uint64_t)(int64_t)pos * turns_a_position(p.freq[i])) >> 32), scale_at(p.freq[i], p.scale));
 }
 
 // 8 columns of a unit: one 16-byte word of bf16, or two of fp32 that lie `words` columns apart,
@@ -300,10 +310,7 @@ __global__ void __launch_bounds__(512) rotary_stream_kernel(RotaryParams p, int 
         for (int i = 0; i < kPairsEach; ++i) {
             const int k = lane + 32 * i;
             if (k >= p.pairs) break;
-            const int phase = (int)(((uint64_t)(int64_t)row[i][token] * F[i]) >> 32);
-            float s, c;
-            sincospif((float)phase * 4.656612873077393e-10f, &s, &c);
-            ((float2 *)turns[warp])[place_k[i]] = make_float2(c * scale[i], s * scale[i]);
+            ((float2 *)turns[warp])[place_k[i]] = turn((uint32_t)(((uint64_t)(int64_t)row[i][token] * F[i]) >> 32), scale[i]);
         }
         __syncwarp();
         if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");

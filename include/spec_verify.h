@@ -503,6 +503,7 @@ int spec_cache_attention(const spec_kv_cache *cache, const void *q, int dtype, i
  *               a negative new_len counts as 0 rows); SPEC_STATUS_NO_PAGES (requests are
  *               served in order: from the first whose pages the list cannot supply, none that
  *               lacks pages gets any).  A failed request keeps its table and held.
+ * None of the arrays may overlap another (only keep_len and new_len may be one).
  * B * ld_table must stay below 2^31.  One kernel or two, no workspace; it may be captured.  Calls
  * on one pool must follow one another in stream order.
  */

@@ -75,6 +75,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 int kv_device_info(int *dev, int *sms);             // verify.cu: the current device and its SM count
 int kv_check_device_pointer(const void *p, int dev);  // verify.cu: p lies on dev, or is managed memory
 
+inline bool overlap(const void *a, size_t bytes_a, const void *b, size_t bytes_b) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x && y && bytes_a && bytes_b && x < y + bytes_b && y < x + bytes_a;
+}
+
 // What every entry point asks of a cache description.
 inline int check_cache(const spec_kv_cache *c) {
     if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return SPEC_EINVAL;

@@ -275,6 +275,17 @@ extern "C" int spec_kv_plan(int32_t *free_pages, int32_t *free_count, int num_pa
          (uintptr_t)new_len | (uintptr_t)out_cu | (uintptr_t)out_seq_len | (uintptr_t)out_position | (uintptr_t)out_status) & 3)
         return SPEC_EINVAL;
     if ((uintptr_t)out_slot & 7) return SPEC_EINVAL;
+    // What is written must overlap nothing else: threads still read the lengths when others write.
+    const size_t rows = 4 * (size_t)B;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } used[] = {{free_pages, 4 * (size_t)num_pages}, {free_count, 4}, {page_table, rows * ld_table}, {held, rows},
+                {out_cu, rows + 4}, {out_seq_len, rows}, {out_slot, 8 * (size_t)n_out}, {out_position, 4 * (size_t)n_out},
+                {out_status, rows}, {keep_len, rows}, {new_len, rows}};
+    for (int i = 0; i < 9; ++i)
+        for (int j = i + 1; j < 11; ++j)
+            if (overlap(used[i].p, used[i].bytes, used[j].p, used[j].bytes)) return SPEC_EINVAL;
     int dev = 0, sms = 0, rc;
     if ((rc = kv_device_info(&dev, &sms))) return rc;
     if ((rc = kv_check_device_pointer(free_pages, dev))) return rc;

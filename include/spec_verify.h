@@ -554,7 +554,8 @@ int spec_rotary(const void *q, const void *k, int dtype, int64_t ld_q, int64_t l
  *  head_dim     a multiple of 16, at most SPEC_KV_MAX_HEAD_DIM
  *  n_query, n_key  rows of q, out, out_lse and of k, v; max_query a bound on every n_b
  *  scale        positive and finite; window >= 0; sinks >= 0 (unused when window == 0)
- *  out          [n_query, num_query_heads, head_dim] of type dtype, 16-byte aligned
+ *  out          [n_query, num_query_heads, head_dim] of type dtype, 16-byte aligned; must not
+ *               overlap q, k or v
  *  out_lse      [n_query, num_query_heads] float, or NULL
  *  out_status   [B]: 0, SPEC_STATUS_BAD_LENGTH (nothing of the request is written) or
  *               SPEC_STATUS_INTERNAL for every request (rows are unspecified)

@@ -355,6 +355,12 @@ extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v
     if (((uintptr_t)cu_query | (uintptr_t)cu_key | (uintptr_t)out_status) & 3) return SPEC_EINVAL;
     const size_t need = spec_prompt_attention_workspace_size(n_query, n_key, B, num_query_heads, num_heads, head_dim, dtype, window, sinks);
     if (need > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 255))) return SPEC_EWORKSPACE;
+    // items read queries, keys and values after others have written
+    const size_t out_bytes = (size_t)n_query * num_query_heads * head_dim * esz;
+    auto rows_bytes = [&](int n, int64_t ld, int64_t columns) { return n > 0 ? ((size_t)(n - 1) * ld + columns) * esz : 0; };
+    if (overlap(out, out_bytes, q, rows_bytes(n_query, ld_q, row * group)) || overlap(out, out_bytes, k, rows_bytes(n_key, ld_k, row)) ||
+        overlap(out, out_bytes, v, rows_bytes(n_key, ld_v, row)))
+        return SPEC_EINVAL;
     int dev = 0, sms = 0, rc;
     if ((rc = kv_device_info(&dev, &sms))) return rc;
     if (n_query > 0 && (rc = kv_check_device_pointer(q, dev))) return rc;

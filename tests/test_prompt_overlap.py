@@ -47,3 +47,28 @@ def test_plan_arrays_that_overlap(lib):
                 assert plan(lib, **{one: a[other] + SIZES[other] - 4})[0] == EINVAL, (one, other)
             assert plan(lib, **{other: a[one] + SIZES[one] - (8 if other == "slot" else 4)})[0] == EINVAL, (one, other)
     assert plan(lib, seq=a["keep"])[0] == EINVAL  # a length advanced in place
+
+
+@pytest.mark.parametrize("esz,code", [(2, 0), (4, 1)])
+def test_prompt_output_over_its_inputs(lib, esz, code):
+    """out may not lie on q, k or v (which may be slices of one product); next to them it may."""
+    n, m, Hq, H, D = 6, 9, 4, 2, 16
+    ld = (Hq + 2 * H) * D
+
+    def call(out, k=None):
+        q = 1 << 20
+        k = q + Hq * D * esz if k is None else k
+        p = [ctypes.c_void_p(x) for x in (q, k, k + H * D * esz)]
+        other = ctypes.c_void_p(1 << 30)
+        return lib.spec_prompt_attention(*p, code, ld, ld, ld, Hq, H, D, n, m, 1, other, n, other, 0.25, 0, 0, ctypes.c_void_p(out), None,
+                                         other, None, 0, None)
+
+    q = 1 << 20
+    apart = 1 << 24
+    q_end, k_end = q + ((n - 1) * ld + Hq * D) * esz, apart + ((m - 1) * ld + H * D) * esz
+    v_end = k_end + H * D * esz
+    size = n * Hq * D * esz
+    for out in (q, q - size + 16, q_end - 16, apart, k_end - 16, v_end - 16, apart - size + 16):
+        assert call(out, apart) == EINVAL, hex(out)
+    for out in (q - size, (q_end + 15) // 16 * 16, (v_end + 15) // 16 * 16, apart - size):
+        assert call(out, apart) != EINVAL, hex(out)

@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(PlanParams p, int ctas) {
         const int b = last_at_most(taken, p.B, j);
         p.table[(int64_t)b * p.width + p.held[b] + (j - taken[b])] = id;
     };
-    for (int k = first; k < moved; k += step) {
-        const int b = last_at_most(given, p.B, k);
+    for (int64_t j = first; j < moved; j += step) {
+        const int k = (int)j, b = last_at_most(given, p.B, k);
         const int need = (int)(((int64_t)p.keep[b] + p.fresh[b] + p.page_size - 1) >> p.shift);
         int32_t *entry = p.table + (int64_t)b * p.width + need + (k - given[b]);
         const int id = *entry;
@@ -317,6 +317,6 @@ extern "C" int spec_kv_plan(int32_t *free_pages, int32_t *free_count, int num_pa
     rc = launch<1024>(p, B <= 1024 ? 4 : 8, smem, dev, st);
     if (rc || !p.rows_apart) return rc;
     constexpr int each = kRowsThreads * kRowsEach;
-    page_rows_kernel<<<(n_out + each - 1) / each, kRowsThreads, 0, st>>>(p);
+    page_rows_kernel<<<(unsigned)(((int64_t)n_out + each - 1) / each), kRowsThreads, 0, st>>>(p);
     return launch_status();
 }

@@ -441,7 +441,7 @@ extern "C" int spec_rotary(const void *q, const void *k, int dtype, int64_t ld_q
     p.adjacent = adjacent != 0;
     p.scale = scale;
     const cudaStream_t st = (cudaStream_t)cuda_stream;
-    const int blocks = (n_tokens + kTokens - 1) / kTokens, heads = num_query_heads + num_heads;
+    const int blocks = (int)(((int64_t)n_tokens + kTokens - 1) / kTokens), heads = num_query_heads + num_heads;
     bool vec = !((pairs & 7) | ((head_dim - 2 * pairs) & 7));
     for (int w = 0; w < (num_heads ? 2 : 1); ++w)
         vec = vec && !(((uintptr_t)p.src[w] | (uintptr_t)p.dst[w]) & 15) && !(((p.ld_src[w] | p.ld_dst[w]) * esz) & 15);
@@ -455,9 +455,9 @@ extern "C" int spec_rotary(const void *q, const void *k, int dtype, int64_t ld_q
     // memory (9000 tokens of 72 heads: 61 us in halves, 76 whole; 16411 of 40: 57 and 61), three
     // where that leaves 16 warps.
     int shares = 1;
-    while (shares < 4 && stream_slot(heads, units, shares, esz) * 2 * 16 > kStreamSmem) shares *= 2;
+    while (shares < 4 && (int64_t)stream_slot(heads, units, shares, esz) * 2 * 16 > kStreamSmem) shares *= 2;
     const int slot = stream_slot(heads, units, shares, esz);
-    if (slot * 2 * 4 <= kStreamSmem && n_tokens >= 16 * sms) {
+    if ((int64_t)slot * 2 * 4 <= kStreamSmem && n_tokens >= 16 * sms) {
         const int stages = slot * 3 * 16 <= kStreamSmem ? 3 : 2;
         const int fit = kStreamSmem / (slot * stages), warps = fit < 16 ? fit : 16;
         if (esz == 2 && adjacent) return launch_stream<uint16_t, true>(p, sms, dev, stages, shares, warps, slot, st);

@@ -1,0 +1,49 @@
+"""Counts of tokens, rows and pages near what an int32 holds."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+MOST = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import speculative_decoding_verification_15_gb300 as pkg
+
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 60 GB")
+    yield pkg
+    torch.cuda.empty_cache()
+
+
+def test_rotary_of_two_billion_tokens(pkg):
+    q = torch.ones((MOST, 1, 2), dtype=torch.bfloat16, device="cuda")
+    position = torch.zeros(MOST, dtype=I32, device="cuda")
+    at = torch.tensor([0, 1, MOST // 2, MOST - 3, MOST - 1], device="cuda")
+    position[at] = 1
+    freq = torch.full((1,), 3.141592653589793 / 2, dtype=torch.float64, device="cuda")
+    pkg.rotary(q, None, position, freq, out_q=q)
+    assert torch.equal(q[at].float().round(), torch.tensor([[[-1.0, 1.0]]], device="cuda").expand(5, 1, 2))
+    q[at] = 1.0
+    assert bool((q == 1).all())
+
+
+def test_plan_of_two_billion_rows(pkg):
+    """Most of them behind the last token, as a padded batch has them."""
+    pool = pkg.kv_pool(9)
+    table, held = torch.full((2, 4), -1, dtype=I32, device="cuda"), torch.zeros(2, dtype=I32, device="cuda")
+    got = pkg.kv_plan(pool, table, held, held.clone(), torch.tensor([20, 30], device="cuda"), 16, MOST)
+    assert got["status"].tolist() == [0, 0] and held.tolist() == [2, 2] and int(pool.count) == 5
+    assert got["position"][:50].tolist() == [*range(20), *range(30)] and bool((got["position"][50:] == -1).all())
+    assert (got["slot"][:50] >= 0).all() and bool((got["slot"][50:] == -1).all())
+
+
+def test_two_billion_pages_go_back(pkg):
+    pages = MOST - 1
+    free, count = torch.full((pages,), -7, dtype=I32, device="cuda"), torch.zeros(1, dtype=I32, device="cuda")
+    table = torch.arange(pages, dtype=I32, device="cuda")[None]
+    held, none = torch.full((1,), pages, dtype=I32, device="cuda"), torch.zeros(1, dtype=I32, device="cuda")
+    got = pkg.kv_plan(pkg.PagePool(free, count), table, held, none, none, 16, 0)
+    assert got["status"].tolist() == [0] and held.tolist() == [0] and count.tolist() == [pages]
+    assert bool((table == -1).all()) and torch.equal(free, torch.arange(pages, dtype=I32, device="cuda"))

@@ -384,8 +384,8 @@ extern "C" int spec_prompt_attention(const void *q, const void *k, const void *v
     p.H = num_heads;
     p.group = group;
     p.D = head_dim;
-    p.window = window < (1 << 30) ? window : (1 << 30);  // positions stay below 2^31
-    p.sinks = window > 0 ? sinks : 0;
+    p.window = window < n_key ? window : 0;  // one that is no shorter than the keys hides none
+    p.sinks = p.window > 0 ? sinks : 0;
     p.scale_log2 = scale * kLog2e;
     p.parts = 1;
     if (need > 0) {

@@ -41,7 +41,6 @@ inline PromptPlan prompt_plan(int n_q, int n_k, int B, int group, int H, int D, 
     // average (a part costs its rows' sums in fp32, written and read).  The kernel, which knows
     // the lengths, cuts each request into as many parts as its length asks for, up to x.parts.
     int64_t keys = (int64_t)n_k / B - n_q / B / 2;
-    window = window < (1 << 30) ? window : (1 << 30);  // as the kernels see it
     if (window > 0 && keys > (int64_t)window + sinks) keys = (int64_t)window + sinks;
     const int64_t most = keys / 128 / kLeastTiles;
     if (x.items < kSms && B <= 128 && most > 1) {
@@ -104,7 +103,6 @@ inline int rows_parts(int n_q, int n_k, int B, int group, int H, int window, int
     constexpr int kSms = 152, kMostParts = 32, kLeastTiles = 3;
     const int64_t items = ((int64_t)n_q * group / 64 + B) * H;
     int64_t keys = (int64_t)n_k / B - n_q / B / 2;
-    window = window < (1 << 30) ? window : (1 << 30);
     if (window > 0 && keys > (int64_t)window + sinks) keys = (int64_t)window + sinks;
     const int64_t most = keys / 64 / kLeastTiles, want = (4 * kSms + items - 1) / items;
     if (items >= 2 * kSms || most < 2 || want < 2) return 1;

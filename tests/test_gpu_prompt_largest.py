@@ -47,3 +47,20 @@ def test_two_billion_pages_go_back(pkg):
     got = pkg.kv_plan(pkg.PagePool(free, count), table, held, none, none, 16, 0)
     assert got["status"].tolist() == [0] and held.tolist() == [0] and count.tolist() == [pages]
     assert bool((table == -1).all()) and torch.equal(free, torch.arange(pages, dtype=I32, device="cuda"))
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30 + 3000, 2 ** 30 + 5000])
+def test_windows_of_a_billion_keys(pkg, window):
+    """One query over 2^30 + 5000 keys, of which the first 6000 have all the weight."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 70 GB")
+    m, D = 2 ** 30 + 5000, 16
+    k = torch.full((m, 1, D), -30.0, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros((m, 1, D), dtype=torch.bfloat16, device="cuda")
+    k[:6000] = 0.0
+    v[:2000], v[2000:6000] = 1.0, 4.0  # 3 on average
+    q = torch.ones((1, 1, D), dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([[0, 1], [0, m]], dtype=I32, device="cuda")
+    got = pkg.prompt_attention(q, k, v, cu[0], 1, cu_key=cu[1], window=window)
+    want = 4.0 if m - window >= 2000 else 3.0  # 2000 keys, or none, are too far back
+    assert got["status"].tolist() == [0] and (got["out"] == want).all()

@@ -499,7 +499,7 @@ int spec_cache_attention(const spec_kv_cache *cache, const void *q, int dtype, i
  *  out_slot     [n_out] page * page_size + position % page_size, where the token goes; -1
  *               for a failed request's tokens.  Rows behind the last token hold -1 in both.
  *  out_status   [B]: 0; SPEC_STATUS_BAD_LENGTH (a negative length, more tokens than ld_table
- *               pages hold, more kept than held, held outside [0, ld_table], rows past n_out;
+ *               pages or an int32 hold, more kept than held, held outside [0, ld_table], rows past n_out;
  *               a negative new_len counts as 0 rows); SPEC_STATUS_NO_PAGES (requests are
  *               served in order: from the first whose pages the list cannot supply, none that
  *               lacks pages gets any).  A failed request keeps its table and held.

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(PlanParams p, int ctas) {
     const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
 
     // ---- sums over the requests
-    const int64_t room = (int64_t)p.width << p.shift;
+    const int64_t room = min((int64_t)p.width << p.shift, (int64_t)0x7fffffff);  // a length is an int32
     int64_t rows = 0, none = 0, all_rows, unused;
     for (int b = b0; b < b1; ++b) rows += max(0, p.fresh[b]);
     int64_t at = rows;

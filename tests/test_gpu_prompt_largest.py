@@ -64,3 +64,21 @@ def test_windows_of_a_billion_keys(pkg, window):
     got = pkg.prompt_attention(q, k, v, cu[0], 1, cu_key=cu[1], window=window)
     want = 4.0 if m - window >= 2000 else 3.0  # 2000 keys, or none, are too far back
     assert got["status"].tolist() == [0] and (got["out"] == want).all()
+
+
+def test_lengths_past_an_int32(pkg):
+    """A request's length must fit; up to that a plan is right, in its last page too."""
+    pages, page = 2 ** 24, 128
+    pool = pkg.PagePool(torch.arange(pages, 2 * pages, dtype=I32, device="cuda"), torch.full((1,), pages, dtype=I32, device="cuda"))
+    table = torch.full((2, pages + 9), -1, dtype=I32, device="cuda")
+    table[0, :pages] = torch.arange(pages, dtype=I32, device="cuda")
+    held = torch.tensor([pages, 0], dtype=I32, device="cuda")
+    keep = torch.tensor([MOST - 3, 0], dtype=I32, device="cuda")
+    for new, status in ((3, 0), (4, 2), (MOST, 2)):
+        got = pkg.kv_plan(pool, table, held, keep, torch.tensor([new, 0], device="cuda"), page, min(new, 10))
+        assert got["status"].tolist() == [status, 2 if new > 10 else 0]  # the second one's row would be past n_out
+        assert got["seq_len"].tolist() == [MOST if status == 0 else MOST - 3, 0]
+        assert held.tolist() == [pages, 0] and int(pool.count) == pages
+        if status == 0:
+            assert got["position"].tolist() == [MOST - 3, MOST - 2, MOST - 1]
+            assert got["slot"].tolist() == [MOST - 3, MOST - 2, MOST - 1]  # page i is the table's i-th

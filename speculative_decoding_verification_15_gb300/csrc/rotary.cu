@@ -411,7 +411,7 @@ extern "C" int spec_rotary(const void *q, const void *k, int dtype, int64_t ld_q
     if (n_tokens == 0) return SPEC_OK;
     const int esz = dtype == SPEC_BF16 ? 2 : 4;
     const int64_t row_q = (int64_t)num_query_heads * head_dim, row_k = (int64_t)num_heads * head_dim;
-    if (!q || !out_q || !position || (pairs > 0 && !freq) || (num_axes > 1 && !axis)) return SPEC_EINVAL;
+    if (!q || !out_q || !position || (pairs > 0 && (!freq || (num_axes > 1 && !axis)))) return SPEC_EINVAL;
     if (num_heads > 0 && (!k || !out_k || ld_k < row_k || ld_out_k < row_k)) return SPEC_EINVAL;
     if (ld_q < row_q || ld_out_q < row_q || (num_axes > 1 && ld_position < n_tokens && ld_position != 0)) return SPEC_EINVAL;
     if (((uintptr_t)q | (uintptr_t)out_q | (num_heads ? (uintptr_t)k | (uintptr_t)out_k : 0)) % esz) return SPEC_EINVAL;

@@ -28,3 +28,12 @@ def test_expanded_positions(pkg, T, kind):
     long = torch.arange(2 * T + 8, device="cuda").to(kind)
     slid = torch.as_strided(long, (3, T), (1, 1))
     assert torch.equal(pkg.rotary(q, None, slid, freq, axis)["q"], pkg.rotary(q, None, slid.contiguous(), freq, axis)["q"])
+
+
+@pytest.mark.parametrize("T", [3, 3000])
+def test_no_pairs_and_several_axes(pkg, T):
+    """Nothing rotates: what comes in is copied."""
+    q, k, pos = inputs(10, T, 3, 1, 32, BF16, 2, 99)
+    freq, axis = pkg.rotary_frequencies(0, sections=(0, 0))
+    got = pkg.rotary(q, k, torch.from_numpy(pos).cuda(), freq, axis)
+    assert torch.equal(got["q"], q) and torch.equal(got["k"], k)

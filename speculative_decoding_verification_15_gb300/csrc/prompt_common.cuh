@@ -33,7 +33,7 @@ inline PromptPlan prompt_plan(int n_q, int n_k, int B, int group, int H, int D, 
     x.tokens = 128 / group;
     x.parts = 1;
     // pairs of row tiles (heads of up to 128 columns), which keep the tensor cores busier;
-    // single ones where there is an SM for each (203 tokens of 32 heads: 11.1 us, in pairs 11.9)
+    // single ones where there is an SM for each (203 tokens of 32 heads: 11.4 us, in pairs 12.8)
     const int64_t pairs = (((int64_t)n_q + 2 * x.tokens - 1) / (2 * x.tokens) + B) * H;
     x.subs = D > 128 || 2 * pairs <= kSms ? 1 : 2;
     x.items = (((int64_t)n_q + x.subs * x.tokens - 1) / (x.subs * x.tokens) + B) * H;

@@ -23,9 +23,10 @@
 // without a counter.  Where the host sees fewer items than SMs over many keys, items are cut
 // along the keys into parts of equal length, whose sums prompt_join_kernel joins in order.
 //
-// Bound by the chain scores, maximum, exponentials, weights of two warps a scheduler (1710
-// TFLOP/s on one prompt of 16384 tokens with 16 heads of 128 columns, 960 on 8 prompts of 4500
-// with 16 heads of 64), and with short items by their starts and ends (some 3 us a pair of row tiles).
+// Bound by the chain scores, maximum, exponentials, weights of two warps a scheduler (1720
+// TFLOP/s on one prompt of 16384 tokens with 16 heads of 128 columns, 990 on 8 prompts of 4500
+// with 16 heads of 64 that share 4 key heads), and with short items by their starts and ends (some
+// 3 us a pair of row tiles); long calls by power (clocks of 1.7 to 1.8 GHz).
 //
 // What a row does not see has weight 0, but 0 times a NaN or an infinity is NaN.  A CTA marks its
 // items with a row that is not finite, and does them again when all are done, with care: what is

@@ -8,10 +8,12 @@
 // Its highest 32 bits, less the nearest quarter turn, go through sincospi in 32 bits.  A
 // product in fp32 would be off by 2^-24 of an angle of up to 2^31 radians.
 //
-// Bound by memory: queries and keys are read and written once.  A CTA takes kTokens tokens;
-// their sines and cosines are computed once each, into shared memory, while the first loads
-// are under way; a thread keeps those of its 8 pairs in registers for all its heads.  CTAs
-// are short and many: the next ones' loads overlap the last ones' stores.
+// Bound by memory: queries and keys are read and written once.  Few tokens: short CTAs of kTokens
+// tokens, whose sines and cosines are computed once each, into shared memory, while the first loads
+// are under way; a thread keeps those of its 8 pairs in registers for all its heads (8 tokens of 40
+// heads: 2.8 us).  From 16 tokens an SM on: warps that stay and copy their next tokens, or shares
+// of them, asynchronously (16411 tokens of 40 heads: 57 us, 5.9 TB/s).  Sizes and addresses that
+// 16-byte words do not fit go pair by pair.
 #include <atomic>
 
 #include "kv_common.cuh"

@@ -12,7 +12,9 @@
 // rarely rescaled.
 //
 // P's rounding to bf16 (2^-8 of each weight at most) is of the size of the output's own; it
-// lets both products run at the bf16 rate.  Everything else is fp32.
+// lets both products run at the bf16 rate.  Everything else is fp32.  P in two terms takes half as
+// many products again: 24 packed prompts 599 -> 860 us, one of 24571 tokens 1476 -> 2158, for outputs
+// that are off by 0.0016 (relative 2-norm) instead of 0.0021.
 //
 // Roles: 8 warps of softmax (4 a row tile), one that issues products, one that copies
 // (tensor maps: queries {D, group, heads, tokens}, keys and values {D, heads, tokens}, in

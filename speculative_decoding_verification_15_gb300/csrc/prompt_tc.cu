@@ -58,14 +58,17 @@ constexpr int kWorking = kThreads - 32;  // all but the watching warp
 constexpr int kSortedBatch = 128; // requests whose items are put in order of length
 constexpr float kRefStep = 8.f;   // log2: how far a score may exceed the reference
 
-// What a CTA's waits go by: whether it has failed, and the pieces of tiles copied so far.
+// What a CTA's waits go by: whether it has failed, and the pieces of tiles copied and the items told
+// so far.
 struct Watch {
-    int failed, pieces;
+    int failed;
+    uint32_t pieces, items;
 };
 
 // Polls: these waits are on the path of every tile, so they look at no clock.  One warp watches over
-// the others: two seconds without a copy, and all waits end.  (A wait may last a whole item, and
-// an item of 200 million keys takes longer than that.)
+// the others: two seconds without a copy or a new item, and all waits end.  (A wait may last a whole
+// item, and an item of 200 million keys takes longer than that; millions of items without keys copy
+// nothing.)
 __device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
@@ -84,12 +87,12 @@ __device__ __forceinline__ bool poll_barrier(uint32_t bar, uint32_t parity, vola
 template <typename F>
 __device__ __forceinline__ bool watch_until(volatile Watch *watch, F done) {
     uint64_t t0 = 0;
-    int pieces = 0;
+    uint32_t before = 0;
     while (!done()) {
         const uint64_t now = global_ns();
-        const int seen = watch->pieces;
-        if (t0 == 0 || seen != pieces) t0 = now;
-        pieces = seen;
+        const uint32_t seen = watch->pieces + watch->items;  // neither falls
+        if (t0 == 0 || seen != before) t0 = now;
+        before = seen;
         if (watch->failed || now - t0 > kWaitNs) {
             watch->failed = 1;
             return false;
@@ -516,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.raw, 1);
         sm.redo_any = 0;
         sm.watch.failed = 0;
-        sm.watch.pieces = 0;
+        sm.watch.pieces = sm.watch.items = 0;
         mbar_init_fence();
     }
     if (tid < kMarks / 32) sm.redo[tid] = 0;
@@ -602,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (told >= kItems) wait(&sm.item_empty[at], (told / kItems - 1) & 1);
                 if (dead) break;
                 if (lane == 0) {
+                    ((volatile Watch *)&sm.watch)->items = told + 1;
                     sm.items[at] = x;
                     mbar_arrive(&sm.item_full[at]);
                 }
@@ -1008,7 +1012,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t row = (int64_t)(x.row0 + token) * p.Hq + x.h * p.group + head_r;
                 const Tiles::Sub sub = a == 0 ? x.t.sub[0] : x.t.sub[1];
                 put_back(p, x, tokens, sub, pos, lane, row);
-                if (lane == 0) ((volatile Watch *)&sm.watch)->pieces = -told;  // for the watching warp
             }
             another_round();
         }
